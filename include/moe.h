@@ -564,6 +564,119 @@ moe_status_t moe_ipc_handle(const void *ptr, void *handle, size_t *offset);
 moe_status_t moe_ipc_open(const void *handle, int device, void **base);
 moe_status_t moe_ipc_close(void *base);
 
+/*
+ * Products of the experts' bf16 weights with ragged groups of rows, and their
+ * gradients: the expert layer's two products for weights that are not
+ * quantised, forward and backward.  offsets i32 [E + 1] (device) gives the
+ * groups: rows offsets[e] .. offsets[e+1]-1 of the row operands belong to
+ * expert e (the `offset` array of moe_read_routing has this form); groups may
+ * be empty, and rows before offsets[0] or from offsets[E] on belong to none.
+ *   moe_grouped_matmul              y[r, n]     = sum_k x[r, k] w[e, n, k]
+ *   moe_grouped_matmul_grad_input   dx[r, k]    = sum_n dy[r, n] w[e, n, k]
+ *   moe_grouped_matmul_grad_weight  dw[e, n, k] = sum_{r of e} dy[r, n] x[r, k]
+ * All operands and results are bf16, sums fp32, one rounding at the end.
+ * x [R, K], dy [R, N], w and dw [E, N, K], row-major and contiguous, 16-byte
+ * aligned; offsets 4-byte aligned; workspace 256-byte aligned, ws_bytes >=
+ * moe_grouped_workspace_bytes (else MOE_ERR_WORKSPACE_TOO_SMALL; it needs no
+ * initialisation and holds the error word only, so calls that may overlap on
+ * the GPU may share it if their status is not read).  Outputs must not overlap
+ * inputs.  Rows of no expert: with zero_unused != 0 their outputs are set to
+ * zero, else they are left as they were; the weight gradient does not read
+ * them.  An expert without rows gets a zero dw.  A row's result does not
+ * depend on other rows, whatever they hold (infinities and NaN included).
+ * Offsets that decrease or leave [0, R] are read as the running maximum of
+ * their values clamped to [0, R] and reported by
+ * moe_check_device_error(workspace) as MOE_ERR_BAD_ROUTING; no memory outside
+ * the operands is touched.  R = 0 enqueues nothing (the weight gradient: zeros
+ * dw and the error word).  N and K must be multiples of 8 and at most 131072,
+ * E at most 1024 (else MOE_ERR_UNSUPPORTED_SHAPE).  One kernel per call.
+ */
+moe_status_t moe_grouped_workspace_bytes(size_t *bytes);
+moe_status_t moe_grouped_matmul(const void *x_bf16, const void *w_bf16, const int32_t *offsets, void *y_bf16, int R,
+                                int E, int N, int K, int zero_unused, void *workspace, size_t ws_bytes,
+                                moe_stream_t stream);
+moe_status_t moe_grouped_matmul_grad_input(const void *dy_bf16, const void *w_bf16, const int32_t *offsets,
+                                           void *dx_bf16, int R, int E, int N, int K, int zero_unused,
+                                           void *workspace, size_t ws_bytes, moe_stream_t stream);
+moe_status_t moe_grouped_matmul_grad_weight(const void *dy_bf16, const void *x_bf16, const int32_t *offsets,
+                                            void *dw_bf16, int R, int E, int N, int K, void *workspace,
+                                            size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * Products of a few bf16 token vectors with a weight matrix in 4 bits, for the
+ * dense projections beside the experts at decode:
+ *   y[t, n] = sum_k x[t, k] * scale(w_sf[n, k / G]) * e2m1(w_fp4[n, k])
+ * with the weights as moe_quantize_fp4 (MOE_FP4_MX: UE8M0 scales, G = 32) or
+ * moe_quantize_nvfp4 (MOE_FP4_NVFP4: UE4M3 scales, G = 16) writes them:
+ * w_fp4 u8 [N, K/2] (16-byte aligned), w_sf u8 [N, K/G]; x bf16 [T, K]
+ * (16-byte aligned), y bf16 [T, N].  x is not quantised; sums are fp32 (x times
+ * a power of two enters them as fp16: an element is exact down to 2^-31 of its
+ * token's largest one in an eighth of K, and off by at most 2^-40 of it
+ * below).  Scale bytes 255 (UE8M0) and 0x7F (UE4M3; bit 7 is not read) are NaN.
+ * The weights are read once per 8 tokens (fewer for K above 7168).  K must be
+ * a multiple of 32 and at most 57344, T at most 65535, else
+ * MOE_ERR_UNSUPPORTED_SHAPE.  T = 0 enqueues nothing.  One kernel per call.
+ */
+#define MOE_FP4_MX 0
+#define MOE_FP4_NVFP4 1
+moe_status_t moe_fp4_matvec(const void *x_bf16, const void *w_fp4, const void *w_sf, void *y_bf16, int T, int N, int K,
+                            int format, moe_stream_t stream);
+
+/*
+ * The norms before and after the expert layer's block, and their gradients.
+ * Per token, over its H columns, with fp32 sums:
+ *   rstd = (mean(x^2) + eps)^(-1/2)
+ *
+ * moe_norm_before -- y = x * rstd * weight, written as bf16 (y_bf16 [T, H])
+ *   and/or as the layer's quantised input (y_fp8 u8 [T, H], y_sf u8 [T, H/32]:
+ *   bit for bit what moe_quantize_fp8 makes of y_bf16); either may be NULL,
+ *   not both; y_fp8 and y_sf go together and need H % 32 == 0.  rstd f32 [T]
+ *   is written if not NULL (the gradient needs it).
+ *
+ * moe_norm_after -- out = residual_scale * residual + gate * (x * rstd *
+ *   weight), one rounding to bf16.  gate_bf16 by gate_kind: MOE_GATE_NONE (not
+ *   read), MOE_GATE_CHANNEL [H], MOE_GATE_TOKEN [T] or MOE_GATE_FULL [T, H].
+ *   out may be the same memory as residual or x.
+ *
+ * moe_norm_before_backward -- with dy the gradient of y: dx = rstd * (dy *
+ *   weight - xhat * mean(dy * weight * xhat)) + dresidual, xhat = x * rstd
+ *   (dresidual bf16 [T, H], the gradient that reaches x past the norm, or
+ *   NULL), and dweight f32 [H] = sum_t dy * xhat.  dx may be the same memory as
+ *   dy or dresidual.
+ *
+ * moe_norm_after_backward -- with dout the gradient of out: dresidual =
+ *   residual_scale * dout; dx as above with gate * dout in place of dy;
+ *   dweight f32 [H]; and dgate: f32 [H] (channel), f32 [T] (token) or bf16
+ *   [T, H] (full); not written without a gate.  The outputs must not overlap
+ *   each other or the gate; dx or dresidual may be the same memory as dout.
+ *
+ * x, dy, residual, weight ... are bf16, contiguous and 16-byte aligned (a
+ * per-token gate 2-byte); float arrays 4-byte.  The gradients take a workspace
+ * (256-byte aligned, moe_norm_workspace_bytes(T, H); no initialisation) for the
+ * column sums of their blocks, which a second kernel adds in a fixed order:
+ * results do not depend on timing.  H must be a multiple of 8 and at most
+ * 16384 (else MOE_ERR_UNSUPPORTED_SHAPE); eps must be positive and finite.
+ * T = 0 enqueues nothing (the gradients: zeros dweight and a per-channel
+ * dgate).
+ */
+#define MOE_GATE_NONE 0
+#define MOE_GATE_CHANNEL 1
+#define MOE_GATE_TOKEN 2
+#define MOE_GATE_FULL 3
+moe_status_t moe_norm_before(const void *x_bf16, const void *weight_bf16, int T, int H, float eps, void *y_bf16,
+                             void *y_fp8, void *y_sf, float *rstd, moe_stream_t stream);
+moe_status_t moe_norm_after(const void *x_bf16, const void *residual_bf16, const void *weight_bf16,
+                            const void *gate_bf16, int gate_kind, int T, int H, float eps, float residual_scale,
+                            void *out_bf16, float *rstd, moe_stream_t stream);
+moe_status_t moe_norm_workspace_bytes(int T_max, int H, size_t *bytes);
+moe_status_t moe_norm_before_backward(const void *dy_bf16, const void *x_bf16, const void *weight_bf16,
+                                      const float *rstd, const void *dresidual_bf16, int T, int H, void *dx_bf16,
+                                      float *dweight, void *workspace, size_t ws_bytes, moe_stream_t stream);
+moe_status_t moe_norm_after_backward(const void *dout_bf16, const void *x_bf16, const void *weight_bf16,
+                                     const float *rstd, const void *gate_bf16, int gate_kind, int T, int H,
+                                     float residual_scale, void *dx_bf16, void *dresidual_bf16, float *dweight,
+                                     void *dgate, void *workspace, size_t ws_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

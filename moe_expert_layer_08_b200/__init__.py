@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -24,6 +25,9 @@ __all__ = [
     "forward_nvfp4", "shared_workspace_bytes", "shared_workspace", "shared_forward", "probe_wait_timeout",
     "ep_workspace_bytes", "ep_dispatch", "ep_combine", "ep_combine_peers", "ep_route", "ep_dispatch_peers",
     "ipc_handle", "ipc_open", "ipc_close", "IPC_HANDLE_BYTES",
+    "grouped_workspace_bytes", "grouped_matmul", "grouped_matmul_grad_input", "grouped_matmul_grad_weight",
+    "fp4_matvec", "norm_workspace_bytes", "norm_before", "norm_after", "norm_before_backward",
+    "norm_after_backward", "NormBefore", "NormAfter",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_b200.so")
@@ -120,6 +124,16 @@ def _declare(lib):
         "moe_ipc_handle": (I32, [P, P, c.POINTER(SZ)]),
         "moe_ipc_open": (I32, [P, I32, c.POINTER(P)]),
         "moe_ipc_close": (I32, [P]),
+        "moe_grouped_workspace_bytes": (I32, [c.POINTER(SZ)]),
+        "moe_grouped_matmul": (I32, [P, P, P, P, I32, I32, I32, I32, I32, P, SZ, P]),
+        "moe_grouped_matmul_grad_input": (I32, [P, P, P, P, I32, I32, I32, I32, I32, P, SZ, P]),
+        "moe_grouped_matmul_grad_weight": (I32, [P, P, P, P, I32, I32, I32, I32, P, SZ, P]),
+        "moe_fp4_matvec": (I32, [P, P, P, P, I32, I32, I32, I32, P]),
+        "moe_norm_before": (I32, [P, P, I32, I32, c.c_float, P, P, P, P, P]),
+        "moe_norm_after": (I32, [P, P, P, P, I32, I32, I32, c.c_float, c.c_float, P, P, P]),
+        "moe_norm_workspace_bytes": (I32, [I32, I32, c.POINTER(SZ)]),
+        "moe_norm_before_backward": (I32, [P, P, P, P, P, I32, I32, P, P, P, SZ, P]),
+        "moe_norm_after_backward": (I32, [P, P, P, P, P, I32, I32, I32, c.c_float, P, P, P, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -698,3 +712,259 @@ def ipc_open(handle: bytes, device: int) -> int:
 def ipc_close(base: int) -> None:
     """Unmaps a base returned by ipc_open (moe_ipc_close)."""
     _check(load().moe_ipc_close(ctypes.c_void_p(base)), "moe_ipc_close")
+
+
+# ------------------------------------------------------------ around the expert layer
+def _need_on(t, dtype, name, shape, device):
+    _need(t, dtype, name)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _stream_on(stream, device):
+    """The given stream, or the current one of ``device``."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"stream must be on {device}, got {stream.device}")
+    return ctypes.c_void_p(stream.cuda_stream)
+
+
+def grouped_workspace_bytes() -> int:
+    """Device workspace bytes of the grouped products (host-only)."""
+    n = ctypes.c_size_t()
+    _check(load().moe_grouped_workspace_bytes(ctypes.byref(n)), "moe_grouped_workspace_bytes")
+    return n.value
+
+
+def _grouped_workspace(workspace, device):
+    if workspace is None:
+        return torch.empty(grouped_workspace_bytes(), dtype=torch.uint8, device=device)
+    _need(workspace, torch.uint8, "workspace")
+    if workspace.device != device:
+        raise ValueError(f"workspace must be on {device}, got {workspace.device}")
+    return workspace
+
+
+def _grouped_rows(fn, rows, w, offsets, out, workspace, stream, width_in, width_out):
+    E, N, K = w.shape
+    R = rows.shape[0]
+    dev = rows.device
+    _need_on(w, torch.bfloat16, "w", w.shape, dev)
+    _need_on(offsets, torch.int32, "offsets", (E + 1,), dev)
+    if rows.shape[1] != (K, N)[width_in]:
+        raise ValueError(f"rows of {rows.shape[1]} columns do not fit weights {tuple(w.shape)}")
+    shape = (R, (N, K)[width_out])
+    zero_unused = out is None
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _need_on(out, torch.bfloat16, "out", shape, dev)
+    ws = _grouped_workspace(workspace, dev)
+    _check(getattr(load(), fn)(_ptr(rows), _ptr(w), _ptr(offsets), _ptr(out), R, E, N, K, int(zero_unused), _ptr(ws),
+                               ws.numel(), _stream_on(stream, dev)), fn)
+    return out
+
+
+def grouped_matmul(x, w, offsets, out=None, workspace=None, stream=None):
+    """The experts' bf16 products over ragged groups of rows: x [R, K] bf16, w
+    [E, N, K] bf16, offsets [E + 1] i32 on the device (rows offsets[e] ..
+    offsets[e+1]-1 belong to expert e) -> y [R, N] bf16, y[r] = w[e] @ x[r].
+    Rows of no expert are zero in a new output and left as they were in a given
+    ``out``.  ``workspace``: u8, grouped_workspace_bytes(); with one of your own
+    check_device_error(workspace) reports offsets that decrease or leave [0, R]
+    (read as their clamped running maximum)."""
+    _need(x, torch.bfloat16, "x", 2)
+    _need(w, torch.bfloat16, "w", 3)
+    return _grouped_rows("moe_grouped_matmul", x, w, offsets, out, workspace, stream, 0, 0)
+
+
+def grouped_matmul_grad_input(dy, w, offsets, out=None, workspace=None, stream=None):
+    """The gradient of grouped_matmul's rows: dy [R, N] bf16 -> dx [R, K] bf16,
+    dx[r] = w[e].T @ dy[r].  Rows of no expert, ``out`` and ``workspace`` as
+    there."""
+    _need(dy, torch.bfloat16, "dy", 2)
+    _need(w, torch.bfloat16, "w", 3)
+    return _grouped_rows("moe_grouped_matmul_grad_input", dy, w, offsets, out, workspace, stream, 1, 1)
+
+
+def grouped_matmul_grad_weight(dy, x, offsets, out=None, workspace=None, stream=None):
+    """The gradient of grouped_matmul's weights: dy [R, N] and x [R, K] bf16 ->
+    dw [E, N, K] bf16, dw[e] = dy[rows of e].T @ x[rows of e] (zero for an
+    expert without rows).  ``out`` is overwritten; ``workspace`` as for
+    grouped_matmul."""
+    _need(dy, torch.bfloat16, "dy", 2)
+    _need(x, torch.bfloat16, "x", 2)
+    (R, N), K, dev = dy.shape, x.shape[1], dy.device
+    _need_on(x, torch.bfloat16, "x", (R, K), dev)
+    _need(offsets, torch.int32, "offsets", 1)
+    E = offsets.shape[0] - 1
+    if E < 1 or offsets.device != dev:
+        raise ValueError(f"offsets must hold E + 1 >= 2 values on {dev}")
+    if out is None:
+        out = torch.empty((E, N, K), dtype=torch.bfloat16, device=dev)
+    else:
+        _need_on(out, torch.bfloat16, "out", (E, N, K), dev)
+    ws = _grouped_workspace(workspace, dev)
+    _check(load().moe_grouped_matmul_grad_weight(_ptr(dy), _ptr(x), _ptr(offsets), _ptr(out), R, E, N, K, _ptr(ws),
+                                                 ws.numel(), _stream_on(stream, dev)),
+           "moe_grouped_matmul_grad_weight")
+    return out
+
+
+_FP4_FORMATS = {"mx": (0, 32), "nvfp4": (1, 16)}  # MOE_FP4_MX, MOE_FP4_NVFP4; elements per scale
+
+
+def fp4_matvec(x, w, w_sf, fmt: str = "mx", out=None, stream=None):
+    """A few token vectors times a weight matrix in 4 bits: x [T, K] bf16, and
+    (w [N, K/2], w_sf) as quantize_fp4 (``fmt`` "mx") or quantize_nvfp4
+    ("nvfp4") returns them -> y [T, N] bf16.  The activations stay bf16.  For
+    decode: the weights are read once per 8 tokens."""
+    _need(x, torch.bfloat16, "x", 2)
+    _need(w, torch.uint8, "w", 2)
+    if fmt not in _FP4_FORMATS:
+        raise ValueError(f"fmt is 'mx' or 'nvfp4', got {fmt!r}")
+    code, group = _FP4_FORMATS[fmt]
+    (T, K), N, dev = x.shape, w.shape[0], x.device
+    _need_on(w, torch.uint8, "w", (N, K // 2), dev)
+    _need_on(w_sf, torch.uint8, "w_sf", (N, K // group), dev)
+    if out is None:
+        out = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
+    else:
+        _need_on(out, torch.bfloat16, "out", (T, N), dev)
+    _check(load().moe_fp4_matvec(_ptr(x), _ptr(w), _ptr(w_sf), _ptr(out), T, N, K, code, _stream_on(stream, dev)),
+           "moe_fp4_matvec")
+    return out
+
+
+class NormBefore(NamedTuple):
+    """What norm_before wrote; None where it was not asked for."""
+    y: Optional[torch.Tensor]       # bf16 [T, H]
+    x_fp8: Optional[torch.Tensor]   # E4M3 codes u8 [T, H]
+    x_sf: Optional[torch.Tensor]    # UE8M0 u8 [T, H/32]
+    rstd: Optional[torch.Tensor]    # f32 [T]
+
+
+class NormAfter(NamedTuple):
+    """What norm_after wrote; rstd is None where it was not asked for."""
+    out: torch.Tensor               # bf16 [T, H]
+    rstd: Optional[torch.Tensor]    # f32 [T]
+
+
+def norm_before(x, weight, eps: float = 1e-6, bf16: bool = True, fp8: bool = False, rstd: bool = False, stream=None):
+    """The norm before the layer: y = x * rsqrt(mean(x^2) + eps) * weight, x [T,
+    H] and weight [H] bf16.  ``bf16``: return y as bf16 (for the shared expert,
+    a router, unquantised experts); ``fp8``: return the layer's quantised input,
+    what quantize_fp8 makes of y, from the same pass; ``rstd``: return the
+    reciprocal deviations, which norm_before_backward takes.  -> NormBefore."""
+    _need(x, torch.bfloat16, "x", 2)
+    (T, H), dev = x.shape, x.device
+    _need_on(weight, torch.bfloat16, "weight", (H,), dev)
+    if not (bf16 or fp8):
+        raise ValueError("ask for bf16, fp8 or both")
+    y = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if bf16 else None
+    q = torch.empty((T, H), dtype=torch.uint8, device=dev) if fp8 else None
+    sf = torch.empty((T, H // 32), dtype=torch.uint8, device=dev) if fp8 else None
+    r = torch.empty(T, dtype=torch.float32, device=dev) if rstd else None
+    _check(load().moe_norm_before(_ptr(x), _ptr(weight), T, H, eps, _ptr(y), _ptr(q), _ptr(sf), _ptr(r),
+                                  _stream_on(stream, dev)), "moe_norm_before")
+    return NormBefore(y, q, sf, r)
+
+
+def _gate(gate, T, H, dev):
+    """The gate's kind (MOE_GATE_*): None, per channel [H], per token [T, 1] or
+    per element [T, H]."""
+    if gate is None:
+        return 0
+    _need(gate, torch.bfloat16, "gate")
+    if gate.device != dev:
+        raise ValueError(f"gate must be on {dev}, got {gate.device}")
+    for kind, shape in ((1, (H,)), (2, (T, 1)), (3, (T, H))):
+        if gate.shape == shape:
+            return kind
+    raise ValueError(f"gate must be [H], [T, 1] or [T, H], got {tuple(gate.shape)}")
+
+
+def norm_after(x, residual, weight, eps: float = 1e-6, gate=None, residual_scale: float = 1.0, out=None,
+               rstd: bool = False, stream=None):
+    """The norm after the layer, into the residual stream: out = residual_scale
+    * residual + gate * (x * rsqrt(mean(x^2) + eps) * weight), all bf16 with one
+    rounding.  ``gate``: None, per channel [H], per token [T, 1] or per element
+    [T, H].  ``out`` may be ``residual`` itself.  -> NormAfter."""
+    _need(x, torch.bfloat16, "x", 2)
+    (T, H), dev = x.shape, x.device
+    _need_on(residual, torch.bfloat16, "residual", (T, H), dev)
+    _need_on(weight, torch.bfloat16, "weight", (H,), dev)
+    kind = _gate(gate, T, H, dev)
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    else:
+        _need_on(out, torch.bfloat16, "out", (T, H), dev)
+    r = torch.empty(T, dtype=torch.float32, device=dev) if rstd else None
+    _check(load().moe_norm_after(_ptr(x), _ptr(residual), _ptr(weight), _ptr(gate), kind, T, H, eps, residual_scale,
+                                 _ptr(out), _ptr(r), _stream_on(stream, dev)), "moe_norm_after")
+    return NormAfter(out, r)
+
+
+def norm_workspace_bytes(T_max: int, H: int) -> int:
+    """Device workspace bytes of the norms' gradients for up to T_max tokens (host-only)."""
+    n = ctypes.c_size_t()
+    _check(load().moe_norm_workspace_bytes(T_max, H, ctypes.byref(n)), "moe_norm_workspace_bytes")
+    return n.value
+
+
+def _norm_workspace(workspace, T, H, device):
+    if workspace is None:
+        return torch.empty(norm_workspace_bytes(T, H), dtype=torch.uint8, device=device)
+    _need(workspace, torch.uint8, "workspace")
+    if workspace.device != device:
+        raise ValueError(f"workspace must be on {device}, got {workspace.device}")
+    return workspace
+
+
+def norm_before_backward(dy, x, weight, rstd, dresidual=None, workspace=None, stream=None):
+    """The gradients of norm_before for dy [T, H] bf16, with the rstd it
+    returned: (dx [T, H] bf16, dweight [H] f32).  ``dresidual`` (bf16 [T, H]),
+    the gradient that reaches x past the norm, is added to dx.  ``workspace``:
+    u8, norm_workspace_bytes(T, H)."""
+    _need(dy, torch.bfloat16, "dy", 2)
+    (T, H), dev = dy.shape, dy.device
+    _need_on(x, torch.bfloat16, "x", (T, H), dev)
+    _need_on(weight, torch.bfloat16, "weight", (H,), dev)
+    _need_on(rstd, torch.float32, "rstd", (T,), dev)
+    if dresidual is not None:
+        _need_on(dresidual, torch.bfloat16, "dresidual", (T, H), dev)
+    ws = _norm_workspace(workspace, T, H, dev)
+    dx = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    dweight = torch.empty(H, dtype=torch.float32, device=dev)
+    _check(load().moe_norm_before_backward(_ptr(dy), _ptr(x), _ptr(weight), _ptr(rstd), _ptr(dresidual), T, H,
+                                           _ptr(dx), _ptr(dweight), _ptr(ws), ws.numel(), _stream_on(stream, dev)),
+           "moe_norm_before_backward")
+    return dx, dweight
+
+
+def norm_after_backward(dout, x, weight, rstd, gate=None, residual_scale: float = 1.0, workspace=None, stream=None):
+    """The gradients of norm_after for dout [T, H] bf16, with the rstd it
+    returned and its gate: (dx [T, H] bf16, dresidual [T, H] bf16, dweight [H]
+    f32, dgate), dgate None without a gate, f32 [H] (per channel), f32 [T, 1]
+    (per token) or bf16 [T, H] (per element).  ``workspace`` as for
+    norm_before_backward."""
+    _need(dout, torch.bfloat16, "dout", 2)
+    (T, H), dev = dout.shape, dout.device
+    _need_on(x, torch.bfloat16, "x", (T, H), dev)
+    _need_on(weight, torch.bfloat16, "weight", (H,), dev)
+    _need_on(rstd, torch.float32, "rstd", (T,), dev)
+    kind = _gate(gate, T, H, dev)
+    ws = _norm_workspace(workspace, T, H, dev)
+    dx = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    dresidual = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    dweight = torch.empty(H, dtype=torch.float32, device=dev)
+    dgate = None
+    if kind:
+        dgate = torch.empty(gate.shape, dtype=torch.bfloat16 if kind == 3 else torch.float32, device=dev)
+    _check(load().moe_norm_after_backward(_ptr(dout), _ptr(x), _ptr(weight), _ptr(rstd), _ptr(gate), kind, T, H,
+                                          residual_scale, _ptr(dx), _ptr(dresidual), _ptr(dweight), _ptr(dgate),
+                                          _ptr(ws), ws.numel(), _stream_on(stream, dev)), "moe_norm_after_backward")
+    return dx, dresidual, dweight, dgate

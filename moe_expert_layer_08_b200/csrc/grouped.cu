@@ -1,0 +1,620 @@
+// grouped.cu -- products of the experts' bf16 weights with ragged groups of
+// rows, and their two gradients.  Rows offsets[e] .. offsets[e+1]-1 of the row
+// operands belong to expert e:
+//   product          y[r, n]     = sum_k x[r, k] W[e, n, k]
+//   input gradient   dx[r, k]    = sum_n dy[r, n] W[e, n, k]
+//   weight gradient  dW[e, n, k] = sum_{r of e} dy[r, n] x[r, k]
+// bf16 operands, fp32 sums in TMEM (tcgen05.mma.kind::f16), one rounding to
+// bf16 at the end.  In all three a CTA's work item is a 256-column strip of
+// the output features (two 128-row MMA tiles, the M side) times up to kN
+// columns of the N side: rows of one expert (product, input gradient; N is
+// the row count rounded up to 16, so a ragged group costs what it has and not
+// a full tile) or 256 columns of k (weight gradient).  Operands come by TMA
+// straight from the caller's row-major tensors in whichever major order the
+// contraction finds them:
+//                    M side                     N side
+//   product          W rows n, K-major          x rows, K-major
+//   input gradient   W columns k, MN-major      dy rows, K-major
+//   weight gradient  dy columns n, MN-major     x columns k, MN-major
+// Columns past a feature width and rows of W past its expert read as zeros
+// through the tensor maps.  The weight gradient's contraction runs over rows,
+// so the rows of the next group inside its last 16-row step are zeroed in
+// shared memory on both sides (a product with zero alone would let a NaN of
+// the neighbour through).
+#include "moe_common.cuh"
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+enum GroupedMode { kProduct = 0, kGradInput = 1, kGradWeight = 2 };
+
+constexpr int kStrip = 256;    // output features of an item: two 128-row MMA tiles
+constexpr int kBlockK = 64;    // contraction elements of a pipeline stage (one 128-byte swizzled row)
+constexpr int kRowBox = 32;    // rows of one TMA box of a K-major N side
+constexpr int kChunkBlock = 16;  // row chunks that share a strip's weights before the next strip
+constexpr int kThreads = 384;  // warps: 0 loads, 1 and 2 issue, 3 zeroes tails, 4-7 and 8-11 drain tiles 0 and 1
+
+// kN: columns of the N side an item may have. 32 for decode loads (a stage is
+// nearly all weights, six of them in flight), 256 otherwise (64 bytes of
+// operands from L2 per MMA cycle instead of 96 with 128).
+template <int kN>
+struct GroupedCfg {
+    static constexpr int kStages = kN == 32 ? 6 : 3;
+    static constexpr int kABytes = kStrip * kBlockK * 2;  // 32 KB, both tiles
+    static constexpr int kBBytes = kN * kBlockK * 2;
+    static constexpr int kStageBytes = kABytes + kBBytes;
+    static constexpr int kBufs = kN == 32 ? 2 : 1;        // accumulator buffers of a tile
+    static constexpr int kTmemCols = 2 * kBufs * kN;
+    static constexpr int kMisc = 512;
+    static constexpr int kOffsetsBytes = 2 * (kMaxExperts + 1) * 4;
+    static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kMisc + kOffsetsBytes;
+    static_assert(kSmemBytes <= 232448, "shared memory budget");
+    static_assert(kTmemCols >= 32 && kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM allocation");
+};
+
+struct GroupedArgs {
+    const int *offsets;   // [E + 1]
+    __nv_bfloat16 *out;
+    int *hdr;             // workspace header (error word)
+    int R, E;
+    int D;                // output features: N (product, weight gradient's rows) or K (input gradient)
+    int C;                // contraction length of the product and input gradient
+    int K;                // weight gradient: columns of dW
+    int zero_unused;      // product, input gradient: write zeros to the rows of no expert
+};
+
+// Shared-memory matrix descriptor, MN-major, 128-byte swizzle: boxes of 64 MN
+// x 64 contraction elements (a contraction row is 128 bytes), 8-row groups
+// 1024 B apart (SBO), the next 64 MN elements one box further (LBO).
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= uint64_t((saddr >> 4) & 0x3FFFu);
+    d |= uint64_t((64 * 128) >> 4) << 16;   // LBO
+    d |= uint64_t(1024 >> 4) << 32;         // SBO
+    d |= uint64_t(1) << 46;                 // descriptor version (sm_100)
+    d |= uint64_t(2) << 61;                 // SWIZZLE_128B
+    return d;
+}
+
+// One step of a warp's inclusive maximum / sum scans.
+__device__ __forceinline__ int warp_scan_max(int v, int lane) {
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+        if (lane >= d) v = max(v, o);
+    }
+    return v;
+}
+__device__ __forceinline__ int warp_scan_sum(int v, int lane) {
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+        if (lane >= d) v += o;
+    }
+    return v;
+}
+
+// Work item u: expert, first output feature of its strip, and the N side: rows
+// [row0, row0 + cols) or columns [col0, col0 + cols) of dW.
+struct Item {
+    int e, d0, n0, cols;
+    int kblocks;   // stages
+    int tail;      // weight gradient: rows of the last stage (1 .. 64)
+};
+
+// Walks the items of one CTA in ascending order; every role keeps its own.
+template <int kMode, int kN>
+struct Walker {
+    const int *row_of;   // [E + 1] group starts, ascending
+    const int *item_of;  // [E + 1] first item of each expert
+    int E, strips, kb_const, K, D;
+    int e = 0;
+
+    __device__ __forceinline__ Item at(int u) {
+        Item it;
+        if constexpr (kMode == kGradWeight) {
+            const int kt = (K + kN - 1) / kN;
+            const int per = strips * kt;
+            it.e = u / per;
+            const int l = u - it.e * per;
+            it.d0 = (l / kt) * kStrip;
+            it.n0 = (l % kt) * kN;
+            it.cols = min(kN, K - it.n0);
+            const int rows = row_of[it.e + 1] - row_of[it.e];
+            it.kblocks = (rows + kBlockK - 1) / kBlockK;
+            it.tail = rows - (it.kblocks - 1) * kBlockK;
+        } else {
+            while (item_of[e + 1] <= u) ++e;
+            it.e = e;
+            const int l = u - item_of[e];
+            const int r0 = row_of[e], rows = row_of[e + 1] - r0;
+            const int nch = (rows + kN - 1) / kN;
+            // blocks of kChunkBlock row chunks; inside one, strip by strip over its chunks
+            const int b = l / (kChunkBlock * strips);
+            const int rem = l - b * kChunkBlock * strips;
+            const int width = min(kChunkBlock, nch - b * kChunkBlock);
+            const int c = b * kChunkBlock + rem % width;
+            it.d0 = (rem / width) * kStrip;
+            it.n0 = r0 + c * kN;
+            it.cols = min(kN, rows - c * kN);
+            it.kblocks = kb_const;
+            it.tail = kBlockK;
+        }
+        return it;
+    }
+};
+
+template <int kMode, int kN>
+__global__ void __launch_bounds__(kThreads, 1)
+    grouped_kernel(const __grid_constant__ CUtensorMap tmap_m, const __grid_constant__ CUtensorMap tmap_n,
+                   const GroupedArgs args) {
+    using C = GroupedCfg<kN>;
+    constexpr int kStages = C::kStages;
+    constexpr bool kMMn = kMode != kProduct;         // M side MN-major
+    constexpr bool kNMn = kMode == kGradWeight;      // N side MN-major
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *tiles = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(tiles + kStages * C::kStageBytes);
+    uint64_t *empty = full + kStages;
+    uint64_t *fixed = empty + kStages;           // weight gradient: tail rows of the stage zeroed
+    uint64_t *tmem_full = fixed + kStages;       // [tile][buf]
+    uint64_t *tmem_empty = tmem_full + 4;        // [tile][buf]
+    uint64_t *mma_done = tmem_empty + 4;         // [tile]
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(mma_done + 2);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+    int *row_of = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(full) + C::kMisc);
+    int *item_of = row_of + kMaxExperts + 1;
+    static_assert((3 * kStages + 10) * 8 + 8 <= C::kMisc, "barriers and flags");
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], kNMn ? 3 : 2);  // both issuers, and the warp that zeroes tails
+            mbar_init(&fixed[s], 1);
+        }
+        for (int b = 0; b < 4; ++b) {
+            mbar_init(&tmem_full[b], 1);
+            mbar_init(&tmem_empty[b], 4);
+        }
+        mbar_init(&mma_done[0], 1);
+        mbar_init(&mma_done[1], 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tmap(&tmap_m);
+        prefetch_tmap(&tmap_n);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_holder, C::kTmemCols);
+        tmem_relinquish();
+    }
+    const int strips = (args.D + kStrip - 1) / kStrip;
+    pdl_wait();
+    if (warp == 0) {
+        // Group starts: the running maximum of the offsets clamped to [0, R],
+        // so a bad array never leads out of the row operands; and each
+        // expert's first item.
+        int carry_row = 0, carry_item = 0, bad = 0;
+        for (int b = 0; b <= args.E; b += 32) {
+            const int i = b + lane;
+            const int raw = i <= args.E ? __ldg(args.offsets + i) : args.R;
+            const int clamped = min(max(raw, 0), args.R);
+            const int row = max(warp_scan_max(clamped, lane), carry_row);
+            if (i <= args.E) {
+                bad |= row != raw;
+                row_of[i] = row;
+            }
+            carry_row = __shfl_sync(0xFFFFFFFFu, row, 31);
+        }
+        __syncwarp();
+        if constexpr (kMode != kGradWeight) {
+            for (int b = 0; b < args.E; b += 32) {
+                const int i = b + lane;
+                const int n = i < args.E ? (row_of[i + 1] - row_of[i] + kN - 1) / kN * strips : 0;
+                const int incl = warp_scan_sum(n, lane) + carry_item;
+                if (i < args.E) item_of[i + 1] = incl;
+                carry_item = __shfl_sync(0xFFFFFFFFu, incl, 31);
+            }
+            if (lane == 0) item_of[0] = 0;
+        }
+        bad = __any_sync(0xFFFFFFFFu, bad);
+        // the call's error word (timeouts are added two seconds later at the earliest)
+        if (blockIdx.x == 0 && lane == 0) {
+            args.hdr[kHdrTimeoutWhere] = 0;
+            args.hdr[kHdrError] = bad ? kDevErrBadRouting : 0;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (threadIdx.x == 0) pdl_trigger();
+    const uint32_t tmem = *tmem_holder;
+
+    Walker<kMode, kN> walk;
+    walk.row_of = row_of;
+    walk.item_of = item_of;
+    walk.E = args.E;
+    walk.strips = strips;
+    walk.kb_const = (args.C + kBlockK - 1) / kBlockK;
+    walk.K = args.K;
+    walk.D = args.D;
+    const int num_items = kMode == kGradWeight ? args.E * strips * ((args.K + kN - 1) / kN) : item_of[args.E];
+    int *err = args.hdr;
+    auto two_tiles = [&](const Item &it) { return it.d0 + kTileRows < args.D; };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ------------------------------------------------------------ loads
+            // the M side of product and input gradient is the weights: one expert's
+            // are read by the row chunks of a block at about the same time
+            const uint64_t pol_m = kN == 32 ? policy_evict_first() : policy_evict_last();
+            const uint64_t pol_n = policy_evict_last();
+            int stage = 0;
+            uint32_t phase = 0, filled = 0, fill_parity = 0;
+            bool ok = true;
+            for (int u = blockIdx.x; ok && u < num_items; u += gridDim.x) {
+                const Item it = walk.at(u);
+                const int tiles_m = two_tiles(it) ? 2 : 1;
+                const int boxes_n = kNMn ? (it.cols + 63) / 64 : (it.cols + kRowBox - 1) / kRowBox;
+                const uint32_t bytes = uint32_t(tiles_m * kTileRows * 128 + boxes_n * (kNMn ? 64 : kRowBox) * 128);
+                for (int kb = 0; kb < it.kblocks; ++kb) {
+                    if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, err, 31)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *a = tiles + stage * C::kStageBytes, *b = a + C::kABytes;
+                    mbar_arrive_expect_tx(&full[stage], bytes);
+                    if constexpr (kMode == kProduct) {
+                        for (int t = 0; t < tiles_m; ++t)
+                            tma_load_3d(a + t * kTileRows * 128, &tmap_m, &full[stage], kb * kBlockK,
+                                        it.d0 + t * kTileRows, it.e, pol_m);
+                    } else {
+                        for (int t = 0; t < 2 * tiles_m; ++t) {
+                            if constexpr (kMode == kGradInput)
+                                tma_load_3d(a + t * 64 * 128, &tmap_m, &full[stage], it.d0 + t * 64, kb * kBlockK, it.e,
+                                            pol_m);
+                            else
+                                tma_load_2d(a + t * 64 * 128, &tmap_m, &full[stage], it.d0 + t * 64,
+                                            row_of[it.e] + kb * kBlockK, pol_n);
+                        }
+                    }
+                    for (int t = 0; t < boxes_n; ++t) {
+                        if constexpr (kNMn)
+                            tma_load_2d(b + t * 64 * 128, &tmap_n, &full[stage], it.n0 + t * 64,
+                                        row_of[it.e] + kb * kBlockK, pol_n);
+                        else
+                            tma_load_2d(b + t * kRowBox * 128, &tmap_n, &full[stage], kb * kBlockK,
+                                        it.n0 + t * kRowBox, pol_n);
+                    }
+                    filled |= 1u << stage;
+                    fill_parity = (fill_parity & ~(1u << stage)) | (phase << stage);
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // every issued copy must have landed before the CTA may exit
+            for (int s = 0; s < kStages; ++s) {
+                if (!(filled >> s & 1u)) continue;
+                const uint32_t par = (fill_parity >> s) & 1u;
+                const unsigned long long t0 = global_timer_ns();
+                while (!mbar_try_wait(&full[s], par) && global_timer_ns() - t0 < kWaitTimeoutNs) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1 || warp == 2) {
+        if (lane == 0) {
+            // ------------------------------------------------------------ MMA issuer of tile a
+            const int a = warp - 1;
+            int stage = 0, li = 0;
+            uint32_t phase = 0, fixed_phase = 0;
+            bool ok = true;
+            for (int u = blockIdx.x; ok && u < num_items; u += gridDim.x) {
+                const Item it = walk.at(u);
+                if (it.kblocks == 0) continue;
+                const bool valid = a == 0 || two_tiles(it);
+                const uint32_t n = uint32_t((it.cols + 15) / 16 * 16);
+                const uint32_t idesc = idesc_bf16(n) | (kMMn ? 1u << 15 : 0u) | (kNMn ? 1u << 16 : 0u);
+                const int buf = li % C::kBufs;
+                const uint32_t use = uint32_t(li / C::kBufs) & 1u;
+                if (valid) {
+                    if (!mbar_wait(&tmem_empty[2 * a + buf], use ^ 1u, abort_flag, err, 32)) break;
+                    tc_fence_after();
+                    ++li;
+                }
+                const uint32_t acc = tmem + uint32_t((buf * 2 + a) * kN);
+                for (int kb = 0; kb < it.kblocks; ++kb) {
+                    if (!mbar_wait(&full[stage], phase, abort_flag, err, 33)) {
+                        ok = false;
+                        break;
+                    }
+                    int steps = kBlockK / 16;
+                    if constexpr (kMode == kGradWeight) {
+                        if (kb == it.kblocks - 1) {
+                            steps = (it.tail + 15) / 16;
+                            if (it.tail % 16) {
+                                if (!mbar_wait(&fixed[stage], (fixed_phase >> stage) & 1u, abort_flag, err, 34)) {
+                                    ok = false;
+                                    break;
+                                }
+                                fixed_phase ^= 1u << stage;
+                            }
+                        }
+                    }
+                    tc_fence_after();
+                    if (valid) {
+                        const uint32_t st = smem_u32(tiles + stage * C::kStageBytes);
+                        const uint32_t sa = st + uint32_t(a * kTileRows * 128), sb = st + C::kABytes;
+                        const uint64_t adesc = kMMn ? smem_desc_mn_sw128(sa) : smem_desc_sw128(sa);
+                        const uint64_t bdesc = kNMn ? smem_desc_mn_sw128(sb) : smem_desc_sw128(sb);
+                        // a step is 16 contraction elements: 32 bytes inside the swizzled
+                        // row (K-major) or 16 rows of 128 bytes (MN-major), in 16-byte units
+                        for (int ks = 0; ks < steps; ++ks)
+                            tc_mma_bf16(acc, adesc + uint64_t(ks * (kMMn ? 128 : 2)),
+                                        bdesc + uint64_t(ks * (kNMn ? 128 : 2)), idesc, (kb | ks) ? 1u : 0u);
+                    }
+                    tc_commit(&empty[stage]);
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                if (valid) tc_commit(&tmem_full[2 * a + buf]);
+            }
+            // all issued MMAs must be finished before TMEM is released
+            tc_commit(&mma_done[a]);
+            const unsigned long long t0 = global_timer_ns();
+            while (!mbar_try_wait(&mma_done[a], 0) && global_timer_ns() - t0 < kWaitTimeoutNs) {
+            }
+        }
+        __syncwarp();
+    } else if (warp == 3) {
+        if constexpr (kMode == kGradWeight) {
+            // ------------------------------------------------------------ tail rows
+            // the rows of the next group (or past the tensor) inside the last
+            // 16-row step of an item, zeroed on both sides; a row is 128 bytes in
+            // every box, so the swizzle inside it does not matter.  This warp is a
+            // consumer of every stage, so that it meets each one in its turn.
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int u = blockIdx.x; ok && u < num_items; u += gridDim.x) {
+                const Item it = walk.at(u);
+                for (int kb = 0; kb < it.kblocks; ++kb) {
+                    if (!mbar_wait(&full[stage], phase, abort_flag, err, 35)) {
+                        ok = false;
+                        break;
+                    }
+                    if (kb == it.kblocks - 1 && it.tail % 16) {
+                        uint8_t *a = tiles + stage * C::kStageBytes + it.tail * 128;
+                        const int per_box = (16 - it.tail % 16) * 8;  // 16-byte pieces
+                        constexpr int kBoxes = C::kStageBytes / (64 * 128);
+                        for (int i = lane; i < kBoxes * per_box; i += 32)
+                            *reinterpret_cast<uint4 *>(a + i / per_box * 64 * 128 + i % per_box * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&fixed[stage]);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&empty[stage]);
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------------- epilogue of tile a
+        const int a = (warp - 4) >> 2, q = warp & 3;
+        if constexpr (kMode != kGradWeight) {
+            if (args.zero_unused) {
+                // rows before the first group and behind the last, 8 columns per store
+                const int64_t v_row = args.D / 8;
+                const int64_t head = row_of[0], behind = args.R - row_of[args.E];
+                const int64_t total = (head + behind) * v_row;
+                uint4 *o = reinterpret_cast<uint4 *>(args.out);
+                for (int64_t i = int64_t(blockIdx.x) * 256 + (threadIdx.x - 128); i < total; i += int64_t(gridDim.x) * 256) {
+                    const int64_t r = i / v_row;
+                    const int64_t row = r < head ? r : r - head + row_of[args.E];
+                    o[row * v_row + (i - r * v_row)] = make_uint4(0, 0, 0, 0);
+                }
+            }
+        }
+        int li = 0;
+        for (int u = blockIdx.x; u < num_items; u += gridDim.x) {
+            const Item it = walk.at(u);
+            if (a == 1 && !two_tiles(it)) continue;
+            const int d = it.d0 + a * kTileRows + q * 32 + lane;
+            const bool have = it.kblocks > 0;  // else a weight gradient without rows: zeros
+            const int buf = li % C::kBufs;
+            const uint32_t use = uint32_t(li / C::kBufs) & 1u;
+            if (have) {
+                if (!mbar_wait(&tmem_full[2 * a + buf], use, abort_flag, err, 36)) break;
+                tc_fence_after();
+                ++li;
+            }
+            const uint32_t acc = tmem + (uint32_t(q * 32) << 16) + uint32_t((buf * 2 + a) * kN);
+            const int blocks = (it.cols + 31) / 32;
+#pragma unroll 1
+            for (int cb = 0; cb < blocks; ++cb) {
+                uint32_t v[32];
+                if (have) {
+                    tmem_ld_32x32(acc + uint32_t(cb * 32), v);
+                    tmem_ld_wait();
+                    if (cb == blocks - 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&tmem_empty[2 * a + buf]);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0u;
+                }
+                const int left = it.cols - cb * 32;
+                if (d >= args.D) {
+                    // a lane past the strip's features
+                } else if constexpr (kMode == kGradWeight) {
+                    // thread = row n of dW, 32 consecutive columns k (K % 8 == 0)
+                    __nv_bfloat16 *o = args.out + (int64_t(it.e) * args.D + d) * args.K + it.n0 + cb * 32;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(v[8 * j + 2 * i]),
+                                                                           __uint_as_float(v[8 * j + 2 * i + 1]));
+                            w[i] = *reinterpret_cast<const uint32_t *>(&p);
+                        }
+                        if (8 * j < left) reinterpret_cast<uint4 *>(o)[j] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else {
+                    // thread = output feature d, 32 consecutive rows
+                    __nv_bfloat16 *o = args.out + int64_t(it.n0 + cb * 32) * args.D + d;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (j < left) o[int64_t(j) * args.D] = __float2bfloat16_rn(__uint_as_float(v[j]));
+                }
+                __syncwarp();
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+}
+
+template <int kMode, int kN>
+cudaError_t launch_grouped(const CUtensorMap &tmap_m, const CUtensorMap &tmap_n, const GroupedArgs &a, int64_t items,
+                           cudaStream_t stream) {
+    using C = GroupedCfg<kN>;
+    const cudaError_t e =
+        set_max_dynamic_smem(reinterpret_cast<const void *>(grouped_kernel<kMode, kN>), C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    const int sms = num_sms();
+    const int grid = items < sms ? int(items) : sms;
+    return launch_pdl(grouped_kernel<kMode, kN>, dim3(unsigned(grid)), dim3(kThreads), C::kSmemBytes, stream, tmap_m,
+                      tmap_n, a);
+}
+
+moe_status_t check_grouped(int R, int E, int N, int K) {
+    if (R < 0 || E <= 0 || N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
+    if (E > kMaxExperts || N % 8 || K % 8 || N > kGroupedMaxWidth || K > kGroupedMaxWidth) return MOE_ERR_UNSUPPORTED_SHAPE;
+    // every expert's items fit an int: strips <= 512, chunks <= R / 32 + E
+    if ((int64_t(R) / 32 + E) * ((int64_t(N > K ? N : K) + kStrip - 1) / kStrip) > 2000000000ll ||
+        int64_t(E) * ((N + 255) / 256) * ((K + 255) / 256) > 2000000000ll)
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+
+// The product (grad = false: rows x [R, K] -> out [R, N]) or the input
+// gradient (rows dy [R, N] -> out [R, K]).
+moe_status_t run_rows(bool grad, const void *rows, const void *w, const int32_t *offsets, void *out, int R, int E,
+                      int N, int K, int zero_unused, void *workspace, size_t ws_bytes, moe_stream_t stream) {
+    moe_status_t s = check_grouped(R, E, N, K);
+    if (s != MOE_OK) return s;
+    if (R == 0) return MOE_OK;
+    if (!rows || !w || !offsets || !out || !workspace || !aligned(rows, 16) || !aligned(w, 16) ||
+        !aligned(offsets, 4) || !aligned(out, 16) || !aligned(workspace, 256))
+        return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < size_t(kHdrBytes)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    DeviceScope dev(out);
+    if (dev.status != MOE_OK) return dev.status;
+    GroupedArgs a{};
+    a.offsets = offsets;
+    a.out = static_cast<__nv_bfloat16 *>(out);
+    a.hdr = static_cast<int *>(workspace);
+    a.R = R;
+    a.E = E;
+    a.D = grad ? K : N;
+    a.C = grad ? N : K;
+    a.K = K;
+    a.zero_unused = zero_unused;
+    // up to 8 rows per expert on average: 32-row chunks, the rule of the routed layer
+    const bool small = R <= int64_t(8) * E;
+    const int kn = small ? 32 : 256;
+    CUtensorMap tm, tn;
+    if (!encode_bf16_3d(&tm, w, uint64_t(K), uint64_t(N), uint64_t(E), grad ? kBlockK : kTileRows) ||
+        !encode_bf16_rows(&tn, rows, uint64_t(a.C), uint64_t(R), kRowBox))
+        return MOE_ERR_CUDA;
+    const int64_t chunks = int64_t(R) / kn + (R < E ? R : E);
+    const int64_t items = chunks * ((a.D + kStrip - 1) / kStrip);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (grad)
+        e = small ? launch_grouped<kGradInput, 32>(tm, tn, a, items, st)
+                  : launch_grouped<kGradInput, 256>(tm, tn, a, items, st);
+    else
+        e = small ? launch_grouped<kProduct, 32>(tm, tn, a, items, st)
+                  : launch_grouped<kProduct, 256>(tm, tn, a, items, st);
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status_t moe_grouped_workspace_bytes(size_t *bytes) {
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    *bytes = kHdrBytes;
+    return MOE_OK;
+}
+
+moe_status_t moe_grouped_matmul(const void *x_bf16, const void *w_bf16, const int32_t *offsets, void *y_bf16, int R,
+                                int E, int N, int K, int zero_unused, void *workspace, size_t ws_bytes,
+                                moe_stream_t stream) {
+    return run_rows(false, x_bf16, w_bf16, offsets, y_bf16, R, E, N, K, zero_unused, workspace, ws_bytes, stream);
+}
+
+moe_status_t moe_grouped_matmul_grad_input(const void *dy_bf16, const void *w_bf16, const int32_t *offsets,
+                                           void *dx_bf16, int R, int E, int N, int K, int zero_unused, void *workspace,
+                                           size_t ws_bytes, moe_stream_t stream) {
+    return run_rows(true, dy_bf16, w_bf16, offsets, dx_bf16, R, E, N, K, zero_unused, workspace, ws_bytes, stream);
+}
+
+moe_status_t moe_grouped_matmul_grad_weight(const void *dy_bf16, const void *x_bf16, const int32_t *offsets,
+                                            void *dw_bf16, int R, int E, int N, int K, void *workspace, size_t ws_bytes,
+                                            moe_stream_t stream) {
+    moe_status_t s = check_grouped(R, E, N, K);
+    if (s != MOE_OK) return s;
+    if (!dw_bf16 || !offsets || !workspace || !aligned(dw_bf16, 16) || !aligned(offsets, 4) ||
+        !aligned(workspace, 256) || (R > 0 && (!dy_bf16 || !x_bf16 || !aligned(dy_bf16, 16) || !aligned(x_bf16, 16))))
+        return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < size_t(kHdrBytes)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    DeviceScope dev(dw_bf16);
+    if (dev.status != MOE_OK) return dev.status;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (R == 0) {
+        // no rows to map: every gradient is zero, and the error word says so
+        cudaError_t e = cudaMemsetAsync(dw_bf16, 0, size_t(E) * size_t(N) * size_t(K) * 2, st);
+        if (e == cudaSuccess) e = cudaMemsetAsync(workspace, 0, kHdrBytes, st);
+        return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    }
+    GroupedArgs a{};
+    a.offsets = offsets;
+    a.out = static_cast<__nv_bfloat16 *>(dw_bf16);
+    a.hdr = static_cast<int *>(workspace);
+    a.R = R;
+    a.E = E;
+    a.D = N;
+    a.K = K;
+    CUtensorMap tm, tn;
+    if (!encode_bf16_rows(&tm, dy_bf16, uint64_t(N), uint64_t(R), kBlockK) ||
+        !encode_bf16_rows(&tn, x_bf16, uint64_t(K), uint64_t(R), kBlockK))
+        return MOE_ERR_CUDA;
+    const int64_t items = int64_t(E) * ((N + kStrip - 1) / kStrip) * ((K + 255) / 256);
+    const cudaError_t e = launch_grouped<kGradWeight, 256>(tm, tn, a, items, st);
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // extern "C"

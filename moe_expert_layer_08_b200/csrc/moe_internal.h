@@ -105,6 +105,11 @@ cudaError_t launch_shared(bool gemm1, const CUtensorMap &tmap_w, const CUtensorM
 // Tensor map of a row-major bf16 matrix [rows][cols]: boxes of 64 columns
 // (128 bytes, 128-byte swizzle) x box_rows rows.
 bool encode_bf16_rows(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, int box_rows);
+// The same for the row-major matrices of several experts, [experts][rows][cols]:
+// a box stays inside one expert (rows past it read as zeros).
+bool encode_bf16_3d(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, uint64_t experts, int box_rows);
+
+constexpr int kGroupedMaxWidth = 131072;  // features of a grouped product's operands, at most
 
 // Multiprocessors of the current device (cached per device).
 int num_sms();
@@ -116,6 +121,22 @@ cudaError_t set_max_dynamic_smem(const void *kernel, int bytes);
 bool aligned(const void *p, uintptr_t a);
 moe_status_t check_shape(int E, int H, int I);
 moe_status_t use_device_of(const void *p);
+// use_device_of for the length of a call: the device that was current before
+// is current again afterwards.
+struct DeviceScope {
+    int prev = -1;
+    moe_status_t status;
+    explicit DeviceScope(const void *p) {
+        if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
+        status = use_device_of(p);
+    }
+    ~DeviceScope() {
+        int cur = -1;
+        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
+    }
+    DeviceScope(const DeviceScope &) = delete;
+    DeviceScope &operator=(const DeviceScope &) = delete;
+};
 
 // The launch sequence of one layer on a validated, large-enough workspace of
 // the current device.
