@@ -608,8 +608,8 @@ moe_status_t moe_grouped_matmul_grad_weight(const void *dy_bf16, const void *x_b
  *   y[t, n] = sum_k x[t, k] * scale(w_sf[n, k / G]) * e2m1(w_fp4[n, k])
  * with the weights as moe_quantize_fp4 (MOE_FP4_MX: UE8M0 scales, G = 32) or
  * moe_quantize_nvfp4 (MOE_FP4_NVFP4: UE4M3 scales, G = 16) writes them:
- * w_fp4 u8 [N, K/2] (16-byte aligned), w_sf u8 [N, K/G]; x bf16 [T, K]
- * (16-byte aligned), y bf16 [T, N].  x is not quantised; sums are fp32 (x times
+ * w_fp4 u8 [N, K/2], w_sf u8 [N, K/G] and x bf16 [T, K], all 16-byte
+ * aligned; y bf16 [T, N].  x is not quantised; sums are fp32 (x times
  * a power of two enters them as fp16: an element is exact down to 2^-31 of its
  * token's largest one in an eighth of K, and off by at most 2^-40 of it
  * below).  Scale bytes 255 (UE8M0) and 0x7F (UE4M3; bit 7 is not read) are NaN.

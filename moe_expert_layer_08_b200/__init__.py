@@ -145,6 +145,8 @@ def _declare(lib):
 def load():
     """The loaded CUDA library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -715,21 +717,29 @@ def ipc_close(base: int) -> None:
 
 
 # ------------------------------------------------------------ around the expert layer
+# These calls take a few microseconds on the GPU at decode, so the binding keeps
+# its own share small: one test of a tensor where it is as it should be.
 def _need_on(t, dtype, name, shape, device):
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device \
+            and t.is_contiguous():
+        return
     _need(t, dtype, name)
     if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _stream_on(stream, device):
     """The given stream, or the current one of ``device``."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    if stream.device != device:
         raise ValueError(f"stream must be on {device}, got {stream.device}")
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 def grouped_workspace_bytes() -> int:
@@ -763,7 +773,7 @@ def _grouped_rows(fn, rows, w, offsets, out, workspace, stream, width_in, width_
     else:
         _need_on(out, torch.bfloat16, "out", shape, dev)
     ws = _grouped_workspace(workspace, dev)
-    _check(getattr(load(), fn)(_ptr(rows), _ptr(w), _ptr(offsets), _ptr(out), R, E, N, K, int(zero_unused), _ptr(ws),
+    _check(getattr(load(), fn)(_addr(rows), _addr(w), _addr(offsets), _addr(out), R, E, N, K, int(zero_unused), _addr(ws),
                                ws.numel(), _stream_on(stream, dev)), fn)
     return out
 
@@ -808,7 +818,7 @@ def grouped_matmul_grad_weight(dy, x, offsets, out=None, workspace=None, stream=
     else:
         _need_on(out, torch.bfloat16, "out", (E, N, K), dev)
     ws = _grouped_workspace(workspace, dev)
-    _check(load().moe_grouped_matmul_grad_weight(_ptr(dy), _ptr(x), _ptr(offsets), _ptr(out), R, E, N, K, _ptr(ws),
+    _check(load().moe_grouped_matmul_grad_weight(_addr(dy), _addr(x), _addr(offsets), _addr(out), R, E, N, K, _addr(ws),
                                                  ws.numel(), _stream_on(stream, dev)),
            "moe_grouped_matmul_grad_weight")
     return out
@@ -834,7 +844,7 @@ def fp4_matvec(x, w, w_sf, fmt: str = "mx", out=None, stream=None):
         out = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
     else:
         _need_on(out, torch.bfloat16, "out", (T, N), dev)
-    _check(load().moe_fp4_matvec(_ptr(x), _ptr(w), _ptr(w_sf), _ptr(out), T, N, K, code, _stream_on(stream, dev)),
+    _check(load().moe_fp4_matvec(_addr(x), _addr(w), _addr(w_sf), _addr(out), T, N, K, code, _stream_on(stream, dev)),
            "moe_fp4_matvec")
     return out
 
@@ -868,7 +878,7 @@ def norm_before(x, weight, eps: float = 1e-6, bf16: bool = True, fp8: bool = Fal
     q = torch.empty((T, H), dtype=torch.uint8, device=dev) if fp8 else None
     sf = torch.empty((T, H // 32), dtype=torch.uint8, device=dev) if fp8 else None
     r = torch.empty(T, dtype=torch.float32, device=dev) if rstd else None
-    _check(load().moe_norm_before(_ptr(x), _ptr(weight), T, H, eps, _ptr(y), _ptr(q), _ptr(sf), _ptr(r),
+    _check(load().moe_norm_before(_addr(x), _addr(weight), T, H, eps, _addr(y), _addr(q), _addr(sf), _addr(r),
                                   _stream_on(stream, dev)), "moe_norm_before")
     return NormBefore(y, q, sf, r)
 
@@ -903,8 +913,8 @@ def norm_after(x, residual, weight, eps: float = 1e-6, gate=None, residual_scale
     else:
         _need_on(out, torch.bfloat16, "out", (T, H), dev)
     r = torch.empty(T, dtype=torch.float32, device=dev) if rstd else None
-    _check(load().moe_norm_after(_ptr(x), _ptr(residual), _ptr(weight), _ptr(gate), kind, T, H, eps, residual_scale,
-                                 _ptr(out), _ptr(r), _stream_on(stream, dev)), "moe_norm_after")
+    _check(load().moe_norm_after(_addr(x), _addr(residual), _addr(weight), _addr(gate), kind, T, H, eps, residual_scale,
+                                 _addr(out), _addr(r), _stream_on(stream, dev)), "moe_norm_after")
     return NormAfter(out, r)
 
 
@@ -939,8 +949,8 @@ def norm_before_backward(dy, x, weight, rstd, dresidual=None, workspace=None, st
     ws = _norm_workspace(workspace, T, H, dev)
     dx = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
     dweight = torch.empty(H, dtype=torch.float32, device=dev)
-    _check(load().moe_norm_before_backward(_ptr(dy), _ptr(x), _ptr(weight), _ptr(rstd), _ptr(dresidual), T, H,
-                                           _ptr(dx), _ptr(dweight), _ptr(ws), ws.numel(), _stream_on(stream, dev)),
+    _check(load().moe_norm_before_backward(_addr(dy), _addr(x), _addr(weight), _addr(rstd), _addr(dresidual), T, H,
+                                           _addr(dx), _addr(dweight), _addr(ws), ws.numel(), _stream_on(stream, dev)),
            "moe_norm_before_backward")
     return dx, dweight
 
@@ -964,7 +974,7 @@ def norm_after_backward(dout, x, weight, rstd, gate=None, residual_scale: float 
     dgate = None
     if kind:
         dgate = torch.empty(gate.shape, dtype=torch.bfloat16 if kind == 3 else torch.float32, device=dev)
-    _check(load().moe_norm_after_backward(_ptr(dout), _ptr(x), _ptr(weight), _ptr(rstd), _ptr(gate), kind, T, H,
-                                          residual_scale, _ptr(dx), _ptr(dresidual), _ptr(dweight), _ptr(dgate),
-                                          _ptr(ws), ws.numel(), _stream_on(stream, dev)), "moe_norm_after_backward")
+    _check(load().moe_norm_after_backward(_addr(dout), _addr(x), _addr(weight), _addr(rstd), _addr(gate), kind, T, H,
+                                          residual_scale, _addr(dx), _addr(dresidual), _addr(dweight), _addr(dgate),
+                                          _addr(ws), ws.numel(), _stream_on(stream, dev)), "moe_norm_after_backward")
     return dx, dresidual, dweight, dgate

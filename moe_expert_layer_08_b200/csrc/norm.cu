@@ -8,12 +8,14 @@
 // and, with xhat = x rstd and dz the gradient that reaches x rstd w,
 //   dx = rstd (dz w - xhat mean(dz w xhat)) [+ the residual branch's gradient]
 //   dw = sum_t dz xhat,  dg = dout (x rstd w) summed to g's shape.
-// All four are bound by HBM: each row is read once into registers, reduced
-// and written.  A block takes every gridDim.x-th row with its columns fixed to
-// its threads (8 at a time, 16-byte accesses), so the weights and the column
-// sums of the gradients stay in registers over the rows.  Sums are fp32; the
-// column sums of the blocks are written out and added in block order by a
-// second kernel, so results do not depend on timing.
+// All four are bound by HBM.  A block takes every gridDim.x-th row with its
+// columns fixed to its threads (8 at a time, 16-byte accesses), so the column
+// sums of the gradients stay in registers over the rows.  A thread brings its
+// own pieces of the rows ahead into its own part of a shared-memory ring
+// (cp.async), so several rows a block are in flight and no barrier is needed
+// to read them.  Sums are fp32; the column sums of the blocks are written out
+// and added in block order by a second kernel, so results do not depend on
+// timing.
 #include "moe_common.cuh"
 #include "moe_internal.h"
 
@@ -33,12 +35,7 @@ struct Bf16x8 {
 
 __device__ __forceinline__ Bf16x8 load8(const __nv_bfloat16 *p) {
     Bf16x8 v;
-    v.u = *reinterpret_cast<const uint4 *>(p);
-    return v;
-}
-__device__ __forceinline__ Bf16x8 load8_stream(const __nv_bfloat16 *p) {
-    Bf16x8 v;
-    v.u = __ldcs(reinterpret_cast<const uint4 *>(p));
+    v.u = __ldg(reinterpret_cast<const uint4 *>(p));
     return v;
 }
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -93,37 +90,84 @@ struct NormArgs {
     void *dgate;                    // per token: f32 [T]; per element: bf16 [T, H]
 };
 
-// Forward of both norms. kVecs: 8-column pieces of a row per thread.
-template <int kVecs, bool kAfter>
-__global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a) {
+// Rows ahead in shared memory: more where a row has fewer streams.
+constexpr int norm_depth(int streams) { return 5 - streams; }
+
+// The ring of one thread's pieces: kStreams inputs of a row, norm_depth rows.
+template <int kVecs, int kStreams>
+struct RowRing {
+    static constexpr int kDepth = norm_depth(kStreams);
+    uint4 *mine;               // this thread's first piece
+    const __nv_bfloat16 *src[kStreams];
+    int T, H, row, slot;       // the next row to bring, and where
+
+    __device__ __forceinline__ uint4 *at(int slot_, int stream, int i) const {
+        return mine + ((slot_ * kStreams + stream) * kVecs + i) * blockDim.x;
+    }
+    __device__ __forceinline__ void next() {
+        if (row < T) {
+#pragma unroll
+            for (int s = 0; s < kStreams; ++s)
+#pragma unroll
+                for (int i = 0; i < kVecs; ++i) {
+                    const int c = threadIdx.x + i * blockDim.x;
+                    if (c < H / 8)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(at(slot, s, i))),
+                                     "l"(src[s] + int64_t(row) * H + c * 8)
+                                     : "memory");
+                }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        row += gridDim.x;
+        if (++slot == kDepth) slot = 0;
+    }
+    // All but the newest kDepth - 1 rows have landed (for this thread).
+    __device__ __forceinline__ void wait() const {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+    }
+    __device__ __forceinline__ Bf16x8 get(int slot_, int stream, int i) const {
+        Bf16x8 v;
+        v.u = *at(slot_, stream, i);
+        return v;
+    }
+};
+
+// Forward of both norms. kVecs: 8-column pieces of a row per thread. Streams:
+// x; after: x, residual and, for a gate per element, that.
+template <int kVecs, bool kAfter, int kStreams>
+__global__ void __launch_bounds__(kVecs == 1 ? 1024 : 512, kVecs == 1 ? 1 : 2) norm_kernel(const NormArgs a) {
+    extern __shared__ uint4 ring_smem[];
     __shared__ float red[2][2][32];
     const int nvec = a.H / 8;
     pdl_wait();
     pdl_trigger();
-    Bf16x8 w[kVecs];
+    RowRing<kVecs, kStreams> ring;
+    ring.mine = ring_smem + threadIdx.x;
+    ring.src[0] = a.x;
+    if constexpr (kStreams > 1) ring.src[1] = a.residual;
+    if constexpr (kStreams > 2) ring.src[2] = a.gate;
+    ring.T = a.T;
+    ring.H = a.H;
+    ring.row = blockIdx.x;
+    ring.slot = 0;
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-        const int c = threadIdx.x + i * blockDim.x;
-        if (c < nvec) w[i] = load8(a.weight + c * 8);
-    }
-    int flip = 0;
+    for (int d = 0; d < ring.kDepth - 1; ++d) ring.next();
+    int flip = 0, slot = 0;
     for (int row = blockIdx.x; row < a.T; row += gridDim.x, flip ^= 1) {
         const int64_t base = int64_t(row) * a.H;
-        Bf16x8 x[kVecs];
+        ring.next();
+        ring.wait();
         float ss = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            const int c = threadIdx.x + i * blockDim.x;
-            x[i].u = make_uint4(0, 0, 0, 0);
-            if (c < nvec) x[i] = load8_stream(a.x + base + c * 8);
-        }
-#pragma unroll
         for (int i = 0; i < kVecs; ++i)
+            if (int(threadIdx.x + i * blockDim.x) < nvec) {
+                const Bf16x8 x = ring.get(slot, 0, i);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 v = x[i].pair(j);
-                ss = fmaf(v.x, v.x, ss);
-                ss = fmaf(v.y, v.y, ss);
+                for (int j = 0; j < 4; ++j) {
+                    const float2 v = x.pair(j);
+                    ss = fmaf(v.x, v.x, ss);
+                    ss = fmaf(v.y, v.y, ss);
+                }
             }
         const float rstd = __frsqrt_rn(block_sum(ss, 0.0f, red[flip]).x / float(a.H) + a.eps);
         if (a.rstd_out && threadIdx.x == 0) a.rstd_out[row] = rstd;
@@ -134,27 +178,37 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a) {
             const int c = threadIdx.x + i * blockDim.x;
             const bool in = c < nvec;
             float v[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 xv = x[i].pair(j), wv = w[i].pair(j);
-                v[2 * j] = xv.x * rstd * wv.x;
-                v[2 * j + 1] = xv.y * rstd * wv.y;
-            }
-            if constexpr (kAfter) {
-                if (!in) continue;
-                const Bf16x8 r = load8_stream(a.residual + base + c * 8);
-                Bf16x8 g;
-                if (a.gate_kind == MOE_GATE_CHANNEL) g = load8(a.gate + c * 8);
-                if (a.gate_kind == MOE_GATE_FULL) g = load8_stream(a.gate + base + c * 8);
+            if (in) {
+                const Bf16x8 x = ring.get(slot, 0, i), w = load8(a.weight + c * 8);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 rv = r.pair(j);
-                    float2 gv = make_float2(tgate, tgate);
-                    if (a.gate_kind == MOE_GATE_CHANNEL || a.gate_kind == MOE_GATE_FULL) gv = g.pair(j);
-                    v[2 * j] = fmaf(gv.x, v[2 * j], a.alpha * rv.x);
-                    v[2 * j + 1] = fmaf(gv.y, v[2 * j + 1], a.alpha * rv.y);
+                    const float2 xv = x.pair(j), wv = w.pair(j);
+                    v[2 * j] = xv.x * rstd * wv.x;
+                    v[2 * j + 1] = xv.y * rstd * wv.y;
                 }
-                store8(a.y + base + c * 8, pack8(v));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+            }
+            if constexpr (kAfter) {
+                if (in) {
+                    const Bf16x8 r = ring.get(slot, 1, i);
+                    Bf16x8 g;
+                    if constexpr (kStreams > 2) {
+                        g = ring.get(slot, 2, i);
+                    } else {
+                        if (a.gate_kind == MOE_GATE_CHANNEL) g = load8(a.gate + c * 8);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 rv = r.pair(j);
+                        float2 gv = make_float2(tgate, tgate);
+                        if (kStreams > 2 || a.gate_kind == MOE_GATE_CHANNEL) gv = g.pair(j);
+                        v[2 * j] = fmaf(gv.x, v[2 * j], a.alpha * rv.x);
+                        v[2 * j + 1] = fmaf(gv.y, v[2 * j + 1], a.alpha * rv.y);
+                    }
+                    store8(a.y + base + c * 8, pack8(v));
+                }
             } else {
                 const Bf16x8 y = pack8(v);
                 if (a.y && in) store8(a.y + base + c * 8, y);
@@ -185,81 +239,91 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a) {
                 }
             }
         }
+        if (++slot == ring.kDepth) slot = 0;
     }
 }
 
 // Gradients of both norms: dx, the residual branch, per-token and per-element
 // gates; the column sums of the weight (and of a per-channel gate) per block.
-template <int kVecs, bool kAfter>
-__global__ void __launch_bounds__(1024) norm_backward_kernel(const NormArgs a) {
+// Streams: dy, x; then before: the residual branch's gradient if there is one,
+// after: a gate per element.
+template <int kVecs, bool kAfter, int kStreams>
+__global__ void __launch_bounds__(kVecs == 1 ? 1024 : 512, kVecs == 2 ? 2 : 1) norm_backward_kernel(const NormArgs a) {
+    extern __shared__ uint4 ring_smem[];
     __shared__ float red[2][2][32];
     const int nvec = a.H / 8;
-    const bool channel = kAfter && a.gate_kind == MOE_GATE_CHANNEL;
+    const bool channel = kAfter && kStreams == 2 && a.gate_kind == MOE_GATE_CHANNEL;
     pdl_wait();
     pdl_trigger();
-    Bf16x8 w[kVecs], gc[kVecs];
-    float dw[kVecs][8], dg[kAfter ? kVecs : 1][8];
+    RowRing<kVecs, kStreams> ring;
+    ring.mine = ring_smem + threadIdx.x;
+    ring.src[0] = a.dy;
+    ring.src[1] = a.x;
+    if constexpr (kStreams > 2) ring.src[2] = kAfter ? a.gate : a.dres_in;
+    ring.T = a.T;
+    ring.H = a.H;
+    ring.row = blockIdx.x;
+    ring.slot = 0;
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-        const int c = threadIdx.x + i * blockDim.x;
-        w[i].u = make_uint4(0, 0, 0, 0);
-        if (c < nvec) w[i] = load8(a.weight + c * 8);
-        if (channel && c < nvec) gc[i] = load8(a.gate + c * 8);
+    for (int d = 0; d < ring.kDepth - 1; ++d) ring.next();
+    float dw[kVecs][8], dg[kAfter && kStreams == 2 ? kVecs : 1][8];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             dw[i][j] = 0.0f;
-            if (kAfter) dg[i][j] = 0.0f;
+            if (kAfter && kStreams == 2) dg[i][j] = 0.0f;
         }
-    }
-    int flip = 0;
+    int flip = 0, slot = 0;
     for (int row = blockIdx.x; row < a.T; row += gridDim.x, flip ^= 1) {
         const int64_t base = int64_t(row) * a.H;
         const float rstd = a.rstd[row];
         float tgate = 1.0f;
         if (kAfter && a.gate_kind == MOE_GATE_TOKEN) tgate = __bfloat162float(a.gate[row]);
-        Bf16x8 x[kVecs], dy[kVecs];
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            const int c = threadIdx.x + i * blockDim.x;
-            x[i].u = dy[i].u = make_uint4(0, 0, 0, 0);
-            if (c < nvec) {
-                x[i] = load8_stream(a.x + base + c * 8);
-                dy[i] = load8_stream(a.dy + base + c * 8);
+        ring.next();
+        ring.wait();
+        // the gate of piece i (its elements, or one value for all of them)
+        auto gate_of = [&](int i, int c, Bf16x8 &g) {
+            if constexpr (kAfter) {
+                if constexpr (kStreams > 2)
+                    g = ring.get(slot, 2, i);
+                else if (channel)
+                    g = load8(a.gate + c * 8);
             }
-        }
+        };
         float dot = 0.0f, tsum = 0.0f;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
             const int c = threadIdx.x + i * blockDim.x;
+            if (c >= nvec) continue;
+            const Bf16x8 dy = ring.get(slot, 0, i), x = ring.get(slot, 1, i), w = load8(a.weight + c * 8);
             Bf16x8 g;
-            if (channel) g = gc[i];
-            if (kAfter && a.gate_kind == MOE_GATE_FULL && c < nvec) g = load8(a.gate + base + c * 8);
+            gate_of(i, c, g);
             float de[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float2 x2 = x[i].pair(j / 2), d2 = dy[i].pair(j / 2), w2 = w[i].pair(j / 2);
-                const float xh = (j & 1 ? x2.y : x2.x) * rstd;
-                const float dout = j & 1 ? d2.y : d2.x;
-                const float wv = j & 1 ? w2.y : w2.x;
-                float dz = dout;
-                if (kAfter) {
-                    const float z = xh * wv;
-                    if (channel || a.gate_kind == MOE_GATE_FULL) {
-                        const float2 g2 = g.pair(j / 2);
-                        dz = dout * (j & 1 ? g2.y : g2.x);
-                    } else {
-                        dz = dout * tgate;
+            for (int j = 0; j < 4; ++j) {
+                const float2 x2 = x.pair(j), d2 = dy.pair(j), w2 = w.pair(j);
+                const float2 xh = make_float2(x2.x * rstd, x2.y * rstd);
+                float2 dz = d2;
+                if constexpr (kAfter) {
+                    float2 g2 = make_float2(tgate, tgate);
+                    if (kStreams > 2 || channel) g2 = g.pair(j);
+                    dz = make_float2(d2.x * g2.x, d2.y * g2.y);
+                    de[2 * j] = d2.x * (xh.x * w2.x);
+                    de[2 * j + 1] = d2.y * (xh.y * w2.y);
+                    if constexpr (kStreams == 2) {
+                        dg[i][2 * j] += de[2 * j];
+                        dg[i][2 * j + 1] += de[2 * j + 1];
+                        tsum += de[2 * j];
+                        tsum += de[2 * j + 1];
                     }
-                    if (channel) dg[i][j] = fmaf(dout, z, dg[i][j]);
-                    de[j] = dout * z;
-                    tsum += de[j];
                 }
-                if (c < nvec) {
-                    dw[i][j] = fmaf(dz, xh, dw[i][j]);
-                    dot = fmaf(dz * wv, xh, dot);
-                }
+                dw[i][2 * j] = fmaf(dz.x, xh.x, dw[i][2 * j]);
+                dw[i][2 * j + 1] = fmaf(dz.y, xh.y, dw[i][2 * j + 1]);
+                dot = fmaf(dz.x * w2.x, xh.x, dot);
+                dot = fmaf(dz.y * w2.y, xh.y, dot);
             }
-            if (kAfter && a.gate_kind == MOE_GATE_FULL && c < nvec)
+            if constexpr (kAfter && kStreams > 2)
                 store8(static_cast<__nv_bfloat16 *>(a.dgate) + base + c * 8, pack8(de));
         }
         const float2 s = block_sum(dot, tsum, red[flip]);
@@ -269,35 +333,35 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(const NormArgs a) {
         for (int i = 0; i < kVecs; ++i) {
             const int c = threadIdx.x + i * blockDim.x;
             if (c >= nvec) continue;
+            const Bf16x8 dy = ring.get(slot, 0, i), x = ring.get(slot, 1, i), w = load8(a.weight + c * 8);
             Bf16x8 g, add;
-            if (channel) g = gc[i];
-            if (kAfter && a.gate_kind == MOE_GATE_FULL) g = load8(a.gate + base + c * 8);
-            if (!kAfter && a.dres_in) add = load8_stream(a.dres_in + base + c * 8);
+            gate_of(i, c, g);
+            if constexpr (!kAfter && kStreams > 2) add = ring.get(slot, 2, i);
             float v[8], r[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float2 x2 = x[i].pair(j / 2), d2 = dy[i].pair(j / 2), w2 = w[i].pair(j / 2);
-                const float xh = (j & 1 ? x2.y : x2.x) * rstd;
-                const float dout = j & 1 ? d2.y : d2.x;
-                float dz = dout;
-                if (kAfter) {
-                    if (channel || a.gate_kind == MOE_GATE_FULL) {
-                        const float2 g2 = g.pair(j / 2);
-                        dz = dout * (j & 1 ? g2.y : g2.x);
-                    } else {
-                        dz = dout * tgate;
-                    }
-                    r[j] = a.alpha * dout;
+            for (int j = 0; j < 4; ++j) {
+                const float2 x2 = x.pair(j), d2 = dy.pair(j), w2 = w.pair(j);
+                const float2 xh = make_float2(x2.x * rstd, x2.y * rstd);
+                float2 dz = d2;
+                if constexpr (kAfter) {
+                    float2 g2 = make_float2(tgate, tgate);
+                    if (kStreams > 2 || channel) g2 = g.pair(j);
+                    dz = make_float2(d2.x * g2.x, d2.y * g2.y);
+                    r[2 * j] = a.alpha * d2.x;
+                    r[2 * j + 1] = a.alpha * d2.y;
                 }
-                v[j] = rstd * (dz * (j & 1 ? w2.y : w2.x) - xh * mean);
-                if (!kAfter && a.dres_in) {
-                    const float2 a2 = add.pair(j / 2);
-                    v[j] += j & 1 ? a2.y : a2.x;
+                v[2 * j] = rstd * (dz.x * w2.x - xh.x * mean);
+                v[2 * j + 1] = rstd * (dz.y * w2.y - xh.y * mean);
+                if constexpr (!kAfter && kStreams > 2) {
+                    const float2 a2 = add.pair(j);
+                    v[2 * j] += a2.x;
+                    v[2 * j + 1] += a2.y;
                 }
             }
             store8(a.dx + base + c * 8, pack8(v));
             if (kAfter) store8(a.dres + base + c * 8, pack8(r));
         }
+        if (++slot == ring.kDepth) slot = 0;
     }
     float *p = a.part + int64_t(blockIdx.x) * (channel ? 2 : 1) * a.H;
 #pragma unroll
@@ -306,44 +370,58 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(const NormArgs a) {
         if (c >= nvec) continue;
         reinterpret_cast<float4 *>(p + c * 8)[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
         reinterpret_cast<float4 *>(p + c * 8)[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
-        if (channel) {
-            reinterpret_cast<float4 *>(p + a.H + c * 8)[0] = make_float4(dg[i][0], dg[i][1], dg[i][2], dg[i][3]);
-            reinterpret_cast<float4 *>(p + a.H + c * 8)[1] = make_float4(dg[i][4], dg[i][5], dg[i][6], dg[i][7]);
-        }
+        if constexpr (kAfter && kStreams == 2)
+            if (channel) {
+                reinterpret_cast<float4 *>(p + a.H + c * 8)[0] = make_float4(dg[i][0], dg[i][1], dg[i][2], dg[i][3]);
+                reinterpret_cast<float4 *>(p + a.H + c * 8)[1] = make_float4(dg[i][4], dg[i][5], dg[i][6], dg[i][7]);
+            }
     }
 }
 
-// The blocks' column sums [blocks][cols] added in block order: 32 columns a
-// block, eight warps each taking every eighth partial, their sums added in
-// warp order.  Columns 0 .. H-1 are dw, H .. 2H-1 a per-channel dgate.
-__global__ void __launch_bounds__(256) column_sums_kernel(const float *part, int blocks, int cols, int H, float *dw,
-                                                          float *dg) {
-    __shared__ float s[8][32];
+// The blocks' column sums [blocks][cols] added up in a fixed order: 32 columns
+// a block, 16 warps each taking every 16th partial, their sums added in warp
+// order.  Columns 0 .. H-1 are dw, H .. 2H-1 a per-channel dgate.
+constexpr int kColumnWarps = 16;
+__global__ void __launch_bounds__(kColumnWarps * 32) column_sums_kernel(const float *part, int blocks, int cols, int H,
+                                                                        float *dw, float *dg) {
+    __shared__ float s[kColumnWarps][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c = blockIdx.x * 32 + lane;
     pdl_wait();
     float v = 0.0f;
-    if (c < cols)
-        for (int b = warp; b < blocks; b += 8) v += part[int64_t(b) * cols + c];
+    if (c < cols) {
+#pragma unroll 8
+        for (int b = warp; b < blocks; b += kColumnWarps) v += part[int64_t(b) * cols + c];
+    }
     s[warp][lane] = v;
     __syncthreads();
     if (warp == 0 && c < cols) {
         v = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v += s[i][lane];
+        for (int i = 0; i < kColumnWarps; ++i) v += s[i][lane];
         (c < H ? dw : dg)[c < H ? c : c - H] = v;
     }
 }
 
-// Threads and 8-column pieces per thread of a row of H columns.
+// Threads, 8-column pieces per thread and ring bytes of a row of H columns.
 struct RowShape {
-    int threads, vecs;
+    int threads, vecs, bytes;
 };
-RowShape row_shape(int H, int vecs) {
+RowShape row_shape(int H, int vecs, int streams) {
     const int nvec = H / 8;
-    while (vecs < 16 && (nvec + vecs - 1) / vecs > 1024) vecs *= 2;
+    while ((nvec + vecs - 1) / vecs > (vecs == 1 ? 1024 : 512)) vecs *= 2;  // H <= 16384: at most 4
     const int threads = ((nvec + vecs - 1) / vecs + 31) / 32 * 32;
-    return {threads, vecs};
+    return {threads, vecs, threads * vecs * 16 * streams * norm_depth(streams)};
+}
+// Blocks of a launch: what one SM holds (64 registers a thread) on every SM.
+int row_blocks(int T, const RowShape &s, int most_per_sm) {
+    int per_sm = 1024 / s.threads;
+    const int by_smem = 232448 / (s.bytes + 2048);
+    if (per_sm > by_smem) per_sm = by_smem;
+    if (per_sm > most_per_sm) per_sm = most_per_sm;
+    if (per_sm < 1) per_sm = 1;
+    const int cap = num_sms() * per_sm;
+    return T < cap ? T : cap;
 }
 
 moe_status_t check_norm(int T, int H, float eps) {
@@ -352,38 +430,46 @@ moe_status_t check_norm(int T, int H, float eps) {
     return MOE_OK;
 }
 
-int norm_grid(int T, int threads) {
-    const int64_t cap = int64_t(num_sms()) * (2048 / threads);
-    return int(T < cap ? T : cap);
-}
-// Blocks of the gradients: two per SM (fewer column sums to write and add).
-int norm_backward_grid(int T) {
-    int cap = num_sms() * 2;
-    if (cap > kNormMaxBlocks) cap = kNormMaxBlocks;
-    return T < cap ? T : cap;
+template <int kVecs, bool kAfter, int kStreams>
+cudaError_t launch_norm(const NormArgs &a, const RowShape &s, cudaStream_t stream) {
+    const cudaError_t e =
+        set_max_dynamic_smem(reinterpret_cast<const void *>(norm_kernel<kVecs, kAfter, kStreams>), s.bytes);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(norm_kernel<kVecs, kAfter, kStreams>, dim3(unsigned(row_blocks(a.T, s, 8))),
+                      dim3(unsigned(s.threads)), size_t(s.bytes), stream, a);
 }
 
-template <bool kAfter>
+template <bool kAfter, int kStreams>
 moe_status_t run_norm(const NormArgs &a, cudaStream_t stream) {
-    // a decode batch: one piece per thread, for latency; else four, for bytes in flight
-    const RowShape s = row_shape(a.H, a.T <= num_sms() ? 1 : 4);
-    const dim3 grid(unsigned(norm_grid(a.T, s.threads))), block(unsigned(s.threads));
-    const cudaError_t e = s.vecs == 1   ? launch_pdl(norm_kernel<1, kAfter>, grid, block, 0, stream, a)
-                          : s.vecs == 2 ? launch_pdl(norm_kernel<2, kAfter>, grid, block, 0, stream, a)
-                                        : launch_pdl(norm_kernel<4, kAfter>, grid, block, 0, stream, a);
+    // a decode batch: one piece per thread, for latency; else four, for fewer barriers a byte
+    const RowShape s = row_shape(a.H, a.T <= num_sms() ? 1 : 4, kStreams);
+    const cudaError_t e = s.vecs == 1   ? launch_norm<1, kAfter, kStreams>(a, s, stream)
+                          : s.vecs == 2 ? launch_norm<2, kAfter, kStreams>(a, s, stream)
+                                        : launch_norm<4, kAfter, kStreams>(a, s, stream);
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-template <bool kAfter>
+template <int kVecs, bool kAfter, int kStreams>
+cudaError_t launch_norm_backward(const NormArgs &a, const RowShape &s, int grid, cudaStream_t stream) {
+    const cudaError_t e =
+        set_max_dynamic_smem(reinterpret_cast<const void *>(norm_backward_kernel<kVecs, kAfter, kStreams>), s.bytes);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(norm_backward_kernel<kVecs, kAfter, kStreams>, dim3(unsigned(grid)), dim3(unsigned(s.threads)),
+                      size_t(s.bytes), stream, a);
+}
+
+template <bool kAfter, int kStreams>
 moe_status_t run_norm_backward(const NormArgs &a, float *dw, float *dg, cudaStream_t stream) {
-    const int grid = norm_backward_grid(a.T);
-    const RowShape s = row_shape(a.H, a.T <= num_sms() ? 1 : 2);
-    const dim3 block(unsigned(s.threads));
-    cudaError_t e = s.vecs == 1 ? launch_pdl(norm_backward_kernel<1, kAfter>, dim3(unsigned(grid)), block, 0, stream, a)
-                                : launch_pdl(norm_backward_kernel<2, kAfter>, dim3(unsigned(grid)), block, 0, stream, a);
+    const RowShape s = row_shape(a.H, a.T <= num_sms() ? 1 : 2, kStreams);
+    // few blocks: each leaves column sums to write and add
+    int grid = row_blocks(a.T, s, 3);
+    if (grid > kNormMaxBlocks) grid = kNormMaxBlocks;
+    cudaError_t e = s.vecs == 1   ? launch_norm_backward<1, kAfter, kStreams>(a, s, grid, stream)
+                    : s.vecs == 2 ? launch_norm_backward<2, kAfter, kStreams>(a, s, grid, stream)
+                                  : launch_norm_backward<4, kAfter, kStreams>(a, s, grid, stream);
     if (e == cudaSuccess) {
         const int cols = a.H * (kAfter && a.gate_kind == MOE_GATE_CHANNEL ? 2 : 1);
-        e = launch_pdl(column_sums_kernel, dim3(unsigned((cols + 31) / 32)), dim3(256), 0, stream,
+        e = launch_pdl(column_sums_kernel, dim3(unsigned((cols + 31) / 32)), dim3(kColumnWarps * 32), 0, stream,
                        static_cast<const float *>(a.part), grid, cols, a.H, dw, dg);
     }
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
@@ -420,7 +506,7 @@ moe_status_t moe_norm_before(const void *x_bf16, const void *weight_bf16, int T,
     a.T = T;
     a.H = H;
     a.eps = eps;
-    return run_norm<false>(a, reinterpret_cast<cudaStream_t>(stream));
+    return run_norm<false, 1>(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 moe_status_t moe_norm_after(const void *x_bf16, const void *residual_bf16, const void *weight_bf16,
@@ -448,7 +534,8 @@ moe_status_t moe_norm_after(const void *x_bf16, const void *residual_bf16, const
     a.H = H;
     a.eps = eps;
     a.alpha = residual_scale;
-    return run_norm<true>(a, reinterpret_cast<cudaStream_t>(stream));
+    return gate_kind == MOE_GATE_FULL ? run_norm<true, 3>(a, reinterpret_cast<cudaStream_t>(stream))
+                                      : run_norm<true, 2>(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 moe_status_t moe_norm_workspace_bytes(int T_max, int H, size_t *bytes) {
@@ -486,7 +573,8 @@ moe_status_t moe_norm_before_backward(const void *dy_bf16, const void *x_bf16, c
     a.H = H;
     a.dx = static_cast<__nv_bfloat16 *>(dx_bf16);
     a.part = static_cast<float *>(workspace);
-    return run_norm_backward<false>(a, dweight, nullptr, st);
+    return a.dres_in ? run_norm_backward<false, 3>(a, dweight, nullptr, st)
+                     : run_norm_backward<false, 2>(a, dweight, nullptr, st);
 }
 
 moe_status_t moe_norm_after_backward(const void *dout_bf16, const void *x_bf16, const void *weight_bf16,
@@ -531,8 +619,9 @@ moe_status_t moe_norm_after_backward(const void *dout_bf16, const void *x_bf16, 
     a.dres = static_cast<__nv_bfloat16 *>(dresidual_bf16);
     a.dgate = gate_kind == MOE_GATE_CHANNEL ? nullptr : dgate;
     a.part = static_cast<float *>(workspace);
-    return run_norm_backward<true>(a, dweight, gate_kind == MOE_GATE_CHANNEL ? static_cast<float *>(dgate) : nullptr,
-                                   st);
+    if (gate_kind == MOE_GATE_FULL) return run_norm_backward<true, 3>(a, dweight, nullptr, st);
+    return run_norm_backward<true, 2>(a, dweight, gate_kind == MOE_GATE_CHANNEL ? static_cast<float *>(dgate) : nullptr,
+                                      st);
 }
 
 }  // extern "C"

@@ -37,7 +37,7 @@ def test_matvec(moelib):
         return moelib.moe_fp4_matvec(x, w, sf, y, T, N, K, fmt, None)
     assert call(T=0, x=None, w=None, sf=None, y=None) == 0
     for kw in (dict(T=-1), dict(N=0), dict(K=0), dict(fmt=2), dict(fmt=-1), dict(x=None), dict(w=None), dict(sf=None),
-               dict(y=None), dict(x=q2), dict(w=q2), dict(y=odd)):
+               dict(y=None), dict(x=q2), dict(w=q2), dict(sf=q2), dict(y=odd)):
         assert call(**kw) == INVALID, kw
     for kw in (dict(K=48), dict(K=57376), dict(T=65536)):
         assert call(**kw) == SHAPE, kw
