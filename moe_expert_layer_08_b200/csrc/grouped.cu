@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int boxes_n = kNMn ? (it.cols + 63) / 64 : (it.cols + kRowBox - 1) / kRowBox;
                 const uint32_t bytes = uint32_t(tiles_m * kTileRows * 128 + boxes_n * (kNMn ? 64 : kRowBox) * 128);
                 for (int kb = 0; kb < it.kblocks; ++kb) {
-                    if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, err, 31)) {
+                    if (!mbar_wait_cycles(&empty[stage], phase ^ 1u, abort_flag, err, 31)) {
                         ok = false;
                         break;
                     }
@@ -321,13 +321,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int buf = li % C::kBufs;
                 const uint32_t use = uint32_t(li / C::kBufs) & 1u;
                 if (valid) {
-                    if (!mbar_wait(&tmem_empty[2 * a + buf], use ^ 1u, abort_flag, err, 32)) break;
+                    if (!mbar_wait_cycles(&tmem_empty[2 * a + buf], use ^ 1u, abort_flag, err, 32)) break;
                     tc_fence_after();
                     ++li;
                 }
                 const uint32_t acc = tmem + uint32_t((buf * 2 + a) * kN);
                 for (int kb = 0; kb < it.kblocks; ++kb) {
-                    if (!mbar_wait(&full[stage], phase, abort_flag, err, 33)) {
+                    if (!mbar_wait_cycles(&full[stage], phase, abort_flag, err, 33)) {
                         ok = false;
                         break;
                     }
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (kb == it.kblocks - 1) {
                             steps = (it.tail + 15) / 16;
                             if (it.tail % 16) {
-                                if (!mbar_wait(&fixed[stage], (fixed_phase >> stage) & 1u, abort_flag, err, 34)) {
+                                if (!mbar_wait_cycles(&fixed[stage], (fixed_phase >> stage) & 1u, abort_flag, err, 34)) {
                                     ok = false;
                                     break;
                                 }
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int u = blockIdx.x; ok && u < num_items; u += gridDim.x) {
                 const Item it = walk.at(u);
                 for (int kb = 0; kb < it.kblocks; ++kb) {
-                    if (!mbar_wait(&full[stage], phase, abort_flag, err, 35)) {
+                    if (!mbar_wait_cycles(&full[stage], phase, abort_flag, err, 35)) {
                         ok = false;
                         break;
                     }
@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int buf = li % C::kBufs;
             const uint32_t use = uint32_t(li / C::kBufs) & 1u;
             if (have) {
-                if (!mbar_wait(&tmem_full[2 * a + buf], use, abort_flag, err, 36)) break;
+                if (!mbar_wait_cycles(&tmem_full[2 * a + buf], use, abort_flag, err, 36)) break;
                 tc_fence_after();
                 ++li;
             }

@@ -40,6 +40,16 @@ constexpr int kMvMaxK = 57344;
 constexpr int mv_fixed_bytes(int stages) { return kMvTeams * kMvWarps * stages * kMvStageBytes + kMvSumBytes; }
 static_assert(mv_fixed_bytes(2) + (2 * kMvMaxK + 127) / 128 * 128 + 64 <= kMvMaxSmem, "one token of the largest K");
 
+// The E2M1 codes in bits 4j.. and 4j + 16.. of w as fp16 times 2^-14: sign,
+// exponent and mantissa bits in place (E2M1's bits are those of an fp16 number
+// with another exponent bias, subnormals included).  The shifts are products
+// with factors the compiler does not know, which go to the multiply-add pipe:
+// the integer pipe, at half its rate, bounds this kernel.  (The conversion
+// instruction ran at a fraction of that: 39 us at N = 14336, K = 7168; byte
+// permutes 29 us.)
+struct PairFactors {
+    uint32_t mag[3], sign[3];  // 2^(9 - 4j), 2^(12 - 4j)
+};
 struct MatvecArgs {
     const __nv_bfloat16 *x;   // [T, K]
     const uint8_t *w;         // [N, K / 2]
@@ -49,6 +59,7 @@ struct MatvecArgs {
     int tokens;               // tokens of a pass (blockIdx.y), <= kMvTokens
     int slice;                // K elements of a warp's slice, a multiple of 32
     int x_stride;             // bytes of a token in shared memory
+    PairFactors factors;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
@@ -60,21 +71,12 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-// Four E2M1 codes (bits 0..15 of w, the first in bits 0..3) as fp16: codes 0
-// and 2 in `even`, 1 and 3 in `odd`.  Of an E2M1 value fp16 needs the high byte
-// alone, which a byte permute looks up for four codes at once; the permute's
-// sign-replicating mode spreads the four sign bits.  (The conversion instruction
-// runs at a sixteenth of the ALU's rate: 39 us against 14 at N = 14336, K = 7168.)
-// kHigh: the codes in bits 16..31 instead.
-template <bool kHigh>
-__device__ __forceinline__ void e2m1x4_to_half(uint32_t w, uint32_t &even, uint32_t &odd) {
-    const uint32_t mag = __byte_perm(0x3E3C3800u, 0x46444240u, (kHigh ? w >> 16 : w) & 0x7777u);
-    // the signs of the odd codes are the top bits of w's own bytes, those of the
-    // even ones the top bits of the bytes of w shifted left by 4
-    const uint32_t v = mag | (__byte_perm(w, w << 4, kHigh ? 0xBFAEu : 0x9D8Cu) & 0x80808080u);
-    even = __byte_perm(v, 0u, 0x2404u);  // bytes 0 and 2 to the high bytes of the halves
-    odd = v & 0xFF00FF00u;               // bytes 1 and 3 are there
+template <int j>
+__device__ __forceinline__ uint32_t e2m1_pair(uint32_t w, const PairFactors &f) {
+    if constexpr (j == 3) return (w & 0x80008000u) | ((w >> 3) & 0x0E000E00u);
+    else return (w & (0x00070007u << (4 * j))) * f.mag[j] + (w & (0x00080008u << (4 * j))) * f.sign[j];
 }
+
 // d = a b + c: c is zero for the first step of a group
 __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                             uint32_t b0, uint32_t b1, const float (&c)[4]) {
@@ -85,7 +87,7 @@ __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
-// 2^(b - 127) for a UE8M0 byte b <= 254 (a subnormal for b = 0).
+// 2^(b - 127) for a UE8M0 byte b <= 254 (a subnormal for b = 0), infinity for 255.
 __device__ __forceinline__ float ue8m0_value(uint32_t b) { return __uint_as_float(max(b << 23, 0x00400000u)); }
 // 2^-8 times the value of a UE4M3 byte below 0x7F (bit 7 is not read): its bits
 // are those of an fp16 number with an exponent bias of 15 instead of 7.
@@ -177,23 +179,20 @@ __global__ void __launch_bounds__(kMvTeams * kMvWarps * 32, 1) fp4_matvec_kernel
         // 2^shift brings amax into [2^14, 2^15); both factors are normal numbers
         const int shift = min(max(14 - (int(__float_as_uint(amax) >> 23) - 127), -113), 126);
         const float mul = amax > 0.0f ? __uint_as_float(uint32_t(127 + shift) << 23) : 1.0f;
-        // (and 2^8 for the UE4M3 scales' exponent bias)
-        const float inv = amax > 0.0f ? __uint_as_float(uint32_t(127 - shift) << 23) : 1.0f;
-        if (lane == 0) unscales[warp * kMvTokens + j] = kNv ? 256.0f * inv : inv;
+        if (lane == 0) unscales[warp * kMvTokens + j] = amax > 0.0f ? __uint_as_float(uint32_t(127 - shift) << 23) : 1.0f;
         if ((j & 1) == team)
             for (int k = k_lo + lane * 8; k < k_hi; k += 256) {
                 const uint4 u = *reinterpret_cast<const uint4 *>(xr + k);
                 const uint32_t v[4] = {u.x, u.y, u.z, u.w};
-                // in the order of the decoded weights: elements 0 and 2, 1 and 3, 4 and 6, 5 and 7
+                // in the order of the decoded weights: NVFP4 elements 0 and 2, 1 and 3, 4
+                // and 6, 5 and 7, MX elements 0 and 4, 1 and 5, 2 and 6, 3 and 7
                 uint32_t h[4];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const __half2 even = __floats2half2_rn(__uint_as_float(v[2 * i] << 16) * mul,
-                                                           __uint_as_float(v[2 * i + 1] << 16) * mul);
-                    const __half2 odd = __floats2half2_rn(__uint_as_float(v[2 * i] & 0xFFFF0000u) * mul,
-                                                          __uint_as_float(v[2 * i + 1] & 0xFFFF0000u) * mul);
-                    h[2 * i] = *reinterpret_cast<const uint32_t *>(&even);
-                    h[2 * i + 1] = *reinterpret_cast<const uint32_t *>(&odd);
+                for (int i = 0; i < 4; ++i) {
+                    const int lo = kNv ? (i & 1) + 4 * (i >> 1) : i, hi = lo + (kNv ? 2 : 4);
+                    const auto value = [&](int e) { return __uint_as_float(e & 1 ? v[e >> 1] & 0xFFFF0000u : v[e >> 1] << 16); };
+                    const __half2 p = __floats2half2_rn(value(lo) * mul, value(hi) * mul);
+                    h[i] = *reinterpret_cast<const uint32_t *>(&p);
                 }
                 *reinterpret_cast<uint4 *>(xs + j * args.x_stride + k * 2) = make_uint4(h[0], h[1], h[2], h[3]);
             }
@@ -206,7 +205,10 @@ __global__ void __launch_bounds__(kMvTeams * kMvWarps * 32, 1) fp4_matvec_kernel
     int slot = 0, buf = 0;
     for (int tile = first; tile < tiles; tile += step, buf ^= 1) {
         float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        uint32_t top0 = 0, top1 = 0;  // the largest scale bytes of rows g and g + 8: NaN is the largest
+        // rows g and g + 8 have a NaN scale: the largest byte of UE4M3; for UE8M0, whose
+        // byte 255 becomes an infinity, the sum of zero times the scales
+        uint32_t top0 = 0, top1 = 0;
+        float nan0 = 0.0f, nan1 = 0.0f;
         // where rows g and g + 8 have their first scale inside its 16-byte piece
         const int64_t s0 = (int64_t(tile) * kMvRows + g) * sf_ld + k_lo / kGroup, s1 = s0 + 8 * sf_ld;
         for (int c = 0; c < chunks; ++c) {
@@ -231,8 +233,11 @@ __global__ void __launch_bounds__(kMvTeams * kMvWarps * 32, 1) fp4_matvec_kernel
                         const uint32_t wb =
                             *reinterpret_cast<const uint16_t *>(st + i * 16 + s * 8 + t * 2 + 8 * kMvRowBytes);
                         const uint2 xv = *reinterpret_cast<const uint2 *>(xk + (i * 32 + s * 16 + t * 4) * 2);
-                        e2m1x4_to_half<false>(wa, a[0], a[2]);
-                        e2m1x4_to_half<false>(wb, a[1], a[3]);
+                        const uint32_t pa = __byte_perm(wa, 0u, 0x4140u), pb = __byte_perm(wb, 0u, 0x4140u);
+                        a[0] = e2m1_pair<0>(pa, args.factors);
+                        a[1] = e2m1_pair<0>(pb, args.factors);
+                        a[2] = e2m1_pair<1>(pa, args.factors);
+                        a[3] = e2m1_pair<1>(pb, args.factors);
                         mma_16x8x16(d, a[0], a[1], a[2], a[3], xv.x, xv.y, zero);
                         const uint32_t b0 = sc0[2 * i + s] & 0x7Fu, b1 = sc1[2 * i + s] & 0x7Fu;
                         top0 = max(top0, b0);
@@ -244,16 +249,20 @@ __global__ void __launch_bounds__(kMvTeams * kMvWarps * 32, 1) fp4_matvec_kernel
                     const uint32_t wa = *reinterpret_cast<const uint32_t *>(st + i * 16 + t * 4);
                     const uint32_t wb = *reinterpret_cast<const uint32_t *>(st + i * 16 + t * 4 + 8 * kMvRowBytes);
                     const uint4 xv = *reinterpret_cast<const uint4 *>(xk + (i * 32 + t * 8) * 2);
-                    e2m1x4_to_half<false>(wa, a[0], a[2]);
-                    e2m1x4_to_half<false>(wb, a[1], a[3]);
+                    a[0] = e2m1_pair<0>(wa, args.factors);
+                    a[1] = e2m1_pair<0>(wb, args.factors);
+                    a[2] = e2m1_pair<1>(wa, args.factors);
+                    a[3] = e2m1_pair<1>(wb, args.factors);
                     mma_16x8x16(d, a[0], a[1], a[2], a[3], xv.x, xv.y, zero);
-                    e2m1x4_to_half<true>(wa, a[0], a[2]);
-                    e2m1x4_to_half<true>(wb, a[1], a[3]);
+                    a[0] = e2m1_pair<2>(wa, args.factors);
+                    a[1] = e2m1_pair<2>(wb, args.factors);
+                    a[2] = e2m1_pair<3>(wa, args.factors);
+                    a[3] = e2m1_pair<3>(wb, args.factors);
                     mma_16x8x16(d, a[0], a[1], a[2], a[3], xv.z, xv.w, d);
-                    const uint32_t b0 = sc0[i], b1 = sc1[i];
-                    top0 = max(top0, b0);
-                    top1 = max(top1, b1);
-                    add_group(acc, d, ue8m0_value(b0), ue8m0_value(b1));
+                    const float f0 = ue8m0_value(sc0[i]), f1 = ue8m0_value(sc1[i]);
+                    nan0 = fmaf(f0, 0.0f, nan0);
+                    nan1 = fmaf(f1, 0.0f, nan1);
+                    add_group(acc, d, f0, f1);
                 }
             };
             const int blocks = min(kMvChunk, k_hi - k_lo - c * kMvChunk) / 32;
@@ -266,15 +275,18 @@ __global__ void __launch_bounds__(kMvTeams * kMvWarps * 32, 1) fp4_matvec_kernel
             }
             if (++slot == kStages) slot = 0;
         }
-        constexpr uint32_t kNanScale = kNv ? 0x7Fu : 255u;
-        if (top0 == kNanScale) acc[0] = acc[1] = __uint_as_float(0x7FC00000u);
-        if (top1 == kNanScale) acc[2] = acc[3] = __uint_as_float(0x7FC00000u);
+        if (kNv) {
+            nan0 = top0 == 0x7Fu ? __uint_as_float(0x7FC00000u) : 0.0f;
+            nan1 = top1 == 0x7Fu ? __uint_as_float(0x7FC00000u) : 0.0f;
+        }
+        // 2^14 for the codes, 2^8 for the UE4M3 scales' exponent bias
+        constexpr float kBack = kNv ? 0x1p22f : 0x1p14f;
         // rows g and g + 8, tokens 2t and 2t + 1 of this slice
         float *mine = sums + (buf * kMvWarps + warp) * kMvRows * kMvTokens;
-        mine[g * kMvTokens + 2 * t] = acc[0] * unscale[0];
-        mine[g * kMvTokens + 2 * t + 1] = acc[1] * unscale[1];
-        mine[(g + 8) * kMvTokens + 2 * t] = acc[2] * unscale[0];
-        mine[(g + 8) * kMvTokens + 2 * t + 1] = acc[3] * unscale[1];
+        mine[g * kMvTokens + 2 * t] = (acc[0] * kBack + nan0) * unscale[0];
+        mine[g * kMvTokens + 2 * t + 1] = (acc[1] * kBack + nan0) * unscale[1];
+        mine[(g + 8) * kMvTokens + 2 * t] = (acc[2] * kBack + nan1) * unscale[0];
+        mine[(g + 8) * kMvTokens + 2 * t + 1] = (acc[3] * kBack + nan1) * unscale[1];
         asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(kMvWarps * 32) : "memory");
         const int id = warp * 32 + lane;
         if (id < kMvRows * ntok) {
@@ -323,6 +335,7 @@ extern "C" moe_status_t moe_fp4_matvec(const void *x_bf16, const void *w_fp4, co
     a.T = T;
     a.N = N;
     a.K = K;
+    a.factors = {{512, 32, 2}, {4096, 256, 16}};
     // the tokens of a quarter-warp's 16-byte reads are 64 bytes apart modulo 128
     a.x_stride = (2 * K + 127) / 128 * 128 + 64;
     const auto fits = [&](int stages) { return (kMvMaxSmem - mv_fixed_bytes(stages)) / a.x_stride; };

@@ -229,6 +229,31 @@ static __device__ __noinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, vo
     }
 }
 
+// The same with the limit counted in SM cycles (kWaitTimeoutCycles, about two
+// seconds): reading the global timer takes longer than a pipeline stage of the
+// kernels that wait this way.
+constexpr long long kWaitTimeoutCycles = 3800000000ll;
+static __device__ __noinline__ bool mbar_wait_cycles_slow(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                                          int *err_word, int where) {
+    const long long t0 = clock64();
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (*abort) return false;
+        if (clock64() - t0 > kWaitTimeoutCycles) {
+            *abort = 1;
+            atomicOr(err_word + kHdrError, kDevErrTimeout);
+            atomicExch(err_word + kHdrTimeoutWhere, where);
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool mbar_wait_cycles(uint64_t *bar, uint32_t parity, volatile int *abort, int *err_word,
+                                                 int where) {
+    return mbar_try_wait(bar, parity) || mbar_wait_cycles_slow(bar, parity, abort, err_word, where);
+}
+
 // ---------------------------------------------------------------- programmatic dependent launch
 // Block until the preceding kernel on the stream has completed and its memory
 // is visible (no-op when the kernel was not launched as a dependent).
