@@ -33,24 +33,31 @@ constexpr int kStrip = 256;    // output features of an item: two 128-row MMA ti
 constexpr int kBlockK = 64;    // contraction elements of a pipeline stage (one 128-byte swizzled row)
 constexpr int kRowBox = 32;    // rows of one TMA box of a K-major N side
 constexpr int kChunkBlock = 16;  // row chunks that share a strip's weights before the next strip
-constexpr int kThreads = 384;  // warps: 0 loads, 1 and 2 issue, 3 zeroes tails, 4-7 and 8-11 drain tiles 0 and 1
+constexpr int kMaxSmem = 232448;
+// warps: 0 loads, 1 and 2 issue, 3 zeroes tails; 4-7, 8-11, 12-15, 16-19 drain tiles
+// 0, 1, 0, 1, the first two every even block of 32 columns, the others the odd ones
+constexpr int kEpiWarps = 16;
+constexpr int kThreads = 32 * (4 + kEpiWarps);
 
-// kN: columns of the N side an item may have. 32 for decode loads (a stage is
-// nearly all weights, six of them in flight), 256 otherwise (64 bytes of
-// operands from L2 per MMA cycle instead of 96 with 128).
+// kN: columns of the N side an item may have.  Fewer columns leave room for more
+// stages of weights in flight; more columns cost fewer operand bytes per MMA.
 template <int kN>
 struct GroupedCfg {
-    static constexpr int kStages = kN == 32 ? 6 : 3;
     static constexpr int kABytes = kStrip * kBlockK * 2;  // 32 KB, both tiles
     static constexpr int kBBytes = kN * kBlockK * 2;
     static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr int kBufs = kN == 32 ? 2 : 1;        // accumulator buffers of a tile
-    static constexpr int kTmemCols = 2 * kBufs * kN;
+    static constexpr int kBufs = kN <= 64 ? 2 : 1;        // accumulator buffers of a tile
+    static constexpr int kTmemCols = kN == 32 ? 128 : kN == 64 ? 256 : 512;
     static constexpr int kMisc = 512;
-    static constexpr int kOffsetsBytes = 2 * (kMaxExperts + 1) * 4;
-    static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kMisc + kOffsetsBytes;
-    static_assert(kSmemBytes <= 232448, "shared memory budget");
-    static_assert(kTmemCols >= 32 && kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM allocation");
+    static constexpr int kMaxStages = 6;
+    static constexpr int kStageOutBytes = kEpiWarps * 16 * 64;    // per epilogue warp, 16 rows x 32 features on their way out
+    // barriers, the results' way out and the group table beside the stages
+    static constexpr int fixed_bytes(int E) { return 1024 + kStageOutBytes + kMisc + 8 * (E + 1); }
+    static constexpr int stages(int E) {
+        return (kMaxSmem - fixed_bytes(E)) / kStageBytes < kMaxStages ? (kMaxSmem - fixed_bytes(E)) / kStageBytes : kMaxStages;
+    }
+    static_assert(stages(kMaxExperts) >= 3, "shared memory budget");
+    static_assert(2 * kBufs * kN <= kTmemCols, "TMEM allocation");
 };
 
 struct GroupedArgs {
@@ -62,6 +69,8 @@ struct GroupedArgs {
     int C;                // contraction length of the product and input gradient
     int K;                // weight gradient: columns of dW
     int zero_unused;      // product, input gradient: write zeros to the rows of no expert
+    int stages;           // of the operand ring
+    int wide;             // weight gradient: rows of dW are aligned to 32 bytes
 };
 
 // Shared-memory matrix descriptor, MN-major, 128-byte swizzle: boxes of 64 MN
@@ -75,6 +84,23 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr) {
     d |= uint64_t(1) << 46;                 // descriptor version (sm_100)
     d |= uint64_t(2) << 61;                 // SWIZZLE_128B
     return d;
+}
+
+// 32 bytes in one store: a whole sector (32-byte aligned).
+__device__ __forceinline__ void st_global_32(void *p, const uint32_t *v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// 32 lanes x 16 columns of 32-bit words.
+__device__ __forceinline__ void tmem_ld_32x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
 }
 
 // One step of a warp's inclusive maximum / sum scans.
@@ -129,15 +155,17 @@ struct Walker {
             it.e = e;
             const int l = u - item_of[e];
             const int r0 = row_of[e], rows = row_of[e + 1] - r0;
+            // as few chunks as hold the rows, of equal size up to the MMA's 16
             const int nch = (rows + kN - 1) / kN;
+            const int size = ((rows + nch - 1) / nch + 15) / 16 * 16;
             // blocks of kChunkBlock row chunks; inside one, strip by strip over its chunks
             const int b = l / (kChunkBlock * strips);
             const int rem = l - b * kChunkBlock * strips;
             const int width = min(kChunkBlock, nch - b * kChunkBlock);
             const int c = b * kChunkBlock + rem % width;
             it.d0 = (rem / width) * kStrip;
-            it.n0 = r0 + c * kN;
-            it.cols = min(kN, rows - c * kN);
+            it.n0 = r0 + c * size;
+            it.cols = max(min(size, rows - c * size), 0);
             it.kblocks = kb_const;
             it.tail = kBlockK;
         }
@@ -145,17 +173,23 @@ struct Walker {
     }
 };
 
+// A bounded wait of a whole warp: true for all of its lanes or for none.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int *err, int where) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait_cycles(bar, parity, abort, err, where));
+}
+
 template <int kMode, int kN>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tmap_m, const __grid_constant__ CUtensorMap tmap_n,
                    const GroupedArgs args) {
     using C = GroupedCfg<kN>;
-    constexpr int kStages = C::kStages;
+    const int kStages = args.stages;
     constexpr bool kMMn = kMode != kProduct;         // M side MN-major
     constexpr bool kNMn = kMode == kGradWeight;      // N side MN-major
     extern __shared__ uint8_t smem_raw[];
     uint8_t *tiles = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *full = reinterpret_cast<uint64_t *>(tiles + kStages * C::kStageBytes);
+    uint8_t *stage_out = tiles + kStages * C::kStageBytes;
+    uint64_t *full = reinterpret_cast<uint64_t *>(stage_out + C::kStageOutBytes);
     uint64_t *empty = full + kStages;
     uint64_t *fixed = empty + kStages;           // weight gradient: tail rows of the stage zeroed
     uint64_t *tmem_full = fixed + kStages;       // [tile][buf]
@@ -164,8 +198,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(mma_done + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     int *row_of = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(full) + C::kMisc);
-    int *item_of = row_of + kMaxExperts + 1;
-    static_assert((3 * kStages + 10) * 8 + 8 <= C::kMisc, "barriers and flags");
+    int *item_of = row_of + args.E + 1;
+    static_assert((3 * C::kMaxStages + 10) * 8 + 8 <= C::kMisc, "barriers and flags");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -176,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int b = 0; b < 4; ++b) {
             mbar_init(&tmem_full[b], 1);
-            mbar_init(&tmem_empty[b], 4);
+            mbar_init(&tmem_empty[b], kEpiWarps / 2);
         }
         mbar_init(&mma_done[0], 1);
         mbar_init(&mma_done[1], 1);
@@ -248,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ------------------------------------------------------------ loads
             // the M side of product and input gradient is the weights: one expert's
             // are read by the row chunks of a block at about the same time
-            const uint64_t pol_m = kN == 32 ? policy_evict_first() : policy_evict_last();
+            const uint64_t pol_m = kN < 256 ? policy_evict_first() : policy_evict_last();
             const uint64_t pol_n = policy_evict_last();
             int stage = 0;
             uint32_t phase = 0, filled = 0, fill_parity = 0;
@@ -385,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int u = blockIdx.x; ok && u < num_items; u += gridDim.x) {
                 const Item it = walk.at(u);
                 for (int kb = 0; kb < it.kblocks; ++kb) {
-                    if (!mbar_wait_cycles(&full[stage], phase, abort_flag, err, 35)) {
+                    if (!warp_wait(&full[stage], phase, abort_flag, err, 35)) {
                         ok = false;
                         break;
                     }
@@ -412,7 +446,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else {
         // ---------------------------------------------------------------- epilogue of tile a
-        const int a = (warp - 4) >> 2, q = warp & 3;
+        const int a = ((warp - 4) >> 2) & 1, q = warp & 3, odd = (warp - 4) >> 3;
+        uint16_t *out_block = reinterpret_cast<uint16_t *>(stage_out + (warp - 4) * 16 * 64);  // [row][32 features]
         if constexpr (kMode != kGradWeight) {
             if (args.zero_unused) {
                 // rows before the first group and behind the last, 8 columns per store
@@ -420,7 +455,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t head = row_of[0], behind = args.R - row_of[args.E];
                 const int64_t total = (head + behind) * v_row;
                 uint4 *o = reinterpret_cast<uint4 *>(args.out);
-                for (int64_t i = int64_t(blockIdx.x) * 256 + (threadIdx.x - 128); i < total; i += int64_t(gridDim.x) * 256) {
+                constexpr int kWide = 32 * kEpiWarps;
+                for (int64_t i = int64_t(blockIdx.x) * kWide + (threadIdx.x - 128); i < total;
+                     i += int64_t(gridDim.x) * kWide) {
                     const int64_t r = i / v_row;
                     const int64_t row = r < head ? r : r - head + row_of[args.E];
                     o[row * v_row + (i - r * v_row)] = make_uint4(0, 0, 0, 0);
@@ -432,56 +469,95 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Item it = walk.at(u);
             if (a == 1 && !two_tiles(it)) continue;
             const int d = it.d0 + a * kTileRows + q * 32 + lane;
-            const bool have = it.kblocks > 0;  // else a weight gradient without rows: zeros
+            if constexpr (kMode == kGradWeight) {
+                if (it.kblocks == 0) {
+                    // an expert without rows: zeros, a warp row by row
+                    const int pieces = it.cols / 8, rows = min(kTileRows, args.D - it.d0 - a * kTileRows);
+                    for (int r = q + 4 * odd; r < rows; r += 8) {
+                        uint4 *o = reinterpret_cast<uint4 *>(
+                            args.out + (int64_t(it.e) * args.D + it.d0 + a * kTileRows + r) * args.K + it.n0);
+                        if (lane < pieces) o[lane] = make_uint4(0, 0, 0, 0);
+                    }
+                    continue;
+                }
+            }
             const int buf = li % C::kBufs;
             const uint32_t use = uint32_t(li / C::kBufs) & 1u;
-            if (have) {
-                if (!mbar_wait_cycles(&tmem_full[2 * a + buf], use, abort_flag, err, 36)) break;
-                tc_fence_after();
-                ++li;
-            }
+            if (!warp_wait(&tmem_full[2 * a + buf], use, abort_flag, err, 36)) break;
+            tc_fence_after();
+            ++li;
             const uint32_t acc = tmem + (uint32_t(q * 32) << 16) + uint32_t((buf * 2 + a) * kN);
             const int blocks = (it.cols + 31) / 32;
-#pragma unroll 1
-            for (int cb = 0; cb < blocks; ++cb) {
-                uint32_t v[32];
-                if (have) {
-                    tmem_ld_32x32(acc + uint32_t(cb * 32), v);
-                    tmem_ld_wait();
-                    if (cb == blocks - 1) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&tmem_empty[2 * a + buf]);
-                    }
-                } else {
+            // Everything that reads TMEM first, rounded and packed in pairs of columns,
+            // so that the next item's MMAs wait for as little as they can.
+            constexpr int kMine = (kN / 32 + 1) / 2;
+            uint32_t h[kMine][16];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0u;
-                }
-                const int left = it.cols - cb * 32;
-                if (d >= args.D) {
-                    // a lane past the strip's features
-                } else if constexpr (kMode == kGradWeight) {
-                    // thread = row n of dW, 32 consecutive columns k (K % 8 == 0)
-                    __nv_bfloat16 *o = args.out + (int64_t(it.e) * args.D + d) * args.K + it.n0 + cb * 32;
+            for (int m = 0; m < kMine; ++m) {
+                const int cb = 2 * m + odd;
+                if (cb < blocks) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t w[4];
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t v[16];
+                        tmem_ld_32x16(acc + uint32_t(cb * 32 + half * 16), v);
+                        tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(v[8 * j + 2 * i]),
-                                                                           __uint_as_float(v[8 * j + 2 * i + 1]));
-                            w[i] = *reinterpret_cast<const uint32_t *>(&p);
+                        for (int j = 0; j < 8; ++j) {
+                            const __nv_bfloat162 p =
+                                __floats2bfloat162_rn(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+                            h[m][8 * half + j] = *reinterpret_cast<const uint32_t *>(&p);
                         }
-                        if (8 * j < left) reinterpret_cast<uint4 *>(o)[j] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tmem_empty[2 * a + buf]);
+#pragma unroll
+            for (int m = 0; m < kMine; ++m) {
+                const int cb = 2 * m + odd;
+                if (cb >= blocks) break;
+                const int left = it.cols - cb * 32;
+                if constexpr (kMode == kGradWeight) {
+                    // thread = row n of dW, 32 consecutive columns k: whole 32-byte sectors
+                    // where the rows are aligned to them (K % 8 == 0 gives 16 bytes)
+                    if (d < args.D) {
+                        __nv_bfloat16 *o = args.out + (int64_t(it.e) * args.D + d) * args.K + it.n0 + cb * 32;
+                        if (args.wide && left >= 32) {
+                            st_global_32(o, &h[m][0]);
+                            st_global_32(o + 16, &h[m][8]);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                if (8 * j < left)
+                                    reinterpret_cast<uint4 *>(o)[j] =
+                                        make_uint4(h[m][4 * j], h[m][4 * j + 1], h[m][4 * j + 2], h[m][4 * j + 3]);
+                        }
                     }
                 } else {
-                    // thread = output feature d, 32 consecutive rows
-                    __nv_bfloat16 *o = args.out + int64_t(it.n0 + cb * 32) * args.D + d;
+                    // thread = output feature d, 32 consecutive rows: turned around in
+                    // shared memory, then 16 bytes of 8 rows at a time per warp
+                    const int d8 = it.d0 + a * kTileRows + q * 32 + (lane & 3) * 8;  // D % 8 == 0
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (j < left) o[int64_t(j) * args.D] = __float2bfloat16_rn(__uint_as_float(v[j]));
+                    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const uint32_t pair = h[m][8 * half + j];
+                            out_block[(2 * j) * 32 + lane] = static_cast<uint16_t>(pair);
+                            out_block[(2 * j + 1) * 32 + lane] = static_cast<uint16_t>(pair >> 16);
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int r = i * 8 + (lane >> 2);
+                            const uint4 piece = *reinterpret_cast<const uint4 *>(out_block + r * 32 + (lane & 3) * 8);
+                            if (16 * half + r < left && d8 < args.D)
+                                *reinterpret_cast<uint4 *>(args.out + int64_t(it.n0 + cb * 32 + 16 * half + r) * args.D +
+                                                           d8) = piece;
+                        }
+                        __syncwarp();
+                    }
                 }
-                __syncwarp();
             }
         }
     }
@@ -492,16 +568,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int kMode, int kN>
-cudaError_t launch_grouped(const CUtensorMap &tmap_m, const CUtensorMap &tmap_n, const GroupedArgs &a, int64_t items,
+cudaError_t launch_grouped(const CUtensorMap &tmap_m, const CUtensorMap &tmap_n, GroupedArgs a, int64_t items,
                            cudaStream_t stream) {
     using C = GroupedCfg<kN>;
-    const cudaError_t e =
-        set_max_dynamic_smem(reinterpret_cast<const void *>(grouped_kernel<kMode, kN>), C::kSmemBytes);
+    a.stages = C::stages(a.E);
+    const cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(grouped_kernel<kMode, kN>), kMaxSmem);
     if (e != cudaSuccess) return e;
     const int sms = num_sms();
     const int grid = items < sms ? int(items) : sms;
-    return launch_pdl(grouped_kernel<kMode, kN>, dim3(unsigned(grid)), dim3(kThreads), C::kSmemBytes, stream, tmap_m,
-                      tmap_n, a);
+    return launch_pdl(grouped_kernel<kMode, kN>, dim3(unsigned(grid)), dim3(kThreads),
+                      size_t(C::fixed_bytes(a.E) + a.stages * C::kStageBytes), stream, tmap_m, tmap_n, a);
+}
+
+template <int kMode>
+cudaError_t launch_rows(int kn, const CUtensorMap &tm, const CUtensorMap &tn, const GroupedArgs &a, int64_t items,
+                        cudaStream_t stream) {
+    return kn == 32    ? launch_grouped<kMode, 32>(tm, tn, a, items, stream)
+           : kn == 64  ? launch_grouped<kMode, 64>(tm, tn, a, items, stream)
+           : kn == 160 ? launch_grouped<kMode, 160>(tm, tn, a, items, stream)
+                       : launch_grouped<kMode, 256>(tm, tn, a, items, stream);
 }
 
 moe_status_t check_grouped(int R, int E, int N, int K) {
@@ -537,9 +622,10 @@ moe_status_t run_rows(bool grad, const void *rows, const void *w, const int32_t 
     a.C = grad ? N : K;
     a.K = K;
     a.zero_unused = zero_unused;
-    // up to 8 rows per expert on average: 32-row chunks, the rule of the routed layer
-    const bool small = R <= int64_t(8) * E;
-    const int kn = small ? 32 : 256;
+    // columns of an item by the mean load: about the mean and three deviations of
+    // a uniform routing, so that most experts' weights are read by one item
+    const int64_t mean = R / E;
+    const int kn = mean <= 16 ? 32 : mean <= 40 ? 64 : mean <= 136 ? 160 : 256;
     CUtensorMap tm, tn;
     if (!encode_bf16_3d(&tm, w, uint64_t(K), uint64_t(N), uint64_t(E), grad ? kBlockK : kTileRows) ||
         !encode_bf16_rows(&tn, rows, uint64_t(a.C), uint64_t(R), kRowBox))
@@ -547,13 +633,8 @@ moe_status_t run_rows(bool grad, const void *rows, const void *w, const int32_t 
     const int64_t chunks = int64_t(R) / kn + (R < E ? R : E);
     const int64_t items = chunks * ((a.D + kStrip - 1) / kStrip);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e;
-    if (grad)
-        e = small ? launch_grouped<kGradInput, 32>(tm, tn, a, items, st)
-                  : launch_grouped<kGradInput, 256>(tm, tn, a, items, st);
-    else
-        e = small ? launch_grouped<kProduct, 32>(tm, tn, a, items, st)
-                  : launch_grouped<kProduct, 256>(tm, tn, a, items, st);
+    const cudaError_t e = grad ? launch_rows<kGradInput>(kn, tm, tn, a, items, st)
+                               : launch_rows<kProduct>(kn, tm, tn, a, items, st);
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -608,6 +689,7 @@ moe_status_t moe_grouped_matmul_grad_weight(const void *dy_bf16, const void *x_b
     a.E = E;
     a.D = N;
     a.K = K;
+    a.wide = K % 16 == 0 && aligned(dw_bf16, 32);
     CUtensorMap tm, tn;
     if (!encode_bf16_rows(&tm, dy_bf16, uint64_t(N), uint64_t(R), kBlockK) ||
         !encode_bf16_rows(&tn, x_bf16, uint64_t(K), uint64_t(R), kBlockK))
