@@ -5,11 +5,13 @@
 //   input gradient   dx[r, k]    = sum_n dy[r, n] W[e, n, k]
 //   weight gradient  dW[e, n, k] = sum_{r of e} dy[r, n] x[r, k]
 // bf16 operands, fp32 sums in TMEM (tcgen05.mma.kind::f16), one rounding to
-// bf16 at the end.  In all three a CTA's work item is a 256-column strip of
-// the output features (two 128-row MMA tiles, the M side) times up to kN
-// columns of the N side: rows of one expert (product, input gradient; N is
-// the row count rounded up to 16, so a ragged group costs what it has and not
-// a full tile) or 256 columns of k (weight gradient).  Operands come by TMA
+// bf16 at the end.  In all three a work item is a strip of the output features
+// (two MMA tiles, the M side) times up to kN columns of the N side: rows of one
+// expert (product, input gradient; N is the row count rounded up to 16, so a
+// ragged group costs what it has and not a full tile) or 256 columns of k
+// (weight gradient).  Large loads run on pairs of CTAs (tcgen05 cta_group::2):
+// a strip of 512 features, each CTA with 256 of them and half of the N side in
+// its shared memory, 48 KB from L2 per 1024 MMA cycles and SM instead of 64.  Operands come by TMA
 // straight from the caller's row-major tensors in whichever major order the
 // contraction finds them:
 //                    M side                     N side
@@ -29,12 +31,12 @@ namespace {
 
 enum GroupedMode { kProduct = 0, kGradInput = 1, kGradWeight = 2 };
 
-constexpr int kStrip = 256;    // output features of an item: two 128-row MMA tiles
+constexpr int kStrip = 256;    // output features of an item per CTA: two 128-row MMA tiles
 constexpr int kBlockK = 64;    // contraction elements of a pipeline stage (one 128-byte swizzled row)
 constexpr int kRowBox = 32;    // rows of one TMA box of a K-major N side
 constexpr int kChunkBlock = 16;  // row chunks that share a strip's weights before the next strip
 constexpr int kMaxSmem = 232448;
-// warps: 0 loads, 1 and 2 issue, 3 zeroes tails; 4-7, 8-11, 12-15, 16-19 drain tiles
+// warps: 0 loads, 1 and 2 issue, 3 zeroes the weight gradient's tails; 4-7, 8-11, 12-15, 16-19 drain tiles
 // 0, 1, 0, 1, the first two every even block of 32 columns, the others the odd ones
 constexpr int kEpiWarps = 16;
 constexpr int kThreads = 32 * (4 + kEpiWarps);
@@ -43,8 +45,11 @@ constexpr int kThreads = 32 * (4 + kEpiWarps);
 // stages of weights in flight; more columns cost fewer operand bytes per MMA.
 template <int kN>
 struct GroupedCfg {
+    static constexpr bool kPair = kN >= 160;
+    static constexpr int kCtas = kPair ? 2 : 1;
     static constexpr int kABytes = kStrip * kBlockK * 2;  // 32 KB, both tiles
-    static constexpr int kBBytes = kN * kBlockK * 2;
+    static constexpr int kBRows = (kN / kCtas + kRowBox - 1) / kRowBox * kRowBox;
+    static constexpr int kBBytes = kBRows * kBlockK * 2;
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr int kBufs = kN <= 64 ? 2 : 1;        // accumulator buffers of a tile
     static constexpr int kTmemCols = kN == 32 ? 128 : kN == 64 ? 256 : 512;
@@ -132,6 +137,7 @@ struct Item {
 // Walks the items of one CTA in ascending order; every role keeps its own.
 template <int kMode, int kN>
 struct Walker {
+    static constexpr int kItemStrip = kStrip * GroupedCfg<kN>::kCtas;
     const int *row_of;   // [E + 1] group starts, ascending
     const int *item_of;  // [E + 1] first item of each expert
     int E, strips, kb_const, K, D;
@@ -144,7 +150,7 @@ struct Walker {
             const int per = strips * kt;
             it.e = u / per;
             const int l = u - it.e * per;
-            it.d0 = (l / kt) * kStrip;
+            it.d0 = (l / kt) * kItemStrip;
             it.n0 = (l % kt) * kN;
             it.cols = min(kN, K - it.n0);
             const int rows = row_of[it.e + 1] - row_of[it.e];
@@ -163,7 +169,7 @@ struct Walker {
             const int rem = l - b * kChunkBlock * strips;
             const int width = min(kChunkBlock, nch - b * kChunkBlock);
             const int c = b * kChunkBlock + rem % width;
-            it.d0 = (rem / width) * kStrip;
+            it.d0 = (rem / width) * kItemStrip;
             it.n0 = r0 + c * size;
             it.cols = max(min(size, rows - c * size), 0);
             it.kblocks = kb_const;
@@ -172,6 +178,96 @@ struct Walker {
         return it;
     }
 };
+
+// ---- CTA pairs
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// Every thread of both CTAs.
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The first CTA's barrier at this CTA's address `bar`.
+__device__ __forceinline__ uint32_t leader_bar(uint64_t *bar) {
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(smem_u32(bar)));
+    return remote;
+}
+// TMA loads (no multicast) into this CTA that complete on a barrier of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map, uint32_t bar, int c0, int c1,
+                                                 uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2,
+                                                 uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+        : "memory");
+}
+// Arrive on the first CTA's barrier at this CTA's address `bar`.
+__device__ __forceinline__ void mbar_arrive_leader(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_bar(bar)) : "memory");
+}
+// mbar_wait_cycles with the acquire of what the other CTA did before it arrived.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort, int *err, int where) {
+    if (!mbar_wait_cycles(bar, parity, abort, err, where)) return false;
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    return true;
+}
+// The pair's D[M = 256, N] (+)= A . B^T: rows 0-127 of A and D are the first
+// CTA's, and so is the first half of B's N; descriptors hold for both CTAs.
+__device__ __forceinline__ void tc_mma_bf16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                 uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrive on the barrier at `bar` in both CTAs when this thread's MMAs complete.
+__device__ __forceinline__ void tc_commit_pair(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+// Arrive on this CTA's barrier alone.
+template <bool kPair>
+__device__ __forceinline__ void tc_commit_own(uint64_t *bar) {
+    if constexpr (kPair)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                     : "memory");
+    else
+        tc_commit(bar);
+}
+template <bool kPair>
+__device__ __forceinline__ void tmem_alloc_for(uint32_t *dst_smem, uint32_t ncols) {
+    if constexpr (kPair) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)), "r"(ncols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        tmem_alloc(dst_smem, ncols);
+        tmem_relinquish();
+    }
+}
+template <bool kPair>
+__device__ __forceinline__ void tmem_dealloc_for(uint32_t taddr, uint32_t ncols) {
+    if constexpr (kPair)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+    else
+        tmem_dealloc(taddr, ncols);
+}
 
 // A bounded wait of a whole warp: true for all of its lanes or for none.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int *err, int where) {
@@ -184,6 +280,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                    const GroupedArgs args) {
     using C = GroupedCfg<kN>;
     const int kStages = args.stages;
+    constexpr bool kPair = C::kPair;
+    constexpr int kCtas = C::kCtas;
+    static_assert(kPair || kMode != kGradWeight, "the weight gradient runs on pairs");
     constexpr bool kMMn = kMode != kProduct;         // M side MN-major
     constexpr bool kNMn = kMode == kGradWeight;      // N side MN-major
     extern __shared__ uint8_t smem_raw[];
@@ -191,26 +290,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *stage_out = tiles + kStages * C::kStageBytes;
     uint64_t *full = reinterpret_cast<uint64_t *>(stage_out + C::kStageOutBytes);
     uint64_t *empty = full + kStages;
-    uint64_t *fixed = empty + kStages;           // weight gradient: tail rows of the stage zeroed
-    uint64_t *tmem_full = fixed + kStages;       // [tile][buf]
+    // weight gradient, a stage whose tail rows are to be zeroed: landed in this CTA;
+    // zeroed in both (the first CTA's). Every other stage completes on `full` (a
+    // pair's on the first CTA's).
+    uint64_t *landed = empty + kStages;
+    uint64_t *zeroed = landed + kStages;
+    uint64_t *tmem_full = zeroed + kStages;       // [tile][buf]
     uint64_t *tmem_empty = tmem_full + 4;        // [tile][buf]
     uint64_t *mma_done = tmem_empty + 4;         // [tile]
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(mma_done + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     int *row_of = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(full) + C::kMisc);
     int *item_of = row_of + args.E + 1;
-    static_assert((3 * C::kMaxStages + 10) * 8 + 8 <= C::kMisc, "barriers and flags");
+    static_assert((4 * C::kMaxStages + 10) * 8 + 8 <= C::kMisc, "barriers and flags");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], kNMn ? 3 : 2);  // both issuers, and the warp that zeroes tails
-            mbar_init(&fixed[s], 1);
+            mbar_init(&empty[s], 2);  // both issuers
+            mbar_init(&landed[s], 1);
+            mbar_init(&zeroed[s], 2);
         }
         for (int b = 0; b < 4; ++b) {
             mbar_init(&tmem_full[b], 1);
-            mbar_init(&tmem_empty[b], kEpiWarps / 2);
+            mbar_init(&tmem_empty[b], kCtas * kEpiWarps / 2);
         }
         mbar_init(&mma_done[0], 1);
         mbar_init(&mma_done[1], 1);
@@ -219,11 +323,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tmap(&tmap_m);
         prefetch_tmap(&tmap_n);
     }
-    if (warp == 1) {
-        tmem_alloc(tmem_holder, C::kTmemCols);
-        tmem_relinquish();
-    }
-    const int strips = (args.D + kStrip - 1) / kStrip;
+    if (warp == 1) tmem_alloc_for<kPair>(tmem_holder, C::kTmemCols);
+    const int rank = kPair ? int(cluster_rank()) : 0;  // blocks 2i and 2i + 1 are a pair
+    const int first = int(blockIdx.x) / kCtas, step = int(gridDim.x) / kCtas;
+    const int strips = (args.D + kStrip * kCtas - 1) / (kStrip * kCtas);
     pdl_wait();
     if (warp == 0) {
         // Group starts: the running maximum of the offsets clamped to [0, R],
@@ -260,7 +363,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     tc_fence_before();
-    __syncthreads();
+    if constexpr (kPair)
+        cluster_barrier();  // and the other CTA's barriers and TMEM are set up
+    else
+        __syncthreads();
     tc_fence_after();
     if (threadIdx.x == 0) pdl_trigger();
     const uint32_t tmem = *tmem_holder;
@@ -275,7 +381,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     walk.D = args.D;
     const int num_items = kMode == kGradWeight ? args.E * strips * ((args.K + kN - 1) / kN) : item_of[args.E];
     int *err = args.hdr;
-    auto two_tiles = [&](const Item &it) { return it.d0 + kTileRows < args.D; };
+    // features of tile a of this CTA: the pair's tile a is its CTAs' 128 rows side by side
+    auto tile_row = [&](const Item &it, int a) { return it.d0 + (kCtas * a + rank) * kTileRows; };
+    auto two_tiles = [&](const Item &it) { return it.d0 + kCtas * kTileRows < args.D; };
+    // stage kb of a weight gradient's item ends inside a 16-row step
+    auto tail_stage = [](const Item &it, int kb) {
+        return kMode == kGradWeight && kb == it.kblocks - 1 && it.tail % 16 != 0;
+    };
+    // this CTA's part of the N side
+    auto part = [&](const Item &it) { return (it.cols + 15) / 16 * 16 / kCtas; };
 
     if (warp == 0) {
         if (lane == 0) {
@@ -287,10 +401,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             int stage = 0;
             uint32_t phase = 0, filled = 0, fill_parity = 0;
             bool ok = true;
-            for (int u = blockIdx.x; ok && u < num_items; u += gridDim.x) {
+            for (int u = first; ok && u < num_items; u += step) {
                 const Item it = walk.at(u);
                 const int tiles_m = two_tiles(it) ? 2 : 1;
-                const int boxes_n = kNMn ? (it.cols + 63) / 64 : (it.cols + kRowBox - 1) / kRowBox;
+                const int n_part = part(it), n0 = it.n0 + rank * n_part;
+                const int boxes_n = kNMn ? (n_part + 63) / 64 : (n_part + kRowBox - 1) / kRowBox;
                 const uint32_t bytes = uint32_t(tiles_m * kTileRows * 128 + boxes_n * (kNMn ? 64 : kRowBox) * 128);
                 for (int kb = 0; kb < it.kblocks; ++kb) {
                     if (!mbar_wait_cycles(&empty[stage], phase ^ 1u, abort_flag, err, 31)) {
@@ -298,28 +413,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     }
                     uint8_t *a = tiles + stage * C::kStageBytes, *b = a + C::kABytes;
-                    mbar_arrive_expect_tx(&full[stage], bytes);
+                    // both CTAs of a pair load the same number of bytes
+                    const bool own = tail_stage(it, kb);
+                    uint64_t *bar = own ? &landed[stage] : &full[stage];
+                    if (own || rank == 0) mbar_arrive_expect_tx(bar, own ? bytes : kCtas * bytes);
+                    const uint32_t signal = kPair && !own ? leader_bar(bar) : smem_u32(bar);
+                    auto load_2d = [&](uint8_t *dst, const CUtensorMap *map, int c0, int c1, uint64_t pol) {
+                        if constexpr (kPair)
+                            tma_load_2d_pair(dst, map, signal, c0, c1, pol);
+                        else
+                            tma_load_2d(dst, map, bar, c0, c1, pol);
+                    };
+                    auto load_3d = [&](uint8_t *dst, const CUtensorMap *map, int c0, int c1, int c2, uint64_t pol) {
+                        if constexpr (kPair)
+                            tma_load_3d_pair(dst, map, signal, c0, c1, c2, pol);
+                        else
+                            tma_load_3d(dst, map, bar, c0, c1, c2, pol);
+                    };
+                    const int k = kb * kBlockK;
                     if constexpr (kMode == kProduct) {
                         for (int t = 0; t < tiles_m; ++t)
-                            tma_load_3d(a + t * kTileRows * 128, &tmap_m, &full[stage], kb * kBlockK,
-                                        it.d0 + t * kTileRows, it.e, pol_m);
+                            load_3d(a + t * kTileRows * 128, &tmap_m, k, tile_row(it, t), it.e, pol_m);
                     } else {
                         for (int t = 0; t < 2 * tiles_m; ++t) {
+                            const int d = tile_row(it, t >> 1) + (t & 1) * 64;
                             if constexpr (kMode == kGradInput)
-                                tma_load_3d(a + t * 64 * 128, &tmap_m, &full[stage], it.d0 + t * 64, kb * kBlockK, it.e,
-                                            pol_m);
+                                load_3d(a + t * 64 * 128, &tmap_m, d, k, it.e, pol_m);
                             else
-                                tma_load_2d(a + t * 64 * 128, &tmap_m, &full[stage], it.d0 + t * 64,
-                                            row_of[it.e] + kb * kBlockK, pol_n);
+                                load_2d(a + t * 64 * 128, &tmap_m, d, row_of[it.e] + k, pol_n);
                         }
                     }
                     for (int t = 0; t < boxes_n; ++t) {
                         if constexpr (kNMn)
-                            tma_load_2d(b + t * 64 * 128, &tmap_n, &full[stage], it.n0 + t * 64,
-                                        row_of[it.e] + kb * kBlockK, pol_n);
+                            load_2d(b + t * 64 * 128, &tmap_n, n0 + t * 64, row_of[it.e] + k, pol_n);
                         else
-                            tma_load_2d(b + t * kRowBox * 128, &tmap_n, &full[stage], kb * kBlockK,
-                                        it.n0 + t * kRowBox, pol_n);
+                            load_2d(b + t * kRowBox * 128, &tmap_n, k, n0 + t * kRowBox, pol_n);
                     }
                     filled |= 1u << stage;
                     fill_parity = (fill_parity & ~(1u << stage)) | (phase << stage);
@@ -329,118 +457,115 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            // every issued copy must have landed before the CTA may exit
-            for (int s = 0; s < kStages; ++s) {
-                if (!(filled >> s & 1u)) continue;
-                const uint32_t par = (fill_parity >> s) & 1u;
-                const unsigned long long t0 = global_timer_ns();
-                while (!mbar_try_wait(&full[s], par) && global_timer_ns() - t0 < kWaitTimeoutNs) {
+            // Every issued copy must have landed before the CTA may exit, and a pair's
+            // last commits must have reached it: both are so once its stages are
+            // consumed.  After a wait that gave up nothing consumes them: a quarter of
+            // a second, in which copies land.
+            for (int s = 0; s < kStages; ++s)
+                if (filled >> s & 1u) mbar_wait_cycles(&empty[s], fill_parity >> s & 1u, abort_flag, err, 37);
+            if (*abort_flag) {
+                const long long t0 = clock64();
+                while (clock64() - t0 < kWaitTimeoutCycles / 8) {
                 }
             }
         }
         __syncwarp();
     } else if (warp == 1 || warp == 2) {
-        if (lane == 0) {
+        if (lane == 0 && rank == 0) {
             // ------------------------------------------------------------ MMA issuer of tile a
             const int a = warp - 1;
+            auto wait = [&](uint64_t *bar, uint32_t parity, int where) {
+                return kPair ? mbar_wait_cluster(bar, parity, abort_flag, err, where)
+                             : mbar_wait_cycles(bar, parity, abort_flag, err, where);
+            };
+            auto commit = [&](uint64_t *bar) {
+                if constexpr (kPair)
+                    tc_commit_pair(bar);
+                else
+                    tc_commit(bar);
+            };
             int stage = 0, li = 0;
-            uint32_t phase = 0, fixed_phase = 0;
+            uint32_t full_uses = 0, zeroed_uses = 0;  // per stage, of each barrier: its phase
             bool ok = true;
-            for (int u = blockIdx.x; ok && u < num_items; u += gridDim.x) {
+            for (int u = first; ok && u < num_items; u += step) {
                 const Item it = walk.at(u);
                 if (it.kblocks == 0) continue;
                 const bool valid = a == 0 || two_tiles(it);
                 const uint32_t n = uint32_t((it.cols + 15) / 16 * 16);
-                const uint32_t idesc = idesc_bf16(n) | (kMMn ? 1u << 15 : 0u) | (kNMn ? 1u << 16 : 0u);
+                const uint32_t idesc = idesc_bf16(n) + (kPair ? (128u >> 4) << 24 : 0u)  // M = 256
+                                       + (kMMn ? 1u << 15 : 0u) + (kNMn ? 1u << 16 : 0u);
                 const int buf = li % C::kBufs;
                 const uint32_t use = uint32_t(li / C::kBufs) & 1u;
                 if (valid) {
-                    if (!mbar_wait_cycles(&tmem_empty[2 * a + buf], use ^ 1u, abort_flag, err, 32)) break;
+                    if (!wait(&tmem_empty[2 * a + buf], use ^ 1u, 32)) break;
                     tc_fence_after();
                     ++li;
                 }
                 const uint32_t acc = tmem + uint32_t((buf * 2 + a) * kN);
                 for (int kb = 0; kb < it.kblocks; ++kb) {
-                    if (!mbar_wait_cycles(&full[stage], phase, abort_flag, err, 33)) {
-                        ok = false;
-                        break;
+                    if (tail_stage(it, kb)) {
+                        ok = wait(&zeroed[stage], zeroed_uses >> stage & 1u, 34);
+                        zeroed_uses ^= 1u << stage;
+                    } else {
+                        ok = mbar_wait_cycles(&full[stage], full_uses >> stage & 1u, abort_flag, err, 33);
+                        full_uses ^= 1u << stage;
                     }
-                    int steps = kBlockK / 16;
-                    if constexpr (kMode == kGradWeight) {
-                        if (kb == it.kblocks - 1) {
-                            steps = (it.tail + 15) / 16;
-                            if (it.tail % 16) {
-                                if (!mbar_wait_cycles(&fixed[stage], (fixed_phase >> stage) & 1u, abort_flag, err, 34)) {
-                                    ok = false;
-                                    break;
-                                }
-                                fixed_phase ^= 1u << stage;
-                            }
-                        }
-                    }
+                    if (!ok) break;
                     tc_fence_after();
                     if (valid) {
+                        const int steps = kMode == kGradWeight && kb == it.kblocks - 1 ? (it.tail + 15) / 16 : kBlockK / 16;
                         const uint32_t st = smem_u32(tiles + stage * C::kStageBytes);
                         const uint32_t sa = st + uint32_t(a * kTileRows * 128), sb = st + C::kABytes;
                         const uint64_t adesc = kMMn ? smem_desc_mn_sw128(sa) : smem_desc_sw128(sa);
                         const uint64_t bdesc = kNMn ? smem_desc_mn_sw128(sb) : smem_desc_sw128(sb);
                         // a step is 16 contraction elements: 32 bytes inside the swizzled
                         // row (K-major) or 16 rows of 128 bytes (MN-major), in 16-byte units
-                        for (int ks = 0; ks < steps; ++ks)
-                            tc_mma_bf16(acc, adesc + uint64_t(ks * (kMMn ? 128 : 2)),
-                                        bdesc + uint64_t(ks * (kNMn ? 128 : 2)), idesc, (kb | ks) ? 1u : 0u);
+                        for (int ks = 0; ks < steps; ++ks) {
+                            const uint64_t ad = adesc + uint64_t(ks * (kMMn ? 128 : 2)), bd = bdesc + uint64_t(ks * (kNMn ? 128 : 2));
+                            if constexpr (kPair)
+                                tc_mma_bf16_pair(acc, ad, bd, idesc, (kb | ks) ? 1u : 0u);
+                            else
+                                tc_mma_bf16(acc, ad, bd, idesc, (kb | ks) ? 1u : 0u);
+                        }
                     }
-                    tc_commit(&empty[stage]);
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                    commit(&empty[stage]);
+                    if (++stage == kStages) stage = 0;
                 }
                 if (!ok) break;
-                if (valid) tc_commit(&tmem_full[2 * a + buf]);
+                if (valid) commit(&tmem_full[2 * a + buf]);
             }
             // all issued MMAs must be finished before TMEM is released
-            tc_commit(&mma_done[a]);
-            const unsigned long long t0 = global_timer_ns();
-            while (!mbar_try_wait(&mma_done[a], 0) && global_timer_ns() - t0 < kWaitTimeoutNs) {
+            tc_commit_own<kPair>(&mma_done[a]);
+            const long long t0 = clock64();
+            while (!mbar_try_wait(&mma_done[a], 0) && clock64() - t0 < kWaitTimeoutCycles) {
             }
         }
         __syncwarp();
     } else if (warp == 3) {
         if constexpr (kMode == kGradWeight) {
             // ------------------------------------------------------------ tail rows
-            // the rows of the next group (or past the tensor) inside the last
-            // 16-row step of an item, zeroed on both sides; a row is 128 bytes in
-            // every box, so the swizzle inside it does not matter.  This warp is a
-            // consumer of every stage, so that it meets each one in its turn.
+            // The rows of the next group (or past the tensor) inside the last 16-row
+            // step of an item, zeroed on both sides; a row is 128 bytes in every box,
+            // so the swizzle inside it does not matter.
             int stage = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int u = blockIdx.x; ok && u < num_items; u += gridDim.x) {
+            uint32_t landed_uses = 0;
+            for (int u = first; u < num_items; u += step) {
                 const Item it = walk.at(u);
-                for (int kb = 0; kb < it.kblocks; ++kb) {
-                    if (!warp_wait(&full[stage], phase, abort_flag, err, 35)) {
-                        ok = false;
-                        break;
-                    }
-                    if (kb == it.kblocks - 1 && it.tail % 16) {
-                        uint8_t *a = tiles + stage * C::kStageBytes + it.tail * 128;
-                        const int per_box = (16 - it.tail % 16) * 8;  // 16-byte pieces
-                        constexpr int kBoxes = C::kStageBytes / (64 * 128);
-                        for (int i = lane; i < kBoxes * per_box; i += 32)
-                            *reinterpret_cast<uint4 *>(a + i / per_box * 64 * 128 + i % per_box * 16) =
-                                make_uint4(0, 0, 0, 0);
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&fixed[stage]);
-                    }
+                if (it.kblocks == 0) continue;
+                const int last = (stage + it.kblocks - 1) % kStages;
+                if (tail_stage(it, it.kblocks - 1)) {
+                    if (!warp_wait(&landed[last], landed_uses >> last & 1u, abort_flag, err, 35)) break;
+                    landed_uses ^= 1u << last;
+                    uint8_t *a = tiles + last * C::kStageBytes + it.tail * 128;
+                    const int per_box = (16 - it.tail % 16) * 8;  // 16-byte pieces
+                    constexpr int kBoxes = C::kStageBytes / (64 * 128);
+                    for (int i = lane; i < kBoxes * per_box; i += 32)
+                        *reinterpret_cast<uint4 *>(a + i / per_box * 64 * 128 + i % per_box * 16) = make_uint4(0, 0, 0, 0);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&empty[stage]);
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                    if (lane == 0) mbar_arrive_leader(&zeroed[last]);
                 }
+                stage = (last + 1) % kStages;
             }
         }
         __syncwarp();
@@ -465,17 +590,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         int li = 0;
-        for (int u = blockIdx.x; u < num_items; u += gridDim.x) {
+        for (int u = first; u < num_items; u += step) {
             const Item it = walk.at(u);
             if (a == 1 && !two_tiles(it)) continue;
-            const int d = it.d0 + a * kTileRows + q * 32 + lane;
+            const int d = tile_row(it, a) + q * 32 + lane;
             if constexpr (kMode == kGradWeight) {
                 if (it.kblocks == 0) {
                     // an expert without rows: zeros, a warp row by row
-                    const int pieces = it.cols / 8, rows = min(kTileRows, args.D - it.d0 - a * kTileRows);
+                    const int pieces = it.cols / 8, rows = min(kTileRows, args.D - tile_row(it, a));
                     for (int r = q + 4 * odd; r < rows; r += 8) {
                         uint4 *o = reinterpret_cast<uint4 *>(
-                            args.out + (int64_t(it.e) * args.D + it.d0 + a * kTileRows + r) * args.K + it.n0);
+                            args.out + (int64_t(it.e) * args.D + tile_row(it, a) + r) * args.K + it.n0);
                         if (lane < pieces) o[lane] = make_uint4(0, 0, 0, 0);
                     }
                     continue;
@@ -512,7 +637,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&tmem_empty[2 * a + buf]);
+            if (lane == 0) {
+                if constexpr (kPair)
+                    mbar_arrive_leader(&tmem_empty[2 * a + buf]);
+                else
+                    mbar_arrive(&tmem_empty[2 * a + buf]);
+            }
 #pragma unroll
             for (int m = 0; m < kMine; ++m) {
                 const int cb = 2 * m + odd;
@@ -537,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     // thread = output feature d, 32 consecutive rows: turned around in
                     // shared memory, then 16 bytes of 8 rows at a time per warp
-                    const int d8 = it.d0 + a * kTileRows + q * 32 + (lane & 3) * 8;  // D % 8 == 0
+                    const int d8 = tile_row(it, a) + q * 32 + (lane & 3) * 8;  // D % 8 == 0
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
 #pragma unroll
@@ -560,11 +690,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
+        __syncwarp();
     }
     tc_fence_before();
-    __syncthreads();
+    if constexpr (kPair)
+        cluster_barrier();  // the other CTA's MMAs, arrivals and commits for this one are over
+    else
+        __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+    if (warp == 1) tmem_dealloc_for<kPair>(tmem, C::kTmemCols);
 }
 
 template <int kMode, int kN>
@@ -574,10 +708,23 @@ cudaError_t launch_grouped(const CUtensorMap &tmap_m, const CUtensorMap &tmap_n,
     a.stages = C::stages(a.E);
     const cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(grouped_kernel<kMode, kN>), kMaxSmem);
     if (e != cudaSuccess) return e;
-    const int sms = num_sms();
-    const int grid = items < sms ? int(items) : sms;
-    return launch_pdl(grouped_kernel<kMode, kN>, dim3(unsigned(grid)), dim3(kThreads),
-                      size_t(C::fixed_bytes(a.E) + a.stages * C::kStageBytes), stream, tmap_m, tmap_n, a);
+    const int64_t groups = num_sms() / C::kCtas;
+    const int grid = int(items < groups ? items : groups) * C::kCtas;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(grid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = size_t(C::fixed_bytes(a.E) + a.stages * C::kStageBytes);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(C::kCtas);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = C::kPair ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, grouped_kernel<kMode, kN>, tmap_m, tmap_n, a);
 }
 
 template <int kMode>
