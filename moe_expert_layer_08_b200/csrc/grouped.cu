@@ -31,38 +31,43 @@ namespace {
 
 enum GroupedMode { kProduct = 0, kGradInput = 1, kGradWeight = 2 };
 
-constexpr int kStrip = 256;    // output features of an item per CTA: two 128-row MMA tiles
 constexpr int kBlockK = 64;    // contraction elements of a pipeline stage (one 128-byte swizzled row)
 constexpr int kRowBox = 32;    // rows of one TMA box of a K-major N side
 constexpr int kChunkBlock = 16;  // row chunks that share a strip's weights before the next strip
 constexpr int kMaxSmem = 232448;
-// warps: 0 loads, 1 and 2 issue, 3 zeroes the weight gradient's tails; 4-7, 8-11, 12-15, 16-19 drain tiles
-// 0, 1, 0, 1, the first two every even block of 32 columns, the others the odd ones
+// warps: 0 loads, 1 and 2 issue, 3 zeroes the weight gradient's tails; 4-19
+// drain the tiles in turn, four warps a block of 32 columns
 constexpr int kEpiWarps = 16;
 constexpr int kThreads = 32 * (4 + kEpiWarps);
 
 // kN: columns of the N side an item may have.  Fewer columns leave room for more
 // stages of weights in flight; more columns cost fewer operand bytes per MMA.
-template <int kN>
+// kTiles: 128-row MMA tiles of a CTA's strip.  With one there is TMEM for two
+// accumulators, so that the next item's MMAs run while the last one's are
+// drained, at 64 operand bytes per MMA cycle and SM instead of 48.
+template <int kMode, int kN, int kTiles>
 struct GroupedCfg {
+    // per epilogue warp, results on their way out: 16 rows x 32 features, or of the
+    // weight gradient 32 rows x 32 columns
+    static constexpr int kStageOutBytes = kEpiWarps * (kMode == kGradWeight ? 32 : 16) * 64;
+    static constexpr int kStrip = kTiles * kTileRows;     // output features of an item per CTA
     static constexpr bool kPair = kN >= 160;
     static constexpr int kCtas = kPair ? 2 : 1;
-    static constexpr int kABytes = kStrip * kBlockK * 2;  // 32 KB, both tiles
+    static constexpr int kABytes = kStrip * kBlockK * 2;  // 16 KB a tile
     static constexpr int kBRows = (kN / kCtas + kRowBox - 1) / kRowBox * kRowBox;
     static constexpr int kBBytes = kBRows * kBlockK * 2;
     static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr int kBufs = kN <= 64 ? 2 : 1;        // accumulator buffers of a tile
-    static constexpr int kTmemCols = kN == 32 ? 128 : kN == 64 ? 256 : 512;
+    static constexpr int kBufs = kTiles * kN <= 256 ? 2 : 1;        // accumulator buffers of a tile
+    static constexpr int kTmemCols = kN == 32 ? 64 * kTiles : kN == 64 ? 128 * kTiles : 512;
     static constexpr int kMisc = 512;
     static constexpr int kMaxStages = 6;
-    static constexpr int kStageOutBytes = kEpiWarps * 16 * 64;    // per epilogue warp, 16 rows x 32 features on their way out
     // barriers, the results' way out and the group table beside the stages
     static constexpr int fixed_bytes(int E) { return 1024 + kStageOutBytes + kMisc + 8 * (E + 1); }
     static constexpr int stages(int E) {
         return (kMaxSmem - fixed_bytes(E)) / kStageBytes < kMaxStages ? (kMaxSmem - fixed_bytes(E)) / kStageBytes : kMaxStages;
     }
     static_assert(stages(kMaxExperts) >= 3, "shared memory budget");
-    static_assert(2 * kBufs * kN <= kTmemCols, "TMEM allocation");
+    static_assert(kTiles * kBufs * kN <= kTmemCols, "TMEM allocation");
 };
 
 struct GroupedArgs {
@@ -75,7 +80,6 @@ struct GroupedArgs {
     int K;                // weight gradient: columns of dW
     int zero_unused;      // product, input gradient: write zeros to the rows of no expert
     int stages;           // of the operand ring
-    int wide;             // weight gradient: rows of dW are aligned to 32 bytes
 };
 
 // Shared-memory matrix descriptor, MN-major, 128-byte swizzle: boxes of 64 MN
@@ -91,12 +95,17 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr) {
     return d;
 }
 
-// 32 bytes in one store: a whole sector (32-byte aligned).
-__device__ __forceinline__ void st_global_32(void *p, const uint32_t *v) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+// TMA store of a box from shared memory (this thread's own bulk group).
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
                  : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
+// This thread's stores have read their shared memory / are complete.
+__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // 32 lanes x 16 columns of 32-bit words.
 __device__ __forceinline__ void tmem_ld_32x16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -135,9 +144,9 @@ struct Item {
 };
 
 // Walks the items of one CTA in ascending order; every role keeps its own.
-template <int kMode, int kN>
+template <int kMode, int kN, int kTiles>
 struct Walker {
-    static constexpr int kItemStrip = kStrip * GroupedCfg<kN>::kCtas;
+    static constexpr int kItemStrip = GroupedCfg<kMode, kN, kTiles>::kStrip * GroupedCfg<kMode, kN, kTiles>::kCtas;
     const int *row_of;   // [E + 1] group starts, ascending
     const int *item_of;  // [E + 1] first item of each expert
     int E, strips, kb_const, K, D;
@@ -217,10 +226,20 @@ __device__ __forceinline__ void mbar_arrive_leader(uint64_t *bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_bar(bar)) : "memory");
 }
 // mbar_wait_cycles with the acquire of what the other CTA did before it arrived.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0u;
+}
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort, int *err, int where) {
-    if (!mbar_wait_cycles(bar, parity, abort, err, where)) return false;
-    asm volatile("fence.acq_rel.cluster;" ::: "memory");
-    return true;
+    return mbar_try_wait_cluster(bar, parity) ||
+           (mbar_wait_cycles_slow(bar, parity, abort, err, where) && mbar_try_wait_cluster(bar, parity));
 }
 // The pair's D[M = 256, N] (+)= A . B^T: rows 0-127 of A and D are the first
 // CTA's, and so is the first half of B's N; descriptors hold for both CTAs.
@@ -274,11 +293,11 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
     return __all_sync(0xFFFFFFFFu, mbar_wait_cycles(bar, parity, abort, err, where));
 }
 
-template <int kMode, int kN>
+template <int kMode, int kN, int kTiles>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tmap_m, const __grid_constant__ CUtensorMap tmap_n,
-                   const GroupedArgs args) {
-    using C = GroupedCfg<kN>;
+                   const __grid_constant__ CUtensorMap tmap_out, const GroupedArgs args) {
+    using C = GroupedCfg<kMode, kN, kTiles>;
     const int kStages = args.stages;
     constexpr bool kPair = C::kPair;
     constexpr int kCtas = C::kCtas;
@@ -308,13 +327,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 2);  // both issuers
+            mbar_init(&empty[s], kTiles);  // the issuers
             mbar_init(&landed[s], 1);
             mbar_init(&zeroed[s], 2);
         }
         for (int b = 0; b < 4; ++b) {
             mbar_init(&tmem_full[b], 1);
-            mbar_init(&tmem_empty[b], kCtas * kEpiWarps / 2);
+            mbar_init(&tmem_empty[b], kCtas * kEpiWarps / kTiles);
         }
         mbar_init(&mma_done[0], 1);
         mbar_init(&mma_done[1], 1);
@@ -326,7 +345,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_alloc_for<kPair>(tmem_holder, C::kTmemCols);
     const int rank = kPair ? int(cluster_rank()) : 0;  // blocks 2i and 2i + 1 are a pair
     const int first = int(blockIdx.x) / kCtas, step = int(gridDim.x) / kCtas;
-    const int strips = (args.D + kStrip * kCtas - 1) / (kStrip * kCtas);
+    constexpr int kItemStrip = C::kStrip * kCtas;
+    const int strips = (args.D + kItemStrip - 1) / kItemStrip;
     pdl_wait();
     if (warp == 0) {
         // Group starts: the running maximum of the offsets clamped to [0, R],
@@ -371,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) pdl_trigger();
     const uint32_t tmem = *tmem_holder;
 
-    Walker<kMode, kN> walk;
+    Walker<kMode, kN, kTiles> walk;
     walk.row_of = row_of;
     walk.item_of = item_of;
     walk.E = args.E;
@@ -383,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int *err = args.hdr;
     // features of tile a of this CTA: the pair's tile a is its CTAs' 128 rows side by side
     auto tile_row = [&](const Item &it, int a) { return it.d0 + (kCtas * a + rank) * kTileRows; };
-    auto two_tiles = [&](const Item &it) { return it.d0 + kCtas * kTileRows < args.D; };
+    auto two_tiles = [&](const Item &it) { return kTiles == 2 && it.d0 + kCtas * kTileRows < args.D; };
     // stage kb of a weight gradient's item ends inside a 16-row step
     auto tail_stage = [](const Item &it, int kb) {
         return kMode == kGradWeight && kb == it.kblocks - 1 && it.tail % 16 != 0;
@@ -471,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp == 1 || warp == 2) {
-        if (lane == 0 && rank == 0) {
+        if (lane == 0 && rank == 0 && warp <= kTiles) {
             // ------------------------------------------------------------ MMA issuer of tile a
             const int a = warp - 1;
             auto wait = [&](uint64_t *bar, uint32_t parity, int where) {
@@ -501,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after();
                     ++li;
                 }
-                const uint32_t acc = tmem + uint32_t((buf * 2 + a) * kN);
+                const uint32_t acc = tmem + uint32_t((buf * kTiles + a) * kN);
                 for (int kb = 0; kb < it.kblocks; ++kb) {
                     if (tail_stage(it, kb)) {
                         ok = wait(&zeroed[stage], zeroed_uses >> stage & 1u, 34);
@@ -557,10 +577,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!warp_wait(&landed[last], landed_uses >> last & 1u, abort_flag, err, 35)) break;
                     landed_uses ^= 1u << last;
                     uint8_t *a = tiles + last * C::kStageBytes + it.tail * 128;
-                    const int per_box = (16 - it.tail % 16) * 8;  // 16-byte pieces
                     constexpr int kBoxes = C::kStageBytes / (64 * 128);
-                    for (int i = lane; i < kBoxes * per_box; i += 32)
-                        *reinterpret_cast<uint4 *>(a + i / per_box * 64 * 128 + i % per_box * 16) = make_uint4(0, 0, 0, 0);
+                    for (int r = lane >> 3; r < 16 - it.tail % 16; r += 4)
+#pragma unroll
+                        for (int box = 0; box < kBoxes; ++box)
+                            *reinterpret_cast<uint4 *>(a + box * 64 * 128 + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) mbar_arrive_leader(&zeroed[last]);
@@ -571,8 +592,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else {
         // ---------------------------------------------------------------- epilogue of tile a
-        const int a = ((warp - 4) >> 2) & 1, q = warp & 3, odd = (warp - 4) >> 3;
-        uint16_t *out_block = reinterpret_cast<uint16_t *>(stage_out + (warp - 4) * 16 * 64);  // [row][32 features]
+        constexpr int kGroups = kEpiWarps / 4 / kTiles;  // warps of a tile's lane quarter: every kGroups-th block of columns
+        const int a = ((warp - 4) >> 2) % kTiles, q = warp & 3, group = ((warp - 4) >> 2) / kTiles;
+        uint16_t *out_block = reinterpret_cast<uint16_t *>(stage_out + (warp - 4) * (C::kStageOutBytes / kEpiWarps));  // [row][32 features]
         if constexpr (kMode != kGradWeight) {
             if (args.zero_unused) {
                 // rows before the first group and behind the last, 8 columns per store
@@ -598,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (it.kblocks == 0) {
                     // an expert without rows: zeros, a warp row by row
                     const int pieces = it.cols / 8, rows = min(kTileRows, args.D - tile_row(it, a));
-                    for (int r = q + 4 * odd; r < rows; r += 8) {
+                    for (int r = q + 4 * group; r < rows; r += 4 * kGroups) {
                         uint4 *o = reinterpret_cast<uint4 *>(
                             args.out + (int64_t(it.e) * args.D + tile_row(it, a) + r) * args.K + it.n0);
                         if (lane < pieces) o[lane] = make_uint4(0, 0, 0, 0);
@@ -611,15 +633,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!warp_wait(&tmem_full[2 * a + buf], use, abort_flag, err, 36)) break;
             tc_fence_after();
             ++li;
-            const uint32_t acc = tmem + (uint32_t(q * 32) << 16) + uint32_t((buf * 2 + a) * kN);
+            const uint32_t acc = tmem + (uint32_t(q * 32) << 16) + uint32_t((buf * kTiles + a) * kN);
             const int blocks = (it.cols + 31) / 32;
             // Everything that reads TMEM first, rounded and packed in pairs of columns,
             // so that the next item's MMAs wait for as little as they can.
-            constexpr int kMine = (kN / 32 + 1) / 2;
+            constexpr int kMine = (kN / 32 + kGroups - 1) / kGroups;
             uint32_t h[kMine][16];
 #pragma unroll
             for (int m = 0; m < kMine; ++m) {
-                const int cb = 2 * m + odd;
+                const int cb = kGroups * m + group;
                 if (cb < blocks) {
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
@@ -645,25 +667,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int m = 0; m < kMine; ++m) {
-                const int cb = 2 * m + odd;
+                const int cb = kGroups * m + group;
                 if (cb >= blocks) break;
                 const int left = it.cols - cb * 32;
                 if constexpr (kMode == kGradWeight) {
-                    // thread = row n of dW, 32 consecutive columns k: whole 32-byte sectors
-                    // where the rows are aligned to them (K % 8 == 0 gives 16 bytes)
-                    if (d < args.D) {
-                        __nv_bfloat16 *o = args.out + (int64_t(it.e) * args.D + d) * args.K + it.n0 + cb * 32;
-                        if (args.wide && left >= 32) {
-                            st_global_32(o, &h[m][0]);
-                            st_global_32(o + 16, &h[m][8]);
-                        } else {
+                    // thread = row n of dW, 32 consecutive columns k: a 32 x 32 box through
+                    // shared memory (64-byte rows, 64-byte swizzle); the map cuts it at the
+                    // last row and column.  (Stores from the registers cost the L1 a cycle
+                    // per row: 933 us instead of 701 for 48 experts of 128 rows, 4096 x 7168.)
+                    if (lane == 0) tma_store_wait_read();
+                    __syncwarp();
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                if (8 * j < left)
-                                    reinterpret_cast<uint4 *>(o)[j] =
-                                        make_uint4(h[m][4 * j], h[m][4 * j + 1], h[m][4 * j + 2], h[m][4 * j + 3]);
-                        }
-                    }
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<uint4 *>(out_block + lane * 32 + ((j ^ ((lane >> 1) & 3)) * 8)) =
+                            make_uint4(h[m][4 * j], h[m][4 * j + 1], h[m][4 * j + 2], h[m][4 * j + 3]);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0 && d < args.D) tma_store_3d(&tmap_out, out_block, it.n0 + cb * 32, d, it.e);
                 } else {
                     // thread = output feature d, 32 consecutive rows: turned around in
                     // shared memory, then 16 bytes of 8 rows at a time per warp
@@ -690,6 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
+        if (kMode == kGradWeight && lane == 0) tma_store_wait_all();
         __syncwarp();
     }
     tc_fence_before();
@@ -701,12 +722,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_dealloc_for<kPair>(tmem, C::kTmemCols);
 }
 
-template <int kMode, int kN>
-cudaError_t launch_grouped(const CUtensorMap &tmap_m, const CUtensorMap &tmap_n, GroupedArgs a, int64_t items,
-                           cudaStream_t stream) {
-    using C = GroupedCfg<kN>;
+template <int kMode, int kN, int kTiles>
+cudaError_t launch_grouped(const CUtensorMap &tmap_m, const CUtensorMap &tmap_n, const CUtensorMap &tmap_out,
+                           GroupedArgs a, int64_t items, cudaStream_t stream) {
+    using C = GroupedCfg<kMode, kN, kTiles>;
     a.stages = C::stages(a.E);
-    const cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(grouped_kernel<kMode, kN>), kMaxSmem);
+    const cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(grouped_kernel<kMode, kN, kTiles>), kMaxSmem);
     if (e != cudaSuccess) return e;
     const int64_t groups = num_sms() / C::kCtas;
     const int grid = int(items < groups ? items : groups) * C::kCtas;
@@ -724,23 +745,23 @@ cudaError_t launch_grouped(const CUtensorMap &tmap_m, const CUtensorMap &tmap_n,
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = C::kPair ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, grouped_kernel<kMode, kN>, tmap_m, tmap_n, a);
+    return cudaLaunchKernelEx(&cfg, grouped_kernel<kMode, kN, kTiles>, tmap_m, tmap_n, tmap_out, a);
 }
 
 template <int kMode>
 cudaError_t launch_rows(int kn, const CUtensorMap &tm, const CUtensorMap &tn, const GroupedArgs &a, int64_t items,
                         cudaStream_t stream) {
-    return kn == 32    ? launch_grouped<kMode, 32>(tm, tn, a, items, stream)
-           : kn == 64  ? launch_grouped<kMode, 64>(tm, tn, a, items, stream)
-           : kn == 160 ? launch_grouped<kMode, 160>(tm, tn, a, items, stream)
-                       : launch_grouped<kMode, 256>(tm, tn, a, items, stream);
+    return kn == 32    ? launch_grouped<kMode, 32, 2>(tm, tn, tm, a, items, stream)
+           : kn == 64  ? launch_grouped<kMode, 64, 2>(tm, tn, tm, a, items, stream)
+           : kn == 160 ? launch_grouped<kMode, 160, 2>(tm, tn, tm, a, items, stream)
+                       : launch_grouped<kMode, 256, 2>(tm, tn, tm, a, items, stream);
 }
 
 moe_status_t check_grouped(int R, int E, int N, int K) {
     if (R < 0 || E <= 0 || N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
     if (E > kMaxExperts || N % 8 || K % 8 || N > kGroupedMaxWidth || K > kGroupedMaxWidth) return MOE_ERR_UNSUPPORTED_SHAPE;
     // every expert's items fit an int: strips <= 512, chunks <= R / 32 + E
-    if ((int64_t(R) / 32 + E) * ((int64_t(N > K ? N : K) + kStrip - 1) / kStrip) > 2000000000ll ||
+    if ((int64_t(R) / 32 + E) * ((int64_t(N > K ? N : K) + kTileRows - 1) / kTileRows) > 2000000000ll ||
         int64_t(E) * ((N + 255) / 256) * ((K + 255) / 256) > 2000000000ll)
         return MOE_ERR_UNSUPPORTED_SHAPE;
     return MOE_OK;
@@ -778,7 +799,7 @@ moe_status_t run_rows(bool grad, const void *rows, const void *w, const int32_t 
         !encode_bf16_rows(&tn, rows, uint64_t(a.C), uint64_t(R), kRowBox))
         return MOE_ERR_CUDA;
     const int64_t chunks = int64_t(R) / kn + (R < E ? R : E);
-    const int64_t items = chunks * ((a.D + kStrip - 1) / kStrip);
+    const int64_t items = chunks * ((a.D + kTileRows - 1) / kTileRows);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t e = grad ? launch_rows<kGradInput>(kn, tm, tn, a, items, st)
                                : launch_rows<kProduct>(kn, tm, tn, a, items, st);
@@ -836,13 +857,13 @@ moe_status_t moe_grouped_matmul_grad_weight(const void *dy_bf16, const void *x_b
     a.E = E;
     a.D = N;
     a.K = K;
-    a.wide = K % 16 == 0 && aligned(dw_bf16, 32);
-    CUtensorMap tm, tn;
+    CUtensorMap tm, tn, to;
     if (!encode_bf16_rows(&tm, dy_bf16, uint64_t(N), uint64_t(R), kBlockK) ||
-        !encode_bf16_rows(&tn, x_bf16, uint64_t(K), uint64_t(R), kBlockK))
+        !encode_bf16_rows(&tn, x_bf16, uint64_t(K), uint64_t(R), kBlockK) ||
+        !encode_bf16_3d(&to, dw_bf16, uint64_t(K), uint64_t(N), uint64_t(E), 32, 32))
         return MOE_ERR_CUDA;
-    const int64_t items = int64_t(E) * ((N + kStrip - 1) / kStrip) * ((K + 255) / 256);
-    const cudaError_t e = launch_grouped<kGradWeight, 256>(tm, tn, a, items, st);
+    const int64_t items = int64_t(E) * ((N + kTileRows - 1) / kTileRows) * ((K + 255) / 256);
+    const cudaError_t e = launch_grouped<kGradWeight, 256, 2>(tm, tn, to, a, items, st);
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

@@ -106,8 +106,10 @@ cudaError_t launch_shared(bool gemm1, const CUtensorMap &tmap_w, const CUtensorM
 // (128 bytes, 128-byte swizzle) x box_rows rows.
 bool encode_bf16_rows(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, int box_rows);
 // The same for the row-major matrices of several experts, [experts][rows][cols]:
-// a box stays inside one expert (rows past it read as zeros).
-bool encode_bf16_3d(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, uint64_t experts, int box_rows);
+// a box stays inside one expert (rows past it read as zeros); box_cols 64
+// (128-byte swizzle) or 32 (64-byte swizzle).
+bool encode_bf16_3d(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, uint64_t experts, int box_rows,
+                    int box_cols = 64);
 
 constexpr int kGroupedMaxWidth = 131072;  // features of a grouped product's operands, at most
 
