@@ -145,15 +145,16 @@ struct NormArgs {
     void *dgate;                    // per token: f32 [T]; per element: bf16 [T, H]
 };
 
-// Rows of the ring: one being worked on, the others on their way.  (A third row
-// of two streams leaves the L1 too little for the weights and the gate: the
-// gradients of 8192 x 7168 took 134 us instead of 114.)
+// Rows of the forward kernels' rings: one being worked on, the others on their
+// way (a block is one of several on its SM).
 constexpr int norm_depth(int streams) { return streams == 1 ? 3 : 2; }
+// The gradients work on two rows at a time up to this width, with as many on
+// their way, and on one with one on its way above.
+constexpr int kNormTwoRowsH = 8192;
 
-// The ring of one thread's pieces: kStreams inputs of a row, norm_depth rows.
-template <int kVecs, int kStreams>
+// The ring of one thread's pieces: kStreams inputs of a row, kDepth rows.
+template <int kVecs, int kStreams, int kDepth>
 struct RowRing {
-    static constexpr int kDepth = norm_depth(kStreams);
     uint32_t mine;             // this thread's first piece (shared memory), and the bytes to its next
     uint32_t piece;
     const __nv_bfloat16 *src[kStreams];  // this thread's first columns of the next row to bring
@@ -161,6 +162,7 @@ struct RowRing {
     int T, row, row_step, slot, first, apart, nvec;
 
     // `threads` take a row, this one from column 8 * first on
+    template <int kAhead>
     __device__ __forceinline__ void start(uint4 *smem, int first_, int threads, int H, int T_, int row_, int row_step_) {
         mine = smem_u32(smem + threadIdx.x);
         piece = blockDim.x * 16u;
@@ -175,7 +177,7 @@ struct RowRing {
 #pragma unroll
         for (int s = 0; s < kStreams; ++s) src[s] += int64_t(row_) * H + first_ * 8;
 #pragma unroll
-        for (int d = 0; d < kDepth - 1; ++d) next();
+        for (int d = 0; d < kAhead; ++d) next();
     }
     __device__ __forceinline__ bool has(int i) const { return first + i * apart < nvec; }
     __device__ __forceinline__ void next() {
@@ -196,9 +198,10 @@ struct RowRing {
         row += row_step;
         if (++slot == kDepth) slot = 0;
     }
-    // All but the newest kDepth - 1 rows have landed (for this thread).
+    // All but the newest kLeft rows have landed (for this thread).
+    template <int kLeft>
     __device__ __forceinline__ void wait() const {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+        asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
     }
     __device__ __forceinline__ Bf16x8 get(int slot_, int stream, int i) const {
         Bf16x8 v;
@@ -210,27 +213,39 @@ struct RowRing {
     }
 };
 
-// Forward of both norms. kVecs: 8-column pieces of a row per thread. Streams:
-// x; after: x, residual and, for a gate per element, that.
+// Forward of both norms. kVecs: 8-column pieces of a row per thread, whose
+// weights (and gate per channel) stay in registers. Streams: x; after: x,
+// residual and, for a gate per element, that.
 template <int kVecs, bool kAfter, int kStreams>
-__global__ void __launch_bounds__(kVecs == 1 ? 1024 : 512, kVecs == 1 ? 1 : 2) norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(1024, 1) norm_kernel(const NormArgs a) {
     extern __shared__ uint4 ring_smem[];
     __shared__ float red[2][2][32];
+    constexpr int kDepth = norm_depth(kStreams);
     const int tid = threadIdx.x;
     pdl_wait();
     pdl_trigger();
-    RowRing<kVecs, kStreams> ring;
+    RowRing<kVecs, kStreams, kDepth> ring;
     ring.src[0] = a.x;
     if constexpr (kStreams > 1) ring.src[1] = a.residual;
     if constexpr (kStreams > 2) ring.src[2] = a.gate;
-    ring.start(ring_smem, tid, blockDim.x, a.H, a.T, blockIdx.x, gridDim.x);
+    ring.template start<kDepth - 1>(ring_smem, tid, blockDim.x, a.H, a.T, blockIdx.x, gridDim.x);
     const int warp = tid >> 5, warps = blockDim.x >> 5;
     const float inv_h = 1.0f / float(a.H);
+    float2 w[kVecs][4];
+    Bf16x8 gc[kAfter && kStreams == 2 ? kVecs : 1];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+        if (ring.has(i)) {
+            const Bf16x8 packed = load8(a.weight + (tid + i * blockDim.x) * 8);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[i][j] = packed.pair(j);
+            if (kAfter && kStreams == 2 && a.gate_kind == MOE_GATE_CHANNEL) gc[i] = load8(a.gate + (tid + i * blockDim.x) * 8);
+        }
     int flip = 0, slot = 0;
     for (int row = blockIdx.x; row < a.T; row += gridDim.x, flip ^= 1) {
         const int64_t base = int64_t(row) * a.H + tid * 8;
         ring.next();
-        ring.wait();
+        ring.template wait<kDepth - 1>();
         float2 ss = both(0.0f);
         Bf16x8 x[kVecs];
 #pragma unroll
@@ -254,18 +269,16 @@ __global__ void __launch_bounds__(kVecs == 1 ? 1024 : 512, kVecs == 1 ? 1 : 2) n
             const int col = i * blockDim.x * 8;  // from this thread's first
             Bf16x8 y;
             if (in) {
-                const Bf16x8 w = load8(a.weight + tid * 8 + col);
                 float2 v[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = mul2(mul2(x[i].pair(j), both(rstd)), w.pair(j));
+                for (int j = 0; j < 4; ++j) v[j] = mul2(mul2(x[i].pair(j), both(rstd)), w[i][j]);
                 if constexpr (kAfter) {
                     const Bf16x8 r = ring.get(slot, 1, i);
                     Bf16x8 g;
-                    if constexpr (kStreams > 2) {
+                    if constexpr (kStreams > 2)
                         g = ring.get(slot, 2, i);
-                    } else {
-                        if (a.gate_kind == MOE_GATE_CHANNEL) g = load8(a.gate + tid * 8 + col);
-                    }
+                    else
+                        g = gc[i];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         float2 gv = both(tgate);
@@ -290,141 +303,167 @@ __global__ void __launch_bounds__(kVecs == 1 ? 1024 : 512, kVecs == 1 ? 1 : 2) n
                 }
             }
         }
-        if (++slot == ring.kDepth) slot = 0;
+        if (++slot == kDepth) slot = 0;
     }
 }
 
 // Gradients of both norms: dx, the residual branch, per-token and per-element
 // gates; the column sums of the weight (and of a per-channel gate) per block.
-// A block's threads are `groups` rows of `row_threads`, each with rows of its
-// own, so that short rows leave few column sums too.  Streams: dy, x; then
-// before: the residual branch's gradient if there is one, after: a gate per
-// element.
-template <int kVecs, bool kAfter, int kStreams>
-__global__ void __launch_bounds__(kVecs == 4 ? 512 : 1024, 1) norm_backward_kernel(const NormArgs a) {
+// A block's threads are `groups` groups of `row_threads`, each with rows of its
+// own, so that short rows leave few column sums too; a group works on kRows rows
+// between two meetings of its threads.  kHold: the weights and a gate per channel
+// stay in registers.  Streams: dy, x; then before: the residual branch's gradient
+// if there is one, after: a gate per element.
+template <int kVecs, bool kAfter, int kStreams, int kRows, bool kHold>
+__global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormArgs a) {
     extern __shared__ uint4 ring_smem[];
-    __shared__ float red[2][16][2][32];
+    __shared__ float red[2][2][16][2][32];
     constexpr bool kChannelToo = kAfter && kStreams == 2;  // the gate may be per channel
+    constexpr int kDepth = 2 * kRows;
     const bool channel = kChannelToo && a.gate_kind == MOE_GATE_CHANNEL;
+    const bool token = kChannelToo && a.gate_kind == MOE_GATE_TOKEN;
     const int group = int(threadIdx.x) / a.row_threads, tid = int(threadIdx.x) - group * a.row_threads;
     const int first = int(blockIdx.x) * a.groups + group, step = int(gridDim.x) * a.groups;
     const int warp = tid >> 5, warps = a.row_threads >> 5;
     pdl_wait();
     pdl_trigger();
-    RowRing<kVecs, kStreams> ring;
+    RowRing<kVecs, kStreams, kDepth> ring;
     ring.src[0] = a.dy;
     ring.src[1] = a.x;
     if constexpr (kStreams > 2) ring.src[2] = kAfter ? a.gate : a.dres_in;
-    ring.start(ring_smem, tid, a.row_threads, a.H, a.T, first, step);
+    ring.template start<kRows>(ring_smem, tid, a.row_threads, a.H, a.T, first, step);
     float2 dw[kVecs][4], dg[kChannelToo ? kVecs : 1][4];
+    float2 wf[kHold ? kVecs : 1][4], gf[kHold && kChannelToo ? kVecs : 1][4];
+    auto column = [&](int i) { return (tid + i * a.row_threads) * 8; };
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i)
+    for (int i = 0; i < kVecs; ++i) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             dw[i][j] = both(0.0f);
             if (kChannelToo) dg[i][j] = both(0.0f);
         }
+        if (kHold && ring.has(i)) {
+            const Bf16x8 w = load8(a.weight + column(i));
+            Bf16x8 g;
+            if (channel) g = load8(a.gate + column(i));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                wf[i][j] = w.pair(j);
+                if (kChannelToo && channel) gf[i][j] = g.pair(j);
+            }
+        }
+    }
     const float inv_h = 1.0f / float(a.H);
-    int flip = 0, slot = 0;
-    for (int row = first; row < a.T; row += step, flip ^= 1) {
-        const int64_t base = int64_t(row) * a.H + tid * 8;
-        const float rstd = a.rstd[row];
-        float tgate = 1.0f;
-        if (kAfter && a.gate_kind == MOE_GATE_TOKEN) tgate = __bfloat162float(a.gate[row]);
-        ring.next();
-        ring.wait();
-        // the gate of piece i (its elements, or one value for all of them)
-        auto gate_of = [&](int i, Bf16x8 &g) {
-            if constexpr (kAfter) {
-                if constexpr (kStreams > 2)
-                    g = ring.get(slot, 2, i);
-                else if (channel)
-                    g = load8(a.gate + tid * 8 + i * a.row_threads * 8);
-            }
+    int flip = 0, slot0 = 0;
+    for (int row0 = first; row0 < a.T; row0 += kRows * step, flip ^= 1) {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) ring.next();
+        ring.template wait<kRows>();
+        float rstd[kRows] = {}, tgate[kRows] = {}, dots[2] = {0.0f, 0.0f}, tsums[2] = {0.0f, 0.0f};
+        // weight and gate of piece i: from registers or memory
+        auto weight_of = [&](int i, Bf16x8 &w) {
+            if (!kHold) w = load8(a.weight + column(i));
         };
-        float2 dot = both(0.0f), tsum = both(0.0f);
-        // of piece i, kept for the second pass where there is one piece: xhat and dz w
-        float2 xh1[4], dzw1[4];
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            if (!ring.has(i)) continue;
-            const Bf16x8 dy = ring.get(slot, 0, i), x = ring.get(slot, 1, i);
-            const Bf16x8 w = load8(a.weight + tid * 8 + i * a.row_threads * 8);
-            Bf16x8 g, de;
-            gate_of(i, g);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 d = dy.pair(j), w2 = w.pair(j), xh = mul2(x.pair(j), both(rstd));
-                float2 dz = d;
-                if constexpr (kAfter) {
-                    dz = mul2(d, kStreams > 2 || channel ? g.pair(j) : both(tgate));
-                    const float2 z = mul2(xh, w2);
-                    if constexpr (kStreams > 2) {
-                        de.set(j, mul2(d, z));
-                    } else {
-                        dg[i][j] = fma2(d, z, dg[i][j]);
-                        tsum = fma2(d, z, tsum);
-                    }
-                }
-                const float2 dzw = mul2(dz, w2);
-                dw[i][j] = fma2(dz, xh, dw[i][j]);
-                dot = fma2(dzw, xh, dot);
-                if (kVecs == 1) {
-                    xh1[j] = xh;
-                    dzw1[j] = dzw;
-                }
-            }
+        auto gate_of = [&](int slot, int i, Bf16x8 &g) {
             if constexpr (kAfter && kStreams > 2)
-                store8(static_cast<__nv_bfloat16 *>(a.dgate) + base + i * a.row_threads * 8, de);
-        }
-        const float2 s = row_sum(dot.x + dot.y, tsum.x + tsum.y, red[flip][group], warp, warps, 1 + group);
-        const float2 mean = both(-s.x * inv_h);
-        if (kAfter && a.gate_kind == MOE_GATE_TOKEN && tid == 0) static_cast<float *>(a.dgate)[row] = s.y;
+                g = ring.get(slot, 2, i);
+            else if (!kHold && channel)
+                g = load8(a.gate + column(i));
+        };
+        // dz of pair j, the gradient that reaches xhat w
+        auto dz_of = [&](float2 d, int r, int i, int j, const Bf16x8 &g) {
+            if constexpr (!kAfter) return d;
+            if constexpr (kStreams > 2) return mul2(d, g.pair(j));
+            return mul2(d, channel ? (kHold ? gf[kChannelToo ? i : 0][j] : g.pair(j)) : both(tgate[r]));
+        };
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            if (!ring.has(i)) continue;
-            const int col = i * a.row_threads * 8;
-            Bf16x8 dy, x, w, g, add, out, res;
-            if (kVecs > 1) {
-                x = ring.get(slot, 1, i);
-                w = load8(a.weight + tid * 8 + col);
-                gate_of(i, g);
-            }
-            if (kVecs > 1 || kAfter) dy = ring.get(slot, 0, i);
-            if constexpr (!kAfter && kStreams > 2) add = ring.get(slot, 2, i);
+        for (int r = 0; r < kRows; ++r) {
+            const int row = row0 + r * step;
+            rstd[r] = 0.0f;
+            tgate[r] = 1.0f;
+            if (row >= a.T) continue;
+            rstd[r] = a.rstd[row];
+            if (token) tgate[r] = __bfloat162float(a.gate[row]);
+            const int slot = slot0 + r;
+            float2 dot = both(0.0f), tsum = both(0.0f);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float2 xh, dzw;
-                if (kVecs > 1) {
-                    float2 dz = dy.pair(j);
-                    if (kAfter) dz = mul2(dz, kStreams > 2 || channel ? g.pair(j) : both(tgate));
-                    xh = mul2(x.pair(j), both(rstd));
-                    dzw = mul2(dz, w.pair(j));
-                } else {
-                    xh = xh1[j];
-                    dzw = dzw1[j];
+            for (int i = 0; i < kVecs; ++i) {
+                if (!ring.has(i)) continue;
+                const Bf16x8 dy = ring.get(slot, 0, i), x = ring.get(slot, 1, i);
+                Bf16x8 w, g, de;
+                weight_of(i, w);
+                gate_of(slot, i, g);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 d = dy.pair(j), w2 = kHold ? wf[i][j] : w.pair(j), xh = mul2(x.pair(j), both(rstd[r]));
+                    const float2 dz = dz_of(d, r, i, j, g);
+                    if constexpr (kAfter) {
+                        const float2 z = mul2(xh, w2);
+                        if constexpr (kStreams > 2) {
+                            de.set(j, mul2(d, z));
+                        } else {
+                            if (channel) dg[i][j] = fma2(d, z, dg[i][j]);
+                            if (token) tsum = fma2(d, z, tsum);
+                        }
+                    }
+                    dw[i][j] = fma2(dz, xh, dw[i][j]);
+                    dot = fma2(mul2(dz, w2), xh, dot);
                 }
-                float2 v = mul2(both(rstd), fma2(xh, mean, dzw));
-                if constexpr (!kAfter && kStreams > 2) v = fma2(both(1.0f), add.pair(j), v);
-                out.set(j, v);
-                if (kAfter) res.set(j, mul2(both(a.alpha), dy.pair(j)));
+                if constexpr (kAfter && kStreams > 2)
+                    store8(static_cast<__nv_bfloat16 *>(a.dgate) + int64_t(row) * a.H + column(i), de);
             }
-            store8(a.dx + base + col, out);
-            if (kAfter) store8(a.dres + base + col, res);
+            dots[r] = dot.x + dot.y;
+            tsums[r] = tsum.x + tsum.y;
         }
-        if (++slot == ring.kDepth) slot = 0;
+        const float2 sums = row_sum(dots[0], dots[1], red[flip][0][group], warp, warps, 1 + group);
+        if (token) {
+            const float2 t = row_sum(tsums[0], tsums[1], red[flip][1][group], warp, warps, 1 + group);
+            if (tid == 0) {
+                static_cast<float *>(a.dgate)[row0] = t.x;
+                if (kRows > 1 && row0 + step < a.T) static_cast<float *>(a.dgate)[row0 + step] = t.y;
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const int row = row0 + r * step;
+            if (row >= a.T) continue;
+            const int slot = slot0 + r;
+            const float2 mean = both(-(r == 0 ? sums.x : sums.y) * inv_h);
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                if (!ring.has(i)) continue;
+                const int64_t at = int64_t(row) * a.H + column(i);
+                const Bf16x8 dy = ring.get(slot, 0, i), x = ring.get(slot, 1, i);
+                Bf16x8 w, g, add, out, res;
+                weight_of(i, w);
+                gate_of(slot, i, g);
+                if constexpr (!kAfter && kStreams > 2) add = ring.get(slot, 2, i);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 d = dy.pair(j), xh = mul2(x.pair(j), both(rstd[r]));
+                    const float2 dzw = mul2(dz_of(d, r, i, j, g), kHold ? wf[i][j] : w.pair(j));
+                    float2 v = mul2(both(rstd[r]), fma2(xh, mean, dzw));
+                    if constexpr (!kAfter && kStreams > 2) v = fma2(both(1.0f), add.pair(j), v);
+                    out.set(j, v);
+                    if (kAfter) res.set(j, mul2(both(a.alpha), d));
+                }
+                store8(a.dx + at, out);
+                if (kAfter) store8(a.dres + at, res);
+            }
+        }
+        slot0 = slot0 ? 0 : kRows;
     }
     // the groups' column sums, added in group order through the ring's memory
     asm volatile("cp.async.wait_all;" ::: "memory");
     float *sums = reinterpret_cast<float *>(ring_smem);  // [group][1 or 2][H]
-    float *p = a.part + int64_t(blockIdx.x) * (channel ? 2 : 1) * a.H;
     const int cols = (channel ? 2 : 1) * a.H;
+    float *p = a.part + int64_t(blockIdx.x) * cols;
     __syncthreads();
     float *to = a.groups > 1 ? sums + group * cols : p;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
         if (!ring.has(i)) continue;
-        const int c = (tid + i * a.row_threads) * 8;
+        const int c = column(i);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             *reinterpret_cast<float2 *>(to + c + 2 * j) = dw[i][j];
@@ -466,16 +505,8 @@ __global__ void __launch_bounds__(kColumnWarps * 32) column_sums_kernel(const fl
     }
 }
 
-// Threads, 8-column pieces per thread and ring bytes of a row of H columns.
-struct RowShape {
-    int threads, vecs, bytes;
-};
-RowShape row_shape(int H, bool one, int streams) {
-    const int nvec = H / 8;
-    const int vecs = one ? 1 : 4;  // (H <= 16384: at most 512 threads of 4)
-    const int threads = ((nvec + vecs - 1) / vecs + 31) / 32 * 32;
-    return {threads, vecs, threads * vecs * 16 * streams * norm_depth(streams)};
-}
+// Threads of a row of H columns, `vecs` 8-column pieces each.
+int row_threads(int H, int vecs) { return ((H / 8 + vecs - 1) / vecs + 31) / 32 * 32; }
 constexpr int kSmSmem = 228 * 1024;  // shared memory of an SM, 1 KB of it per resident block
 
 moe_status_t check_norm(int T, int H, float eps) {
@@ -485,68 +516,55 @@ moe_status_t check_norm(int T, int H, float eps) {
 }
 
 template <int kVecs, bool kAfter, int kStreams>
-cudaError_t launch_norm(const NormArgs &a, const RowShape &s, cudaStream_t stream) {
-    const cudaError_t e =
-        set_max_dynamic_smem(reinterpret_cast<const void *>(norm_kernel<kVecs, kAfter, kStreams>), s.bytes);
+cudaError_t launch_norm(const NormArgs &a, cudaStream_t stream) {
+    const int threads = row_threads(a.H, kVecs), bytes = threads * kVecs * 16 * kStreams * norm_depth(kStreams);
+    const cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(norm_kernel<kVecs, kAfter, kStreams>), bytes);
     if (e != cudaSuccess) return e;
     // as many blocks as fit at once (64 registers a thread), each with every gridDim-th row
-    const int by_threads = 1024 / s.threads, by_smem = kSmSmem / (s.bytes + 2048);
+    const int by_threads = 1024 / threads, by_smem = kSmSmem / (bytes + 2048);
     int per_sm = by_threads < by_smem ? by_threads : by_smem;
     if (per_sm < 1) per_sm = 1;
-    if (per_sm > 32) per_sm = 32;
     const int cap = num_sms() * per_sm;
-    return launch_pdl(norm_kernel<kVecs, kAfter, kStreams>, dim3(unsigned(a.T < cap ? a.T : cap)),
-                      dim3(unsigned(s.threads)), size_t(s.bytes), stream, a);
+    return launch_pdl(norm_kernel<kVecs, kAfter, kStreams>, dim3(unsigned(a.T < cap ? a.T : cap)), dim3(unsigned(threads)),
+                      size_t(bytes), stream, a);
 }
 
 template <bool kAfter, int kStreams>
 moe_status_t run_norm(const NormArgs &a, cudaStream_t stream) {
-    // a decode batch: one piece per thread, for latency; else four, for fewer barriers a byte
-    const RowShape s = row_shape(a.H, a.T <= num_sms() && a.H <= 8192, kStreams);
-    const cudaError_t e = s.vecs == 1 ? launch_norm<1, kAfter, kStreams>(a, s, stream)
-                                      : launch_norm<4, kAfter, kStreams>(a, s, stream);
+    // a decode batch: one piece per thread, for latency; else two, which is also
+    // what 1024 threads need for the widest rows
+    const bool one = a.T <= num_sms() && a.H <= 8192;
+    const cudaError_t e =
+        one ? launch_norm<1, kAfter, kStreams>(a, stream) : launch_norm<2, kAfter, kStreams>(a, stream);
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-template <int kVecs, bool kAfter, int kStreams>
-cudaError_t launch_norm_backward(NormArgs a, const RowShape &s, int grid, int bytes, cudaStream_t stream) {
-    const cudaError_t e =
-        set_max_dynamic_smem(reinterpret_cast<const void *>(norm_backward_kernel<kVecs, kAfter, kStreams>), bytes);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(norm_backward_kernel<kVecs, kAfter, kStreams>, dim3(unsigned(grid)),
-                      dim3(unsigned(s.threads * a.groups)), size_t(bytes), stream, a);
-}
-
-template <bool kAfter, int kStreams>
-moe_status_t run_norm_backward(NormArgs a, float *dw, float *dg, cudaStream_t stream) {
-    // One piece of a row per thread, whose intermediate values then stay in
-    // registers, or four; a block has at least two rows under way either way, so
-    // that one computes while the other's threads meet.  8192 tokens, H = 7168,
-    // gate per channel: 134 us with one row of 896 threads, 114 with two of 224.
-    // H = 4096: within 5 % of one another.
-    const RowShape s = row_shape(a.H, a.H <= 4096, kStreams);
+template <int kVecs, bool kAfter, int kStreams, int kRows, bool kHold>
+cudaError_t launch_norm_backward(NormArgs a, float *dw, float *dg, cudaStream_t stream) {
+    const auto kernel = norm_backward_kernel<kVecs, kAfter, kStreams, kRows, kHold>;
     const int cols = a.H * (kAfter && a.gate_kind == MOE_GATE_CHANNEL ? 2 : 1);
-    a.row_threads = s.threads;
-    a.groups = (s.vecs == 4 ? 512 : 1024) / s.threads;
+    a.row_threads = row_threads(a.H, kVecs);
+    a.groups = 512 / a.row_threads;
     if (a.groups > 15) a.groups = 15;  // named barriers
     const int rows_per_block = (a.T + num_sms() - 1) / num_sms();
     if (a.groups > rows_per_block) a.groups = rows_per_block;
-    if (a.groups < 1) a.groups = 1;
-    int bytes = s.bytes * a.groups;
+    int bytes = a.row_threads * a.groups * kVecs * 16 * kStreams * 2 * kRows;
     if (a.groups > 1 && bytes < a.groups * cols * 4) bytes = a.groups * cols * 4;
-    // blocks of one SM: with fewer threads two fit
-    int per_sm = (s.vecs == 4 ? 512 : 1024) / (s.threads * a.groups);
-    if (per_sm > 2) per_sm = 2;
-    if (per_sm > 1 && 2 * (bytes + 10240) > kSmSmem) per_sm = 1;
-    int grid = num_sms() * per_sm;
-    if (grid > kNormMaxBlocks) grid = kNormMaxBlocks;
+    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kernel), bytes);
+    if (e != cudaSuccess) return e;
     const int needed = (a.T + a.groups - 1) / a.groups;
+    int grid = num_sms() < kNormMaxBlocks ? num_sms() : kNormMaxBlocks;
     if (grid > needed) grid = needed;
-    cudaError_t e = s.vecs == 1 ? launch_norm_backward<1, kAfter, kStreams>(a, s, grid, bytes, stream)
-                                : launch_norm_backward<4, kAfter, kStreams>(a, s, grid, bytes, stream);
-    if (e == cudaSuccess)
-        e = launch_pdl(column_sums_kernel, dim3(unsigned((cols + 31) / 32)), dim3(kColumnWarps * 32), 0, stream,
-                       static_cast<const float *>(a.part), grid, cols, a.H, dw, dg);
+    e = launch_pdl(kernel, dim3(unsigned(grid)), dim3(unsigned(a.row_threads * a.groups)), size_t(bytes), stream, a);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(column_sums_kernel, dim3(unsigned((cols + 31) / 32)), dim3(kColumnWarps * 32), 0, stream,
+                      static_cast<const float *>(a.part), grid, cols, a.H, dw, dg);
+}
+
+template <bool kAfter, int kStreams>
+moe_status_t run_norm_backward(const NormArgs &a, float *dw, float *dg, cudaStream_t stream) {
+    const cudaError_t e = a.H <= kNormTwoRowsH ? launch_norm_backward<2, kAfter, kStreams, 2, true>(a, dw, dg, stream)
+                                               : launch_norm_backward<4, kAfter, kStreams, 1, false>(a, dw, dg, stream);
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
