@@ -100,31 +100,38 @@ __device__ __forceinline__ Quantised quantise8(const Bf16x8 &y) {
     return q;
 }
 
-// The sum of v (and of w) over the `warps` warps that take a row, in all of
-// their threads; `warp` is this one's number among them.  The caller alternates
-// two sets of `red`, so one barrier a call is enough: number `bar`, for one row
-// group of several in a block.
-__device__ __forceinline__ float2 row_sum(float v, float w, float (*red)[32], int warp, int warps, int bar) {
+// The sums of kCount values over the `warps` warps that take a row, in all of
+// their threads; `warp` is this one's number among them.  The warps' sums meet in
+// `red` (zero beyond `warps`) and every thread adds them in the same order.  The
+// caller alternates two sets of `red`, so one barrier a call is enough: number
+// `bar`, for one row group of several in a block.
+template <int kCount>
+__device__ __forceinline__ void row_sum(float (&v)[kCount], float (*red)[32], int warp, int warps, int bar) {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-        w += __shfl_xor_sync(0xFFFFFFFFu, w, d);
-    }
-    if (warps == 1) return make_float2(v, w);
-    const int lane = threadIdx.x & 31;
-    if (lane == 0) {
-        red[0][warp] = v;
-        red[1][warp] = w;
-    }
+    for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+        for (int c = 0; c < kCount; ++c) v[c] += __shfl_xor_sync(0xFFFFFFFFu, v[c], d);
+    if (warps == 1) return;
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+        for (int c = 0; c < kCount; ++c) red[c][warp] = v[c];
     asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(warps * 32) : "memory");
-    v = lane < warps ? red[0][lane] : 0.0f;
-    w = lane < warps ? red[1][lane] : 0.0f;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-        w += __shfl_xor_sync(0xFFFFFFFFu, w, d);
+    for (int c = 0; c < kCount; ++c) {
+        float4 t = *reinterpret_cast<const float4 *>(&red[c][0]);
+        for (int i = 4; i < warps; i += 4) {
+            const float4 u = *reinterpret_cast<const float4 *>(&red[c][i]);
+            t.x += u.x;
+            t.y += u.y;
+            t.z += u.z;
+            t.w += u.w;
+        }
+        v[c] = (t.x + t.y) + (t.z + t.w);
     }
-    return make_float2(v, w);
+}
+__device__ __forceinline__ void clear(float *red, int count) {
+    for (int i = threadIdx.x; i < count; i += blockDim.x) red[i] = 0.0f;
+    __syncthreads();
 }
 
 struct NormArgs {
@@ -219,7 +226,7 @@ struct RowRing {
 template <int kVecs, bool kAfter, int kStreams>
 __global__ void __launch_bounds__(1024, 1) norm_kernel(const NormArgs a) {
     extern __shared__ uint4 ring_smem[];
-    __shared__ float red[2][2][32];
+    __shared__ __align__(16) float red[2][1][32];
     constexpr int kDepth = norm_depth(kStreams);
     const int tid = threadIdx.x;
     pdl_wait();
@@ -231,19 +238,23 @@ __global__ void __launch_bounds__(1024, 1) norm_kernel(const NormArgs a) {
     ring.template start<kDepth - 1>(ring_smem, tid, blockDim.x, a.H, a.T, blockIdx.x, gridDim.x);
     const int warp = tid >> 5, warps = blockDim.x >> 5;
     const float inv_h = 1.0f / float(a.H);
-    float2 w[kVecs][4];
-    Bf16x8 gc[kAfter && kStreams == 2 ? kVecs : 1];
+    Bf16x8 w[kVecs], gc[kAfter && kStreams == 2 ? kVecs : 1];
 #pragma unroll
     for (int i = 0; i < kVecs; ++i)
         if (ring.has(i)) {
-            const Bf16x8 packed = load8(a.weight + (tid + i * blockDim.x) * 8);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[i][j] = packed.pair(j);
+            w[i] = load8(a.weight + (tid + i * blockDim.x) * 8);
             if (kAfter && kStreams == 2 && a.gate_kind == MOE_GATE_CHANNEL) gc[i] = load8(a.gate + (tid + i * blockDim.x) * 8);
         }
+    clear(&red[0][0][0], 2 * 32);
+    // the token's gate, brought a row ahead
+    const bool token = kAfter && a.gate_kind == MOE_GATE_TOKEN;
+    __nv_bfloat16 next_gate = __float2bfloat16_rn(1.0f);
+    if (token && blockIdx.x < a.T) next_gate = a.gate[blockIdx.x];
     int flip = 0, slot = 0;
     for (int row = blockIdx.x; row < a.T; row += gridDim.x, flip ^= 1) {
         const int64_t base = int64_t(row) * a.H + tid * 8;
+        const float tgate = __bfloat162float(next_gate);
+        if (token && row + int(gridDim.x) < a.T) next_gate = a.gate[row + gridDim.x];
         ring.next();
         ring.template wait<kDepth - 1>();
         float2 ss = both(0.0f);
@@ -258,11 +269,10 @@ __global__ void __launch_bounds__(1024, 1) norm_kernel(const NormArgs a) {
                     ss = fma2(v, v, ss);
                 }
             }
-        const float sum = row_sum(ss.x + ss.y, 0.0f, red[flip], warp, warps, 0).x;
-        const float rstd = __frsqrt_rn(sum * inv_h + a.eps);
+        float sum[1] = {ss.x + ss.y};
+        row_sum(sum, red[flip], warp, warps, 0);
+        const float rstd = __frsqrt_rn(sum[0] * inv_h + a.eps);
         if (a.rstd_out && tid == 0) a.rstd_out[row] = rstd;
-        float tgate = 1.0f;
-        if (kAfter && a.gate_kind == MOE_GATE_TOKEN) tgate = __bfloat162float(a.gate[row]);
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
             const bool in = ring.has(i);
@@ -271,7 +281,7 @@ __global__ void __launch_bounds__(1024, 1) norm_kernel(const NormArgs a) {
             if (in) {
                 float2 v[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = mul2(mul2(x[i].pair(j), both(rstd)), w[i][j]);
+                for (int j = 0; j < 4; ++j) v[j] = mul2(mul2(x[i].pair(j), both(rstd)), w[i].pair(j));
                 if constexpr (kAfter) {
                     const Bf16x8 r = ring.get(slot, 1, i);
                     Bf16x8 g;
@@ -317,7 +327,7 @@ __global__ void __launch_bounds__(1024, 1) norm_kernel(const NormArgs a) {
 template <int kVecs, bool kAfter, int kStreams, int kRows, bool kHold>
 __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormArgs a) {
     extern __shared__ uint4 ring_smem[];
-    __shared__ float red[2][2][16][2][32];
+    __shared__ __align__(16) float red[2][2][16][kRows][32];
     constexpr bool kChannelToo = kAfter && kStreams == 2;  // the gate may be per channel
     constexpr int kDepth = 2 * kRows;
     const bool channel = kChannelToo && a.gate_kind == MOE_GATE_CHANNEL;
@@ -353,13 +363,31 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormArgs a)
             }
         }
     }
+    clear(&red[0][0][0][0][0], 2 * 2 * 16 * kRows * 32);
     const float inv_h = 1.0f / float(a.H);
+    // the rows' scalars, brought as far ahead as their elements
+    float next_rstd[kRows] = {};
+    __nv_bfloat16 next_gate[kRows] = {};
+    auto fetch = [&](int row0) {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+            if (row0 + r * step < a.T) {
+                next_rstd[r] = a.rstd[row0 + r * step];
+                if (token) next_gate[r] = a.gate[row0 + r * step];
+            }
+    };
+    fetch(first);
     int flip = 0, slot0 = 0;
     for (int row0 = first; row0 < a.T; row0 += kRows * step, flip ^= 1) {
+        float rstd[kRows], tgate[kRows], dots[kRows] = {}, tsums[kRows] = {};
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) ring.next();
+        for (int r = 0; r < kRows; ++r) {
+            rstd[r] = next_rstd[r];
+            tgate[r] = token ? __bfloat162float(next_gate[r]) : 1.0f;
+            ring.next();
+        }
+        fetch(row0 + kRows * step);
         ring.template wait<kRows>();
-        float rstd[kRows] = {}, tgate[kRows] = {}, dots[2] = {0.0f, 0.0f}, tsums[2] = {0.0f, 0.0f};
         // weight and gate of piece i: from registers or memory
         auto weight_of = [&](int i, Bf16x8 &w) {
             if (!kHold) w = load8(a.weight + column(i));
@@ -379,11 +407,7 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormArgs a)
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
             const int row = row0 + r * step;
-            rstd[r] = 0.0f;
-            tgate[r] = 1.0f;
             if (row >= a.T) continue;
-            rstd[r] = a.rstd[row];
-            if (token) tgate[r] = __bfloat162float(a.gate[row]);
             const int slot = slot0 + r;
             float2 dot = both(0.0f), tsum = both(0.0f);
 #pragma unroll
@@ -415,20 +439,19 @@ __global__ void __launch_bounds__(512, 1) norm_backward_kernel(const NormArgs a)
             dots[r] = dot.x + dot.y;
             tsums[r] = tsum.x + tsum.y;
         }
-        const float2 sums = row_sum(dots[0], dots[1], red[flip][0][group], warp, warps, 1 + group);
+        row_sum(dots, red[flip][0][group], warp, warps, 1 + group);
         if (token) {
-            const float2 t = row_sum(tsums[0], tsums[1], red[flip][1][group], warp, warps, 1 + group);
-            if (tid == 0) {
-                static_cast<float *>(a.dgate)[row0] = t.x;
-                if (kRows > 1 && row0 + step < a.T) static_cast<float *>(a.dgate)[row0 + step] = t.y;
-            }
+            row_sum(tsums, red[flip][1][group], warp, warps, 1 + group);
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+                if (tid == 0 && row0 + r * step < a.T) static_cast<float *>(a.dgate)[row0 + r * step] = tsums[r];
         }
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
             const int row = row0 + r * step;
             if (row >= a.T) continue;
             const int slot = slot0 + r;
-            const float2 mean = both(-(r == 0 ? sums.x : sums.y) * inv_h);
+            const float2 mean = both(-dots[r] * inv_h);
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
                 if (!ring.has(i)) continue;
