@@ -749,9 +749,12 @@ def grouped_workspace_bytes() -> int:
     return n.value
 
 
+_GROUPED_WORKSPACE = 2048  # moe_grouped_workspace_bytes
+
+
 def _grouped_workspace(workspace, device):
     if workspace is None:
-        return torch.empty(grouped_workspace_bytes(), dtype=torch.uint8, device=device)
+        return torch.empty(_GROUPED_WORKSPACE, dtype=torch.uint8, device=device)
     _need(workspace, torch.uint8, "workspace")
     if workspace.device != device:
         raise ValueError(f"workspace must be on {device}, got {workspace.device}")
@@ -769,7 +772,7 @@ def _grouped_rows(fn, rows, w, offsets, out, workspace, stream, width_in, width_
     shape = (R, (N, K)[width_out])
     zero_unused = out is None
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        out = rows.new_empty(shape)
     else:
         _need_on(out, torch.bfloat16, "out", shape, dev)
     ws = _grouped_workspace(workspace, dev)
@@ -814,7 +817,7 @@ def grouped_matmul_grad_weight(dy, x, offsets, out=None, workspace=None, stream=
     if E < 1 or offsets.device != dev:
         raise ValueError(f"offsets must hold E + 1 >= 2 values on {dev}")
     if out is None:
-        out = torch.empty((E, N, K), dtype=torch.bfloat16, device=dev)
+        out = x.new_empty((E, N, K))
     else:
         _need_on(out, torch.bfloat16, "out", (E, N, K), dev)
     ws = _grouped_workspace(workspace, dev)
@@ -841,7 +844,7 @@ def fp4_matvec(x, w, w_sf, fmt: str = "mx", out=None, stream=None):
     _need_on(w, torch.uint8, "w", (N, K // 2), dev)
     _need_on(w_sf, torch.uint8, "w_sf", (N, K // group), dev)
     if out is None:
-        out = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
+        out = x.new_empty((T, N))
     else:
         _need_on(out, torch.bfloat16, "out", (T, N), dev)
     _check(load().moe_fp4_matvec(_addr(x), _addr(w), _addr(w_sf), _addr(out), T, N, K, code, _stream_on(stream, dev)),
@@ -874,10 +877,10 @@ def norm_before(x, weight, eps: float = 1e-6, bf16: bool = True, fp8: bool = Fal
     _need_on(weight, torch.bfloat16, "weight", (H,), dev)
     if not (bf16 or fp8):
         raise ValueError("ask for bf16, fp8 or both")
-    y = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if bf16 else None
-    q = torch.empty((T, H), dtype=torch.uint8, device=dev) if fp8 else None
-    sf = torch.empty((T, H // 32), dtype=torch.uint8, device=dev) if fp8 else None
-    r = torch.empty(T, dtype=torch.float32, device=dev) if rstd else None
+    y = torch.empty_like(x) if bf16 else None
+    q = torch.empty_like(x, dtype=torch.uint8) if fp8 else None
+    sf = x.new_empty((T, H // 32), dtype=torch.uint8) if fp8 else None
+    r = x.new_empty(T, dtype=torch.float32) if rstd else None
     _check(load().moe_norm_before(_addr(x), _addr(weight), T, H, eps, _addr(y), _addr(q), _addr(sf), _addr(r),
                                   _stream_on(stream, dev)), "moe_norm_before")
     return NormBefore(y, q, sf, r)
@@ -909,10 +912,10 @@ def norm_after(x, residual, weight, eps: float = 1e-6, gate=None, residual_scale
     _need_on(weight, torch.bfloat16, "weight", (H,), dev)
     kind = _gate(gate, T, H, dev)
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        out = torch.empty_like(x)
     else:
         _need_on(out, torch.bfloat16, "out", (T, H), dev)
-    r = torch.empty(T, dtype=torch.float32, device=dev) if rstd else None
+    r = x.new_empty(T, dtype=torch.float32) if rstd else None
     _check(load().moe_norm_after(_addr(x), _addr(residual), _addr(weight), _addr(gate), kind, T, H, eps, residual_scale,
                                  _addr(out), _addr(r), _stream_on(stream, dev)), "moe_norm_after")
     return NormAfter(out, r)
@@ -947,8 +950,8 @@ def norm_before_backward(dy, x, weight, rstd, dresidual=None, workspace=None, st
     if dresidual is not None:
         _need_on(dresidual, torch.bfloat16, "dresidual", (T, H), dev)
     ws = _norm_workspace(workspace, T, H, dev)
-    dx = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-    dweight = torch.empty(H, dtype=torch.float32, device=dev)
+    dx = torch.empty_like(x)
+    dweight = x.new_empty(H, dtype=torch.float32)
     _check(load().moe_norm_before_backward(_addr(dy), _addr(x), _addr(weight), _addr(rstd), _addr(dresidual), T, H,
                                            _addr(dx), _addr(dweight), _addr(ws), ws.numel(), _stream_on(stream, dev)),
            "moe_norm_before_backward")
@@ -968,9 +971,8 @@ def norm_after_backward(dout, x, weight, rstd, gate=None, residual_scale: float 
     _need_on(rstd, torch.float32, "rstd", (T,), dev)
     kind = _gate(gate, T, H, dev)
     ws = _norm_workspace(workspace, T, H, dev)
-    dx = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-    dresidual = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-    dweight = torch.empty(H, dtype=torch.float32, device=dev)
+    dx, dresidual = torch.empty_like(x), torch.empty_like(x)
+    dweight = x.new_empty(H, dtype=torch.float32)
     dgate = None
     if kind:
         dgate = torch.empty(gate.shape, dtype=torch.bfloat16 if kind == 3 else torch.float32, device=dev)

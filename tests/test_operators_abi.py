@@ -99,3 +99,8 @@ def test_the_binding_takes_cuda_tensors_only(moelib, name):
     t = torch.zeros((4, 64), dtype=torch.bfloat16)
     with pytest.raises(TypeError):
         getattr(m, name)(t, t, t)
+
+
+def test_the_bindings_workspace_of_the_grouped_products(moelib):
+    import moe_expert_layer_08_b200 as m
+    assert m._GROUPED_WORKSPACE == m.grouped_workspace_bytes()
