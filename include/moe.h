@@ -611,11 +611,12 @@ moe_status_t moe_grouped_matmul_grad_weight(const void *dy_bf16, const void *x_b
  * w_fp4 u8 [N, K/2], w_sf u8 [N, K/G] and x bf16 [T, K], all 16-byte
  * aligned; y bf16 [T, N].  x is not quantised; sums are fp32 (x times
  * a power of two enters them as fp16: an element is exact down to 2^-31 of its
- * token's largest one in an eighth of K, and off by at most 2^-40 of it
- * below).  Scale bytes 255 (UE8M0) and 0x7F (UE4M3; bit 7 is not read) are NaN.
- * The weights are read once per 8 tokens (fewer for K above 7168).  K must be
- * a multiple of 32 and at most 57344, T at most 65535, else
- * MOE_ERR_UNSUPPORTED_SHAPE.  T = 0 enqueues nothing.  One kernel per call.
+ * token's largest one, and off by at most 2^-40 of it below).  Scale bytes 255
+ * (UE8M0) and 0x7F (UE4M3; bit 7 is not read) are NaN.  The weights are read
+ * once per 8 tokens (fewer for K above 7168).  K must be a multiple of 32 and at
+ * most 57344, T at most 65535, else MOE_ERR_UNSUPPORTED_SHAPE.  T = 0 enqueues
+ * nothing.  One kernel per call.  A wait inside the kernel that gave up (2 s)
+ * leaves NaN in its outputs.
  */
 #define MOE_FP4_MX 0
 #define MOE_FP4_NVFP4 1

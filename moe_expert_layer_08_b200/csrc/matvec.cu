@@ -5,17 +5,21 @@
 // byte is used once per 8 tokens, so the kernel is bound by the HBM stream of
 // N K (1/2 + 1/G) bytes.
 //
-// A block has two teams of eight warps; a team cuts K into eight slices and
-// walks over tiles of 16 rows.  A warp streams its slice of a tile, weights and
-// scales, through its own ring of cp.async stages (no waits on other warps), and
-// multiplies on the tensor cores: mma.m16n8k16 with the weights as the 16-row
-// operand and 8 tokens as the other, so 1 to 8 tokens cost the same.  c is exact
-// in fp16.  The tokens are brought to fp16 too, each token's slice scaled by a
-// power of two that puts its largest finite magnitude in [2^14, 2^15): bf16's 8
-// bits fit, and an element loses bits only below 2^-31 of that largest one (it
-// is then off by at most 2^-40 of it, less than a rounding of the fp32 sum).
-// The group scale multiplies the fp32 sum of its group.  The eight slices' sums
-// meet in shared memory and are added in slice order.
+// A block's 16 warps are two teams, each with a tile of 16 rows at a time and K cut
+// into eight slices (a tile costs a team about 100 instructions besides its
+// weights: as one team of 16 slices 30.1 us instead of 27.2 at N = 14336, K =
+// 7168).  A warp streams its slice of a tile through its
+// own ring (TMA boxes of 16 rows x 128 bytes, the scales by cp.async; no waits on
+// other warps), and multiplies on the tensor cores: mma.m16n8k16 with the weights
+// as the 16-row operand and 8 tokens as the other, so 1 to 8 tokens cost the
+// same.  c is exact in fp16.  The tokens are brought to fp16 too, each token's
+// slice scaled by a power of two that puts its largest finite magnitude in
+// [2^14, 2^15): bf16's 8 bits fit, and an element loses bits only below 2^-31 of
+// that largest one (it is then off by at most 2^-40 of it, less than a rounding
+// of the fp32 sum).  The group scale multiplies the fp32 sum of its group.  The
+// slices' sums meet in shared memory and are added in slice order.
+// What bounds it is the decoding: about 50 instructions per warp and 512 weights,
+// half of them on the integer pipe, against 11 cycles of an SM's share of HBM.
 #include <cuda_fp16.h>
 
 #include "moe_common.cuh"
@@ -24,21 +28,24 @@
 namespace moe {
 namespace {
 
-constexpr int kMvWarps = 8;                        // of a team: slices of K
+constexpr int kMvWarps = 16;
 constexpr int kMvTeams = 2;
+constexpr int kMvSlices = kMvWarps / kMvTeams;     // of K, one per warp of a team
 constexpr int kMvRows = 16;                        // rows of a tile (MMA M)
 constexpr int kMvTokens = 8;                       // tokens of a pass (MMA N)
-constexpr int kMvChunk = 256;                      // K elements of a stage
-constexpr int kMvRowBytes = kMvChunk / 2 + 16;     // padded: a quad's words of 8 rows fall into 32 banks
-// a row's scales of a stage (at most 16 bytes) inside two aligned 16-byte
-// pieces, padded likewise
-constexpr int kMvScaleBytes = 48;
-constexpr int kMvStageBytes = kMvRows * (kMvRowBytes + kMvScaleBytes);
-constexpr int kMvSumBytes = 2 * kMvTeams * kMvWarps * kMvRows * kMvTokens * 4;
+constexpr int kMvChunk = 256;                      // K elements of a stage: 128 bytes of codes a row
+constexpr int kMvCodeBytes = kMvRows * 128;        // of a stage
+constexpr int kMvScaleBytes = kMvRows * 32;        // of a stage: two aligned pieces around a row's scales
+constexpr int kMvSumBytes = 2 * kMvWarps * kMvRows * kMvTokens * 4;
+constexpr int kMvMaxBytes = (kMvWarps + 1) * kMvTokens * 4 + 96;  // the tokens' largest magnitudes and factors
 constexpr int kMvMaxSmem = 232448;
 constexpr int kMvMaxK = 57344;
-constexpr int mv_fixed_bytes(int stages) { return kMvTeams * kMvWarps * stages * kMvStageBytes + kMvSumBytes; }
-static_assert(mv_fixed_bytes(2) + (2 * kMvMaxK + 127) / 128 * 128 + 64 <= kMvMaxSmem, "one token of the largest K");
+// a stage's scales as fp32, per warp
+constexpr int mv_float_bytes(bool nv) { return kMvRows * (nv ? 64 : 32); }
+constexpr int mv_fixed_bytes(bool nv, int stages) {
+    return 1024 + kMvWarps * (stages * (kMvCodeBytes + kMvScaleBytes + 8) + mv_float_bytes(nv)) + kMvSumBytes + kMvMaxBytes;
+}
+static_assert(mv_fixed_bytes(true, 2) + (2 * kMvMaxK + 127) / 128 * 128 + 64 <= kMvMaxSmem, "one token of the largest K");
 
 // The E2M1 codes in bits 4j.. and 4j + 16.. of w as fp16 times 2^-14: sign,
 // exponent and mantissa bits in place (E2M1's bits are those of an fp16 number
@@ -57,7 +64,6 @@ struct MatvecArgs {
     __nv_bfloat16 *y;         // [T, N]
     int T, N, K;
     int tokens;               // tokens of a pass (blockIdx.y), <= kMvTokens
-    int slice;                // K elements of a warp's slice, a multiple of 32
     int x_stride;             // bytes of a token in shared memory
     PairFactors factors;
 };
@@ -80,21 +86,22 @@ __device__ __forceinline__ uint32_t e2m1_pair(uint32_t w, const PairFactors &f) 
 // d = a b + c: c is zero for the first step of a group
 __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                             uint32_t b0, uint32_t b1, const float (&c)[4]) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%10, %11, %12, %13};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
-// 2^(b - 127) for a UE8M0 byte b <= 254 (a subnormal for b = 0), infinity for 255.
-__device__ __forceinline__ float ue8m0_value(uint32_t b) { return __uint_as_float(max(b << 23, 0x00400000u)); }
-// 2^-8 times the value of a UE4M3 byte below 0x7F (bit 7 is not read): its bits
+// 2^(b - 127) for a UE8M0 byte b (a subnormal for 0, NaN for 255).
+__device__ __forceinline__ float ue8m0_value(uint32_t b) {
+    return __uint_as_float(b == 255u ? 0x7FC00000u : max(b << 23, 0x00400000u));
+}
+// 2^-8 times the value of a UE4M3 byte (bit 7 is not read, 0x7F is NaN): its bits
 // are those of an fp16 number with an exponent bias of 15 instead of 7.
 __device__ __forceinline__ float ue4m3_value_256th(uint32_t b) {
     __half_raw h;
     h.x = static_cast<unsigned short>((b & 0x7Fu) << 7);
-    return __half2float(__half(h));
+    return (b & 0x7Fu) == 0x7Fu ? __uint_as_float(0x7FC00000u) : __half2float(__half(h));
 }
 
 // acc += d * scale: rows g (first two sums) and g + 8 (last two).
@@ -105,48 +112,65 @@ __device__ __forceinline__ void add_group(float (&acc)[4], const float (&d)[4], 
     acc[3] = fmaf(d[3], s1, acc[3]);
 }
 
+// Where a wait that gave up leaves its mark (the outputs become NaN).
+__device__ int g_matvec_err[8];
+
 template <bool kNv, int kStages>
-__global__ void __launch_bounds__(kMvTeams * kMvWarps * 32, 1) fp4_matvec_kernel(const MatvecArgs args) {
+__global__ void __launch_bounds__(kMvWarps * 32, 1)
+    fp4_matvec_kernel(const __grid_constant__ CUtensorMap tmap_w, const MatvecArgs args) {
     constexpr int kGroup = kNv ? 16 : 32;
-    extern __shared__ __align__(128) uint8_t smem[];
-    const int wid = threadIdx.x >> 5, team = wid / kMvWarps, warp = wid % kMvWarps, lane = threadIdx.x & 31;
+    constexpr int kChunkScales = kMvChunk / kGroup;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ volatile int abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     const int tok0 = int(blockIdx.y) * args.tokens;
     const int ntok = min(args.tokens, args.T - tok0);
-    const int k_lo = min(warp * args.slice, args.K), k_hi = min(k_lo + args.slice, args.K);
+    const int units = args.K / 32, team = warp / kMvSlices, mine = warp % kMvSlices;
+    const int k_lo = mine * units / kMvSlices * 32, k_hi = (mine + 1) * units / kMvSlices * 32;
     const int chunks = (k_hi - k_lo + kMvChunk - 1) / kMvChunk;
     const int tiles = (args.N + kMvRows - 1) / kMvRows;
     const int first = int(blockIdx.x) + team * int(gridDim.x), step = kMvTeams * int(gridDim.x);
-    uint8_t *ring = smem + wid * kStages * kMvStageBytes;
-    float *sums = reinterpret_cast<float *>(smem + kMvTeams * kMvWarps * kStages * kMvStageBytes) +
-                  team * 2 * kMvWarps * kMvRows * kMvTokens;
-    uint8_t *xs = smem + mv_fixed_bytes(kStages);
-    const int64_t w_ld = args.K / 2, sf_ld = args.K / kGroup, sf_end = args.N * sf_ld;
+    uint8_t *codes = smem + warp * kStages * kMvCodeBytes;
+    uint8_t *scales = smem + kMvWarps * kStages * kMvCodeBytes + warp * kStages * kMvScaleBytes;
+    uint8_t *floats = smem + kMvWarps * kStages * (kMvCodeBytes + kMvScaleBytes) + warp * mv_float_bytes(kNv);
+    uint8_t *after = smem + kMvWarps * (kStages * (kMvCodeBytes + kMvScaleBytes) + mv_float_bytes(kNv));
+    float *sums = reinterpret_cast<float *>(after);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(after + kMvSumBytes) + warp * kStages;
+    uint8_t *xs = after + kMvSumBytes + kMvWarps * kStages * 8 + kMvMaxBytes;
+    const int64_t sf_ld = args.K / kGroup, sf_end = args.N * sf_ld;
 
+    if (threadIdx.x == 0) abort_flag = 0;  // (read by waits, which come after the block has met)
+    if (lane == 0) {
+        for (int s = 0; s < kStages; ++s) mbar_init(&bars[s], 1);  // this warp's own
+        fence_mbar_init();
+    }
+    __syncwarp();
     pdl_wait();
     pdl_trigger();
-    // the stages of this warp's stream in order: the chunks of its tiles
+    const uint64_t pol = policy_evict_first();
+    // The stages of this warp's stream in order: the chunks of its tiles. Lane 0
+    // brings the codes; every lane a 16-byte piece of a row's scales (the two
+    // aligned pieces around them, cut at the array's end).
     int load_tile = first, load_chunk = 0, load_slot = 0;
+    const int piece_row = lane >> 1;
+    int64_t at = 0;  // of this lane's row of the tile, the first scale of the chunk
     auto load_next = [&]() {
         if (load_tile < tiles && chunks > 0) {
             const int k0 = k_lo + load_chunk * kMvChunk;
-            const int elems = min(kMvChunk, k_hi - k0);
-            const uint32_t dst = smem_u32(ring + load_slot * kMvStageBytes);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = i * 4 + (lane >> 3), p = lane & 7;
-                const int n = load_tile * kMvRows + r;
-                const bool real = n < args.N;
-                if (p * 32 < elems)
-                    cp_async16(dst + r * kMvRowBytes + p * 16, args.w + (real ? n : 0) * w_ld + k0 / 2 + p * 16,
-                               real ? 16 : 0);
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bars[load_slot], kMvCodeBytes);
+                tma_load_2d(codes + load_slot * kMvCodeBytes, &tmap_w, &bars[load_slot], k0 / 2, load_tile * kMvRows, pol);
             }
-            // the aligned 16-byte pieces that hold the scales, cut at the array's end
-            const int n = load_tile * kMvRows + (lane >> 1);
-            const int64_t s = int64_t(n) * sf_ld + k0 / kGroup, p = (s & ~int64_t(15)) + (lane & 1) * 16;
-            if (n < args.N && p < s + elems / kGroup)
-                cp_async16(dst + kMvRows * kMvRowBytes + (lane >> 1) * kMvScaleBytes + (lane & 1) * 16, args.sf + p,
-                           int(min(int64_t(16), sf_end - p)));
+            if (load_chunk == 0) at = min(load_tile * kMvRows + piece_row, args.N - 1) * sf_ld + k_lo / kGroup;
+            const int64_t p = (at & ~int64_t(15)) + (lane & 1) * 16;
+            if ((lane & 1) == 0 || (int(at) & 15) + kChunkScales > 16) {
+                const int64_t left = sf_end - p;
+                if (left > 0)
+                    cp_async16(smem_u32(scales + load_slot * kMvScaleBytes + lane * 16), args.sf + p, left < 16 ? int(left) : 16);
+            }
+            at += kChunkScales;
             if (++load_chunk == chunks) {
                 load_chunk = 0;
                 load_tile += step;
@@ -158,14 +182,28 @@ __global__ void __launch_bounds__(kMvTeams * kMvWarps * 32, 1) fp4_matvec_kernel
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) load_next();
 
-    // the tokens' slices in fp16: each of the two warps of a slice takes every second token
-    float *unscales = sums + kMvWarps * kMvRows * kMvTokens;  // in the second buffer of sums until the first tile ends
-    float unscale[2];                                         // of tokens 2t and 2t + 1, the columns of this lane's sums
-    for (int j = 0; j < ntok; ++j) {
-        const __nv_bfloat16 *xr = args.x + int64_t(tok0 + j) * args.K;
-        float amax = 0.0f;
-        for (int k = k_lo + lane * 8; k < k_hi; k += 256) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(xr + k);
+    // The tokens in fp16, a sixteenth of K per warp, in the order of the decoded
+    // weights: NVFP4 elements 0 and 2, 1 and 3, 4 and 6, 5 and 7, MX elements 0 and
+    // 4, 1 and 5, 2 and 6, 3 and 7.  First every token's largest magnitude, then
+    // the values; two tokens at a time, the next two on their way.
+    float *amaxs = reinterpret_cast<float *>(after + kMvSumBytes + kMvWarps * kStages * 8);  // [warp][token]
+    float *unscales = amaxs + kMvWarps * kMvTokens;                                            // [token]
+    {
+        const int x_lo = warp * units / kMvWarps * 32, x_hi = (warp + 1) * units / kMvWarps * 32;
+        const int k0 = x_lo + lane * 8, k1 = k0 + 256;  // two pieces of a token: all of a sixteenth of up to 512
+        const auto piece = [&](int j, int k) {
+            return __ldg(reinterpret_cast<const uint4 *>(args.x + int64_t(tok0 + j) * args.K + k));
+        };
+        uint4 raw[2][2];
+        const auto fetch = [&](int j0) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                raw[j][0] = raw[j][1] = make_uint4(0, 0, 0, 0);
+                if (j0 + j < ntok && k0 < x_hi) raw[j][0] = piece(j0 + j, k0);
+                if (j0 + j < ntok && k1 < x_hi) raw[j][1] = piece(j0 + j, k1);
+            }
+        };
+        const auto largest = [](uint4 u, float amax) {
             const uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -173,82 +211,131 @@ __global__ void __launch_bounds__(kMvTeams * kMvWarps * 32, 1) fp4_matvec_kernel
                 if (a <= 3.4e38f) amax = fmaxf(amax, a);
                 if (b <= 3.4e38f) amax = fmaxf(amax, b);
             }
-        }
+            return amax;
+        };
+        fetch(0);
+#pragma unroll 1
+        for (int j0 = 0; j0 < ntok; j0 += 2) {
+            const uint4 cur[2][2] = {{raw[0][0], raw[0][1]}, {raw[1][0], raw[1][1]}};
+            fetch(j0 + 2 < ntok ? j0 + 2 : 0);  // the values' loop begins with the first two
+            float amax[2];
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
-        // 2^shift brings amax into [2^14, 2^15); both factors are normal numbers
-        const int shift = min(max(14 - (int(__float_as_uint(amax) >> 23) - 127), -113), 126);
-        const float mul = amax > 0.0f ? __uint_as_float(uint32_t(127 + shift) << 23) : 1.0f;
-        if (lane == 0) unscales[warp * kMvTokens + j] = amax > 0.0f ? __uint_as_float(uint32_t(127 - shift) << 23) : 1.0f;
-        if ((j & 1) == team)
-            for (int k = k_lo + lane * 8; k < k_hi; k += 256) {
-                const uint4 u = *reinterpret_cast<const uint4 *>(xr + k);
-                const uint32_t v[4] = {u.x, u.y, u.z, u.w};
-                // in the order of the decoded weights: NVFP4 elements 0 and 2, 1 and 3, 4
-                // and 6, 5 and 7, MX elements 0 and 4, 1 and 5, 2 and 6, 3 and 7
-                uint32_t h[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int lo = kNv ? (i & 1) + 4 * (i >> 1) : i, hi = lo + (kNv ? 2 : 4);
-                    const auto value = [&](int e) { return __uint_as_float(e & 1 ? v[e >> 1] & 0xFFFF0000u : v[e >> 1] << 16); };
-                    const __half2 p = __floats2half2_rn(value(lo) * mul, value(hi) * mul);
-                    h[i] = *reinterpret_cast<const uint32_t *>(&p);
-                }
-                *reinterpret_cast<uint4 *>(xs + j * args.x_stride + k * 2) = make_uint4(h[0], h[1], h[2], h[3]);
+            for (int j = 0; j < 2; ++j) {
+                amax[j] = largest(cur[j][1], largest(cur[j][0], 0.0f));
+                if (j0 + j < ntok)
+                    for (int k = k1 + 256; k < x_hi; k += 256) amax[j] = largest(piece(j0 + j, k), amax[j]);
             }
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) amax[j] = fmaxf(amax[j], __shfl_xor_sync(0xFFFFFFFFu, amax[j], d));
+            if (lane < 2) amaxs[warp * kMvTokens + j0 + lane] = lane ? amax[1] : amax[0];
+        }
+        __syncthreads();
+        const auto put = [&](int j, int k, uint4 u, float mul) {
+            const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+            uint32_t h[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int lo = kNv ? (i & 1) + 4 * (i >> 1) : i, hi = lo + (kNv ? 2 : 4);
+                const auto value = [&](int e) { return __uint_as_float(e & 1 ? v[e >> 1] & 0xFFFF0000u : v[e >> 1] << 16); };
+                const __half2 p = __floats2half2_rn(value(lo) * mul, value(hi) * mul);
+                h[i] = *reinterpret_cast<const uint32_t *>(&p);
+            }
+            *reinterpret_cast<uint4 *>(xs + j * args.x_stride + k * 2) = make_uint4(h[0], h[1], h[2], h[3]);
+        };
+#pragma unroll 1
+        for (int j0 = 0; j0 < ntok; j0 += 2) {
+            const uint4 cur[2][2] = {{raw[0][0], raw[0][1]}, {raw[1][0], raw[1][1]}};
+            fetch(j0 + 2);
+            // lanes 0-15 the warps' largest of the first token, 16-31 of the second
+            float amax = amaxs[(lane & 15) * kMvTokens + j0 + (lane >> 4)];
+#pragma unroll
+            for (int d = 8; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+            // 2^shift brings amax into [2^14, 2^15); both factors are normal numbers
+            const int shift = min(max(14 - (int(__float_as_uint(amax) >> 23) - 127), -113), 126);
+            const float factor = amax > 0.0f ? __uint_as_float(uint32_t(127 + shift) << 23) : 1.0f;
+            if (warp == 0 && (lane & 15) == 0)
+                unscales[j0 + (lane >> 4)] = amax > 0.0f ? __uint_as_float(uint32_t(127 - shift) << 23) : 1.0f;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float mul = __shfl_sync(0xFFFFFFFFu, factor, 16 * j);
+                if (j0 + j >= ntok) break;
+                if (k0 < x_hi) put(j0 + j, k0, cur[j][0], mul);
+                if (k1 < x_hi) put(j0 + j, k1, cur[j][1], mul);
+                for (int k = k1 + 256; k < x_hi; k += 256) put(j0 + j, k, piece(j0 + j, k), mul);
+            }
+        }
     }
     __syncthreads();
-    unscale[0] = 2 * t < ntok ? unscales[warp * kMvTokens + 2 * t] : 0.0f;
-    unscale[1] = 2 * t + 1 < ntok ? unscales[warp * kMvTokens + 2 * t + 1] : 0.0f;
+    float unscale[2];  // of tokens 2t and 2t + 1, the columns of this lane's sums
+    unscale[0] = 2 * t < ntok ? unscales[2 * t] : 0.0f;
+    unscale[1] = 2 * t + 1 < ntok ? unscales[2 * t + 1] : 0.0f;
 
-    const uint8_t *xrow = xs + min(g, ntok - 1) * args.x_stride;  // token g
+    const uint8_t *xrow = xs + min(g, ntok - 1) * args.x_stride + (kNv ? t * 8 : t * 16);  // token g
     int slot = 0, buf = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    const int swz = g * 16;  // 16-byte pieces of a row of codes: piece ^ row % 8
     for (int tile = first; tile < tiles; tile += step, buf ^= 1) {
         float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        // rows g and g + 8 have a NaN scale: the largest byte of UE4M3; for UE8M0, whose
-        // byte 255 becomes an infinity, the sum of zero times the scales
-        uint32_t top0 = 0, top1 = 0;
-        float nan0 = 0.0f, nan1 = 0.0f;
-        // where rows g and g + 8 have their first scale inside its 16-byte piece
-        const int64_t s0 = (int64_t(tile) * kMvRows + g) * sf_ld + k_lo / kGroup, s1 = s0 + 8 * sf_ld;
+        // where this lane's row of the tile (two lanes a row) has its first scale
+        int64_t first_scale = min(tile * kMvRows + piece_row, args.N - 1) * sf_ld + k_lo / kGroup;
         for (int c = 0; c < chunks; ++c) {
             cp_async_wait<kStages - 2>();
+            ok = mbar_wait_cycles(&bars[slot], phase, &abort_flag, g_matvec_err, 61) && ok;
             __syncwarp();  // this stage has landed for every lane, and the one before it is read
             load_next();
-            const uint8_t *st = ring + slot * kMvStageBytes + g * kMvRowBytes;
-            const uint8_t *sc = ring + slot * kMvStageBytes + kMvRows * kMvRowBytes + g * kMvScaleBytes;
-            const uint8_t *sc0 = sc + ((s0 + c * (kMvChunk / kGroup)) & 15);
-            const uint8_t *sc1 = sc + 8 * kMvScaleBytes + ((s1 + c * (kMvChunk / kGroup)) & 15);
+            // the stage's scales as fp32: half a row per lane
+            {
+                const uint8_t *sc = scales + slot * kMvScaleBytes + piece_row * 32 + (int(first_scale) & 15) +
+                                    (lane & 1) * (kChunkScales / 2);
+                const int r = piece_row;
+                float f[kChunkScales / 2];
+#pragma unroll
+                for (int i = 0; i < kChunkScales / 2; ++i) f[i] = kNv ? ue4m3_value_256th(sc[i]) : ue8m0_value(sc[i]);
+#pragma unroll
+                for (int i = 0; i < kChunkScales / 8; ++i) {
+                    const int piece = (lane & 1) * (kChunkScales / 8) + i;
+                    uint8_t *to = floats + (kNv ? r * 64 + ((piece ^ (r >> 1 & 3)) << 4) : r * 32 + ((piece ^ (r >> 2 & 1)) << 4));
+                    *reinterpret_cast<float4 *>(to) = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+                }
+                first_scale += kChunkScales;
+            }
+            __syncwarp();
+            const uint8_t *st = codes + slot * kMvCodeBytes + g * 128;
             const uint8_t *xk = xrow + (k_lo + c * kMvChunk) * 2;
             const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            // four scales of rows g and g + 8 (the swizzle is the same for both)
+            auto four = [&](int row, int piece) {
+                return *reinterpret_cast<const float4 *>(
+                    floats + (kNv ? row * 64 + ((piece ^ (g >> 1 & 3)) << 4) : row * 32 + ((piece ^ (g >> 2 & 1)) << 4)));
+            };
             // 32 elements: two groups of 16 or one of 32
-            auto block = [&](int i) {
+            auto block = [&](int i, float s0, float s1, float s2, float s3) {
                 float d[4];
                 uint32_t a[4];
+                const uint8_t *row = st + ((i << 4) ^ swz);
                 if constexpr (kNv) {
                     // a group of 16 is one step: lane t holds its elements 4t .. 4t + 3
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
-                        const uint32_t wa = *reinterpret_cast<const uint16_t *>(st + i * 16 + s * 8 + t * 2);
-                        const uint32_t wb =
-                            *reinterpret_cast<const uint16_t *>(st + i * 16 + s * 8 + t * 2 + 8 * kMvRowBytes);
-                        const uint2 xv = *reinterpret_cast<const uint2 *>(xk + (i * 32 + s * 16 + t * 4) * 2);
+                        const uint32_t wa = *reinterpret_cast<const uint16_t *>(row + s * 8 + t * 2);
+                        const uint32_t wb = *reinterpret_cast<const uint16_t *>(row + s * 8 + t * 2 + 8 * 128);
+                        const uint2 xv = *reinterpret_cast<const uint2 *>(xk + (i * 32 + s * 16) * 2);
                         const uint32_t pa = __byte_perm(wa, 0u, 0x4140u), pb = __byte_perm(wb, 0u, 0x4140u);
                         a[0] = e2m1_pair<0>(pa, args.factors);
                         a[1] = e2m1_pair<0>(pb, args.factors);
                         a[2] = e2m1_pair<1>(pa, args.factors);
                         a[3] = e2m1_pair<1>(pb, args.factors);
                         mma_16x8x16(d, a[0], a[1], a[2], a[3], xv.x, xv.y, zero);
-                        const uint32_t b0 = sc0[2 * i + s] & 0x7Fu, b1 = sc1[2 * i + s] & 0x7Fu;
-                        top0 = max(top0, b0);
-                        top1 = max(top1, b1);
-                        add_group(acc, d, ue4m3_value_256th(b0), ue4m3_value_256th(b1));
+                        add_group(acc, d, s ? s2 : s0, s ? s3 : s1);
                     }
                 } else {
                     // a group of 32 is two steps: lane t holds its elements 8t .. 8t + 7
-                    const uint32_t wa = *reinterpret_cast<const uint32_t *>(st + i * 16 + t * 4);
-                    const uint32_t wb = *reinterpret_cast<const uint32_t *>(st + i * 16 + t * 4 + 8 * kMvRowBytes);
-                    const uint4 xv = *reinterpret_cast<const uint4 *>(xk + (i * 32 + t * 8) * 2);
+                    const uint32_t wa = *reinterpret_cast<const uint32_t *>(row + t * 4);
+                    const uint32_t wb = *reinterpret_cast<const uint32_t *>(row + t * 4 + 8 * 128);
+                    const uint4 xv = *reinterpret_cast<const uint4 *>(xk + i * 32 * 2);
                     a[0] = e2m1_pair<0>(wa, args.factors);
                     a[1] = e2m1_pair<0>(wb, args.factors);
                     a[2] = e2m1_pair<1>(wa, args.factors);
@@ -259,57 +346,86 @@ __global__ void __launch_bounds__(kMvTeams * kMvWarps * 32, 1) fp4_matvec_kernel
                     a[2] = e2m1_pair<3>(wa, args.factors);
                     a[3] = e2m1_pair<3>(wb, args.factors);
                     mma_16x8x16(d, a[0], a[1], a[2], a[3], xv.z, xv.w, d);
-                    const float f0 = ue8m0_value(sc0[i]), f1 = ue8m0_value(sc1[i]);
-                    nan0 = fmaf(f0, 0.0f, nan0);
-                    nan1 = fmaf(f1, 0.0f, nan1);
-                    add_group(acc, d, f0, f1);
+                    add_group(acc, d, s0, s1);
                 }
             };
             const int blocks = min(kMvChunk, k_hi - k_lo - c * kMvChunk) / 32;
-            if (blocks == kMvChunk / 32) {
+            constexpr int kPer = kNv ? 2 : 4;  // blocks of four scales a row
+            auto quad = [&](int i0) {          // four blocks
 #pragma unroll
-                for (int i = 0; i < kMvChunk / 32; ++i) block(i);
+                for (int i = i0; i < i0 + 4; i += kPer) {
+                    const float4 u = four(g, i / kPer), v = four(g + 8, i / kPer);
+                    if constexpr (kNv) {
+                        block(i, u.x, v.x, u.y, v.y);
+                        block(i + 1, u.z, v.z, u.w, v.w);
+                    } else {
+                        block(i, u.x, v.x, 0.0f, 0.0f);
+                        block(i + 1, u.y, v.y, 0.0f, 0.0f);
+                        block(i + 2, u.z, v.z, 0.0f, 0.0f);
+                        block(i + 3, u.w, v.w, 0.0f, 0.0f);
+                    }
+                }
+            };
+            if (blocks == kMvChunk / 32) {
+                quad(0);
+                quad(4);
             } else {
+                if (blocks >= 4) quad(0);
 #pragma unroll 1
-                for (int i = 0; i < blocks; ++i) block(i);
+                for (int i = blocks & 4; i < blocks; ++i) {
+                    const float4 u = four(g, i / kPer), v = four(g + 8, i / kPer);
+                    if constexpr (kNv) {
+                        const bool odd = i & 1;
+                        block(i, odd ? u.z : u.x, odd ? v.z : v.x, odd ? u.w : u.y, odd ? v.w : v.y);
+                    } else {
+                        const int k = i & 3;
+                        block(i, k == 0 ? u.x : k == 1 ? u.y : k == 2 ? u.z : u.w,
+                              k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w, 0.0f, 0.0f);
+                    }
+                }
             }
-            if (++slot == kStages) slot = 0;
-        }
-        if (kNv) {
-            nan0 = top0 == 0x7Fu ? __uint_as_float(0x7FC00000u) : 0.0f;
-            nan1 = top1 == 0x7Fu ? __uint_as_float(0x7FC00000u) : 0.0f;
+            if (++slot == kStages) {
+                slot = 0;
+                phase ^= 1u;
+            }
         }
         // 2^14 for the codes, 2^8 for the UE4M3 scales' exponent bias
-        constexpr float kBack = kNv ? 0x1p22f : 0x1p14f;
+        const float back = !ok ? __uint_as_float(0x7FC00000u) : kNv ? 0x1p22f : 0x1p14f;
         // rows g and g + 8, tokens 2t and 2t + 1 of this slice
-        float *mine = sums + (buf * kMvWarps + warp) * kMvRows * kMvTokens;
-        mine[g * kMvTokens + 2 * t] = (acc[0] * kBack + nan0) * unscale[0];
-        mine[g * kMvTokens + 2 * t + 1] = (acc[1] * kBack + nan0) * unscale[1];
-        mine[(g + 8) * kMvTokens + 2 * t] = (acc[2] * kBack + nan1) * unscale[0];
-        mine[(g + 8) * kMvTokens + 2 * t + 1] = (acc[3] * kBack + nan1) * unscale[1];
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(kMvWarps * 32) : "memory");
-        const int id = warp * 32 + lane;
+        float *part = sums + (buf * kMvWarps + warp) * kMvRows * kMvTokens;
+        part[g * kMvTokens + 2 * t] = acc[0] * back * unscale[0];
+        part[g * kMvTokens + 2 * t + 1] = acc[1] * back * unscale[1];
+        part[(g + 8) * kMvTokens + 2 * t] = acc[2] * back * unscale[0];
+        part[(g + 8) * kMvTokens + 2 * t + 1] = acc[3] * back * unscale[1];
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(kMvSlices * 32) : "memory");
+        const int id = mine * 32 + lane;
         if (id < kMvRows * ntok) {
             const int j = id >> 4, r = id & 15;
             const int n = tile * kMvRows + r;
             if (n < args.N) {
                 float v = 0.0f;
 #pragma unroll
-                for (int i = 0; i < kMvWarps; ++i)
-                    v += sums[(buf * kMvWarps + i) * kMvRows * kMvTokens + r * kMvTokens + j];
+                for (int i = 0; i < kMvSlices; ++i)
+                    v += sums[(buf * kMvWarps + team * kMvSlices + i) * kMvRows * kMvTokens + r * kMvTokens + j];
                 args.y[int64_t(tok0 + j) * args.N + n] = __float2bfloat16_rn(v);
             }
+        }
+    }
+    if (abort_flag) {
+        // a wait gave up: a quarter of a second, in which the copies under way land
+        const long long t0 = clock64();
+        while (clock64() - t0 < kWaitTimeoutCycles / 8) {
         }
     }
 }
 
 template <bool kNv, int kStages>
-cudaError_t launch_matvec(const MatvecArgs &a, dim3 grid, cudaStream_t stream) {
+cudaError_t launch_matvec(const CUtensorMap &tmap_w, const MatvecArgs &a, dim3 grid, cudaStream_t stream) {
     const cudaError_t e =
-        set_max_dynamic_smem(reinterpret_cast<const void *>(fp4_matvec_kernel<kNv, kStages>), kMvMaxSmem);
+        set_max_dynamic_smem(reinterpret_cast<const void *>(fp4_matvec_kernel<kNv, kStages>), kMvMaxSmem - 16);
     if (e != cudaSuccess) return e;
-    return launch_pdl(fp4_matvec_kernel<kNv, kStages>, grid, dim3(kMvTeams * kMvWarps * 32),
-                      size_t(mv_fixed_bytes(kStages) + a.tokens * a.x_stride), stream, a);
+    return launch_pdl(fp4_matvec_kernel<kNv, kStages>, grid, dim3(kMvWarps * 32),
+                      size_t(mv_fixed_bytes(kNv, kStages) + a.tokens * a.x_stride), stream, tmap_w, a);
 }
 
 }  // namespace
@@ -338,17 +454,18 @@ extern "C" moe_status_t moe_fp4_matvec(const void *x_bf16, const void *w_fp4, co
     a.factors = {{512, 32, 2}, {4096, 256, 16}};
     // the tokens of a quarter-warp's 16-byte reads are 64 bytes apart modulo 128
     a.x_stride = (2 * K + 127) / 128 * 128 + 64;
-    const auto fits = [&](int stages) { return (kMvMaxSmem - mv_fixed_bytes(stages)) / a.x_stride; };
+    const bool nv = format == MOE_FP4_NVFP4;
+    const auto fits = [&](int stages) { return (kMvMaxSmem - 16 - mv_fixed_bytes(nv, stages)) / a.x_stride; };
     a.tokens = T < kMvTokens ? T : kMvTokens;
     if (a.tokens > fits(2)) a.tokens = fits(2);
-    a.slice = (K / 32 + kMvWarps - 1) / kMvWarps * 32;
     const int tiles = (N + kMvRows - 1) / kMvRows, sms = num_sms();
     const dim3 grid(unsigned(tiles < sms ? tiles : sms), unsigned((T + a.tokens - 1) / a.tokens));
-    const bool nv = format == MOE_FP4_NVFP4;
+    CUtensorMap tm;
+    if (!encode_bytes_rows(&tm, w_fp4, uint64_t(K / 2), uint64_t(N), kMvRows)) return MOE_ERR_CUDA;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     // as many stages in flight as the tokens leave room for
-    const cudaError_t e = a.tokens <= fits(4)   ? (nv ? launch_matvec<true, 4>(a, grid, st) : launch_matvec<false, 4>(a, grid, st))
-                          : a.tokens <= fits(3) ? (nv ? launch_matvec<true, 3>(a, grid, st) : launch_matvec<false, 3>(a, grid, st))
-                                                : (nv ? launch_matvec<true, 2>(a, grid, st) : launch_matvec<false, 2>(a, grid, st));
+    const cudaError_t e = a.tokens <= fits(4)   ? (nv ? launch_matvec<true, 4>(tm, a, grid, st) : launch_matvec<false, 4>(tm, a, grid, st))
+                          : a.tokens <= fits(3) ? (nv ? launch_matvec<true, 3>(tm, a, grid, st) : launch_matvec<false, 3>(tm, a, grid, st))
+                                                : (nv ? launch_matvec<true, 2>(tm, a, grid, st) : launch_matvec<false, 2>(tm, a, grid, st));
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

@@ -111,6 +111,10 @@ bool encode_bf16_rows(CUtensorMap *m, const void *base, uint64_t cols, uint64_t 
 bool encode_bf16_3d(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, uint64_t experts, int box_rows,
                     int box_cols = 64);
 
+// Tensor map of a row-major byte matrix [rows][cols], cols % 16 == 0: boxes of
+// 128 columns (128-byte swizzle) x box_rows rows.
+bool encode_bytes_rows(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, int box_rows);
+
 constexpr int kGroupedMaxWidth = 131072;  // features of a grouped product's operands, at most
 
 // Multiprocessors of the current device (cached per device).
