@@ -185,23 +185,15 @@ __global__ void __launch_bounds__(kMvWarps * 32, 1)
     // The tokens in fp16, a sixteenth of K per warp, in the order of the decoded
     // weights: NVFP4 elements 0 and 2, 1 and 3, 4 and 6, 5 and 7, MX elements 0 and
     // 4, 1 and 5, 2 and 6, 3 and 7.  First every token's largest magnitude, then
-    // the values; two tokens at a time, the next two on their way.
+    // the values.  A lane's first two 16-byte pieces of every token (all of it for K
+    // up to 8192) are asked for at once and stay in registers.
     float *amaxs = reinterpret_cast<float *>(after + kMvSumBytes + kMvWarps * kStages * 8);  // [warp][token]
     float *unscales = amaxs + kMvWarps * kMvTokens;                                            // [token]
     {
         const int x_lo = warp * units / kMvWarps * 32, x_hi = (warp + 1) * units / kMvWarps * 32;
-        const int k0 = x_lo + lane * 8, k1 = k0 + 256;  // two pieces of a token: all of a sixteenth of up to 512
+        const int k0 = x_lo + lane * 8, k1 = k0 + 256, rest = k0 + 512;
         const auto piece = [&](int j, int k) {
             return __ldg(reinterpret_cast<const uint4 *>(args.x + int64_t(tok0 + j) * args.K + k));
-        };
-        uint4 raw[2][2];
-        const auto fetch = [&](int j0) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                raw[j][0] = raw[j][1] = make_uint4(0, 0, 0, 0);
-                if (j0 + j < ntok && k0 < x_hi) raw[j][0] = piece(j0 + j, k0);
-                if (j0 + j < ntok && k1 < x_hi) raw[j][1] = piece(j0 + j, k1);
-            }
         };
         const auto largest = [](uint4 u, float amax) {
             const uint32_t v[4] = {u.x, u.y, u.z, u.w};
@@ -213,25 +205,6 @@ __global__ void __launch_bounds__(kMvWarps * 32, 1)
             }
             return amax;
         };
-        fetch(0);
-#pragma unroll 1
-        for (int j0 = 0; j0 < ntok; j0 += 2) {
-            const uint4 cur[2][2] = {{raw[0][0], raw[0][1]}, {raw[1][0], raw[1][1]}};
-            fetch(j0 + 2 < ntok ? j0 + 2 : 0);  // the values' loop begins with the first two
-            float amax[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                amax[j] = largest(cur[j][1], largest(cur[j][0], 0.0f));
-                if (j0 + j < ntok)
-                    for (int k = k1 + 256; k < x_hi; k += 256) amax[j] = largest(piece(j0 + j, k), amax[j]);
-            }
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) amax[j] = fmaxf(amax[j], __shfl_xor_sync(0xFFFFFFFFu, amax[j], d));
-            if (lane < 2) amaxs[warp * kMvTokens + j0 + lane] = lane ? amax[1] : amax[0];
-        }
-        __syncthreads();
         const auto put = [&](int j, int k, uint4 u, float mul) {
             const uint32_t v[4] = {u.x, u.y, u.z, u.w};
             uint32_t h[4];
@@ -244,27 +217,36 @@ __global__ void __launch_bounds__(kMvWarps * 32, 1)
             }
             *reinterpret_cast<uint4 *>(xs + j * args.x_stride + k * 2) = make_uint4(h[0], h[1], h[2], h[3]);
         };
-#pragma unroll 1
-        for (int j0 = 0; j0 < ntok; j0 += 2) {
-            const uint4 cur[2][2] = {{raw[0][0], raw[0][1]}, {raw[1][0], raw[1][1]}};
-            fetch(j0 + 2);
-            // lanes 0-15 the warps' largest of the first token, 16-31 of the second
-            float amax = amaxs[(lane & 15) * kMvTokens + j0 + (lane >> 4)];
+        uint4 raw[kMvTokens][2];
+#pragma unroll
+        for (int j = 0; j < kMvTokens; ++j) {
+            raw[j][0] = raw[j][1] = make_uint4(0, 0, 0, 0);
+            if (j < ntok && k0 < x_hi) raw[j][0] = piece(j, k0);
+            if (j < ntok && k1 < x_hi) raw[j][1] = piece(j, k1);
+        }
+#pragma unroll
+        for (int j = 0; j < kMvTokens; ++j) {
+            if (j >= ntok) break;
+            float amax = largest(raw[j][1], largest(raw[j][0], 0.0f));
+            for (int k = rest; k < x_hi; k += 256) amax = largest(piece(j, k), amax);
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+            if (lane == 0) amaxs[warp * kMvTokens + j] = amax;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kMvTokens; ++j) {
+            if (j >= ntok) break;
+            float amax = amaxs[(lane & 15) * kMvTokens + j];
 #pragma unroll
             for (int d = 8; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
             // 2^shift brings amax into [2^14, 2^15); both factors are normal numbers
             const int shift = min(max(14 - (int(__float_as_uint(amax) >> 23) - 127), -113), 126);
-            const float factor = amax > 0.0f ? __uint_as_float(uint32_t(127 + shift) << 23) : 1.0f;
-            if (warp == 0 && (lane & 15) == 0)
-                unscales[j0 + (lane >> 4)] = amax > 0.0f ? __uint_as_float(uint32_t(127 - shift) << 23) : 1.0f;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float mul = __shfl_sync(0xFFFFFFFFu, factor, 16 * j);
-                if (j0 + j >= ntok) break;
-                if (k0 < x_hi) put(j0 + j, k0, cur[j][0], mul);
-                if (k1 < x_hi) put(j0 + j, k1, cur[j][1], mul);
-                for (int k = k1 + 256; k < x_hi; k += 256) put(j0 + j, k, piece(j0 + j, k), mul);
-            }
+            const float mul = amax > 0.0f ? __uint_as_float(uint32_t(127 + shift) << 23) : 1.0f;
+            if (warp == 0 && lane == 0) unscales[j] = amax > 0.0f ? __uint_as_float(uint32_t(127 - shift) << 23) : 1.0f;
+            if (k0 < x_hi) put(j, k0, raw[j][0], mul);
+            if (k1 < x_hi) put(j, k1, raw[j][1], mul);
+            for (int k = rest; k < x_hi; k += 256) put(j, k, piece(j, k), mul);
         }
     }
     __syncthreads();

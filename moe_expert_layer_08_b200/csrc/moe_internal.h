@@ -131,14 +131,24 @@ moe_status_t use_device_of(const void *p);
 // is current again afterwards.
 struct DeviceScope {
     int prev = -1;
+    bool changed = false;
     moe_status_t status;
     explicit DeviceScope(const void *p) {
-        if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-        status = use_device_of(p);
+        cudaPointerAttributes attr;
+        if (cudaPointerGetAttributes(&attr, p) != cudaSuccess) {
+            cudaGetLastError();
+            status = MOE_ERR_INVALID_ARG;
+        } else if (attr.type != cudaMemoryTypeDevice && attr.type != cudaMemoryTypeManaged) {
+            status = MOE_ERR_INVALID_ARG;
+        } else if (cudaGetDevice(&prev) != cudaSuccess) {
+            status = MOE_ERR_CUDA;
+        } else {
+            changed = prev != attr.device;
+            status = !changed || cudaSetDevice(attr.device) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+        }
     }
     ~DeviceScope() {
-        int cur = -1;
-        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
+        if (changed) cudaSetDevice(prev);
     }
     DeviceScope(const DeviceScope &) = delete;
     DeviceScope &operator=(const DeviceScope &) = delete;
