@@ -58,15 +58,17 @@ struct GroupedCfg {
     static constexpr int kBBytes = kBRows * kBlockK * 2;
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr int kBufs = kTiles * kN <= 256 ? 2 : 1;        // accumulator buffers of a tile
-    static constexpr int kTmemCols = kN == 32 ? 64 * kTiles : kN == 64 ? 128 * kTiles : 512;
+    static constexpr int kTmemCols = kN == 64 ? 128 * kTiles : 512;
+    static constexpr bool kSplits = kN == 64 && kTiles == 1;        // may share an item's contraction among a cluster
     static constexpr int kMisc = 512;
-    static constexpr int kMaxStages = 6;
+    static constexpr int kMaxStages = 10;
     // barriers, the results' way out and the group table beside the stages
     static constexpr int fixed_bytes(int E) { return 1024 + kStageOutBytes + kMisc + 8 * (E + 1); }
     static constexpr int stages(int E) {
         return (kMaxSmem - fixed_bytes(E)) / kStageBytes < kMaxStages ? (kMaxSmem - fixed_bytes(E)) / kStageBytes : kMaxStages;
     }
     static_assert(stages(kMaxExperts) >= 3, "shared memory budget");
+    static_assert(!kSplits || kN * kTileRows * 4 <= 3 * kStageBytes, "a part's sums fit the ring");
     static_assert(kTiles * kBufs * kN <= kTmemCols, "TMEM allocation");
 };
 
@@ -80,6 +82,7 @@ struct GroupedArgs {
     int K;                // weight gradient: columns of dW
     int zero_unused;      // product, input gradient: write zeros to the rows of no expert
     int stages;           // of the operand ring
+    int split;            // parts of the contraction, the CTAs of a cluster (then one item per cluster)
 };
 
 // Shared-memory matrix descriptor, MN-major, 128-byte swizzle: boxes of 64 MN
@@ -197,6 +200,14 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 // Every thread of both CTAs.
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Two floats at this CTA's shared address `at`, of CTA `cta` of the cluster.
+__device__ __forceinline__ float2 cluster_load(uint32_t at, int cta) {
+    uint32_t remote;
+    float2 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(at), "r"(cta));
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(remote) : "memory");
+    return v;
 }
 // The first CTA's barrier at this CTA's address `bar`.
 __device__ __forceinline__ uint32_t leader_bar(uint64_t *bar) {
@@ -344,7 +355,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == 1) tmem_alloc_for<kPair>(tmem_holder, C::kTmemCols);
     const int rank = kPair ? int(cluster_rank()) : 0;  // blocks 2i and 2i + 1 are a pair
-    const int first = int(blockIdx.x) / kCtas, step = int(gridDim.x) / kCtas;
+    const int split = C::kSplits ? args.split : 1, cut = split > 1 ? int(cluster_rank()) : 0;
+    const int first = int(blockIdx.x) / (kCtas * split), step = int(gridDim.x) / (kCtas * split);
     constexpr int kItemStrip = C::kStrip * kCtas;
     const int strips = (args.D + kItemStrip - 1) / kItemStrip;
     pdl_wait();
@@ -404,6 +416,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // features of tile a of this CTA: the pair's tile a is its CTAs' 128 rows side by side
     auto tile_row = [&](const Item &it, int a) { return it.d0 + (kCtas * a + rank) * kTileRows; };
     auto two_tiles = [&](const Item &it) { return kTiles == 2 && it.d0 + kCtas * kTileRows < args.D; };
+    // this CTA's stages of an item
+    auto kb_lo = [&](const Item &it) { return C::kSplits ? it.kblocks * cut / split : 0; };
+    auto kb_hi = [&](const Item &it) { return C::kSplits ? it.kblocks * (cut + 1) / split : it.kblocks; };
     // stage kb of a weight gradient's item ends inside a 16-row step
     auto tail_stage = [](const Item &it, int kb) {
         return kMode == kGradWeight && kb == it.kblocks - 1 && it.tail % 16 != 0;
@@ -427,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int n_part = part(it), n0 = it.n0 + rank * n_part;
                 const int boxes_n = kNMn ? (n_part + 63) / 64 : (n_part + kRowBox - 1) / kRowBox;
                 const uint32_t bytes = uint32_t(tiles_m * kTileRows * 128 + boxes_n * (kNMn ? 64 : kRowBox) * 128);
-                for (int kb = 0; kb < it.kblocks; ++kb) {
+                for (int kb = kb_lo(it); kb < kb_hi(it); ++kb) {
                     if (!mbar_wait_cycles(&empty[stage], phase ^ 1u, abort_flag, err, 31)) {
                         ok = false;
                         break;
@@ -522,7 +537,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++li;
                 }
                 const uint32_t acc = tmem + uint32_t((buf * kTiles + a) * kN);
-                for (int kb = 0; kb < it.kblocks; ++kb) {
+                const int kb0 = kb_lo(it);
+                for (int kb = kb0; kb < kb_hi(it); ++kb) {
                     if (tail_stage(it, kb)) {
                         ok = wait(&zeroed[stage], zeroed_uses >> stage & 1u, 34);
                         zeroed_uses ^= 1u << stage;
@@ -543,9 +559,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int ks = 0; ks < steps; ++ks) {
                             const uint64_t ad = adesc + uint64_t(ks * (kMMn ? 128 : 2)), bd = bdesc + uint64_t(ks * (kNMn ? 128 : 2));
                             if constexpr (kPair)
-                                tc_mma_bf16_pair(acc, ad, bd, idesc, (kb | ks) ? 1u : 0u);
+                                tc_mma_bf16_pair(acc, ad, bd, idesc, kb > kb0 || ks ? 1u : 0u);
                             else
-                                tc_mma_bf16(acc, ad, bd, idesc, (kb | ks) ? 1u : 0u);
+                                tc_mma_bf16(acc, ad, bd, idesc, kb > kb0 || ks ? 1u : 0u);
                         }
                     }
                     commit(&empty[stage]);
@@ -635,6 +651,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++li;
             const uint32_t acc = tmem + (uint32_t(q * 32) << 16) + uint32_t((buf * kTiles + a) * kN);
             const int blocks = (it.cols + 31) / 32;
+            if (split > 1) {
+                // a part of the contraction: its fp32 sums, [column][128 features], to the
+                // ring (every stage of it has been consumed), for the whole cluster
+                float *sums = reinterpret_cast<float *>(tiles) + q * 32 + lane;
+#pragma unroll 1
+                for (int cb = group; cb < blocks; cb += kGroups)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t v[16];
+                        tmem_ld_32x16(acc + uint32_t(cb * 32 + half * 16), v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) sums[(cb * 32 + half * 16 + j) * kTileRows] = __uint_as_float(v[j]);
+                    }
+                break;
+            }
             // Everything that reads TMEM first, rounded and packed in pairs of columns,
             // so that the next item's MMAs wait for as little as they can.
             constexpr int kMine = (kN / 32 + kGroups - 1) / kGroups;
@@ -713,6 +745,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (kMode == kGradWeight && lane == 0) tma_store_wait_all();
         __syncwarp();
     }
+    if constexpr (C::kSplits)
+        if (split > 1) {
+            // the parts' sums, added in the order of the parts: every split-th column here
+            cluster_barrier();
+            if (warp >= 4 && first < num_items) {
+                const Item it = walk.at(first);
+                const int id = int(threadIdx.x) - 128, d = (id & 63) * 2;
+                for (int c = cut + split * (id >> 6); c < it.cols && it.d0 + d < args.D; c += split * (kEpiWarps / 2)) {
+                    const uint32_t at = smem_u32(reinterpret_cast<float *>(tiles) + c * kTileRows + d);
+                    float2 v = make_float2(0.0f, 0.0f);
+                    for (int p = 0; p < split; ++p) {
+                        const float2 u = cluster_load(at, p);
+                        v.x += u.x;
+                        v.y += u.y;
+                    }
+                    *reinterpret_cast<__nv_bfloat162 *>(args.out + int64_t(it.n0 + c) * args.D + it.d0 + d) =
+                        __floats2bfloat162_rn(v.x, v.y);
+                }
+            }
+            cluster_barrier();  // the other parts have read this CTA's sums
+        }
     tc_fence_before();
     if constexpr (kPair)
         cluster_barrier();  // the other CTA's MMAs, arrivals and commits for this one are over
@@ -729,8 +782,8 @@ cudaError_t launch_grouped(const CUtensorMap &tmap_m, const CUtensorMap &tmap_n,
     a.stages = C::stages(a.E);
     const cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(grouped_kernel<kMode, kN, kTiles>), kMaxSmem);
     if (e != cudaSuccess) return e;
-    const int64_t groups = num_sms() / C::kCtas;
-    const int grid = int(items < groups ? items : groups) * C::kCtas;
+    const int64_t groups = num_sms() / (C::kCtas * a.split);
+    const int grid = int(items < groups ? items : groups) * C::kCtas * a.split;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(grid));
     cfg.blockDim = dim3(kThreads);
@@ -740,28 +793,84 @@ cudaError_t launch_grouped(const CUtensorMap &tmap_m, const CUtensorMap &tmap_n,
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = unsigned(C::kCtas);
+    attr[1].val.clusterDim.x = unsigned(C::kCtas * a.split);
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = C::kPair ? 2 : 1;
+    cfg.numAttrs = C::kCtas * a.split > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, grouped_kernel<kMode, kN, kTiles>, tmap_m, tmap_n, tmap_out, a);
 }
 
+// A configuration of the product and the input gradient.
+struct Choice {
+    int kn, tiles, split;
+    int64_t items;  // at most, whatever the groups
+};
+
+// The one of the shortest time by an estimate in SM cycles from the sizes alone (the
+// groups are on the device: rows are taken as spread evenly over the experts).  A
+// stage costs the longest of its MMAs (2 cycles a column and tile), of the ring's
+// round trip (4500 cycles over its stages), and of what L2 delivers to all CTAs at
+// work (5300 bytes a cycle); an item its stages and the fill, longer with one
+// accumulator.  On 24 shapes from 1 x 1024 x 1024 to 16384 x 4096 x 2048, both
+// directions, its choice took 1.6 % more time than the best one in the mean and 25 %
+// at most.  Examples, product: 8 experts, 2048 rows, 1024 x 1024: 12.8 us with 160
+// columns and one tile, 19.8 with 256 and two; 48 experts, 6144 rows, 4096 x 7168:
+// 497 and 515; 16 experts, 16384 rows, 4096 x 2048: 313 and 203; 48 experts, 8 rows,
+// 4096 x 7168: 86 and 78, and 70 with 64 columns and two tiles.  A contraction in
+// parts: 16 rows, 4096 x 4096: 26.6 us whole, 16.9 in two, 12.7 in four.
+Choice choose(int R, int E, int D, int contraction) {
+    const int sms = num_sms(), kblocks = (contraction + kBlockK - 1) / kBlockK, experts = R < E ? R : E;
+    const double mean = double(R) / experts;
+    Choice best = {};
+    double best_time = 0;
+    for (int kn : {64, 160, 256})
+        for (int tiles = 1; tiles <= 2; ++tiles) {
+            const int ctas = kn >= 160 ? 2 : 1, units = sms / ctas;
+            const int64_t strips = (D + kTileRows * tiles * ctas - 1) / (kTileRows * tiles * ctas);
+            const int64_t most = (R + int64_t(experts) * (kn - 1)) / kn * strips;
+            const double chunks = mean <= kn ? 1.0 : mean / kn;
+            const double cols = mean / chunks < 16 ? 16 : mean / chunks;
+            const double items = experts * chunks * double(strips);
+            const double bytes = tiles * 16384.0 + ceil(cols / 32) * 4096 / ctas;
+            const double ring = floor(214000.0 / (tiles * 16384.0 + kn * 128.0 / ctas));
+            const double mma = 2.0 * tiles * cols < 280 ? 280 : 2.0 * tiles * cols;
+            for (int split = 1; split <= 8; split *= 2) {
+                // one item per cluster, and stages enough in each part
+                if (split > 1 && (kn > 64 || tiles > 1 || most * split > units || kblocks < 4 * split)) break;
+                const double at_work = items * split < units ? items * split : units;
+                const double l2 = bytes * at_work * ctas / 5300, trip = 4500 / ring;
+                const double stage = mma > l2 ? (mma > trip ? mma : trip) : (l2 > trip ? l2 : trip);
+                const double time = 3000 + ceil(items * split / units) * (stage * kblocks / split + (tiles * kn > 256 ? 2000 : 1000)) +
+                                    (split > 1 ? 2500 : 0);
+                if (best.kn == 0 || time < best_time) {
+                    best_time = time;
+                    best = {kn, tiles, split, most};
+                }
+            }
+        }
+    return best;
+}
+
 template <int kMode>
-cudaError_t launch_rows(int kn, const CUtensorMap &tm, const CUtensorMap &tn, const GroupedArgs &a, int64_t items,
-                        cudaStream_t stream) {
-    return kn == 32    ? launch_grouped<kMode, 32, 2>(tm, tn, tm, a, items, stream)
-           : kn == 64  ? launch_grouped<kMode, 64, 2>(tm, tn, tm, a, items, stream)
-           : kn == 160 ? launch_grouped<kMode, 160, 2>(tm, tn, tm, a, items, stream)
-                       : launch_grouped<kMode, 256, 2>(tm, tn, tm, a, items, stream);
+cudaError_t launch_rows(const CUtensorMap &tm, const CUtensorMap &tn, GroupedArgs a, cudaStream_t stream) {
+    const Choice c = choose(a.R, a.E, a.D, a.C);
+    a.split = c.split;
+    switch (c.kn + c.tiles) {
+        case 64 + 1: return launch_grouped<kMode, 64, 1>(tm, tn, tm, a, c.items, stream);
+        case 64 + 2: return launch_grouped<kMode, 64, 2>(tm, tn, tm, a, c.items, stream);
+        case 160 + 1: return launch_grouped<kMode, 160, 1>(tm, tn, tm, a, c.items, stream);
+        case 160 + 2: return launch_grouped<kMode, 160, 2>(tm, tn, tm, a, c.items, stream);
+        case 256 + 1: return launch_grouped<kMode, 256, 1>(tm, tn, tm, a, c.items, stream);
+        default: return launch_grouped<kMode, 256, 2>(tm, tn, tm, a, c.items, stream);
+    }
 }
 
 moe_status_t check_grouped(int R, int E, int N, int K) {
     if (R < 0 || E <= 0 || N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
     if (E > kMaxExperts || N % 8 || K % 8 || N > kGroupedMaxWidth || K > kGroupedMaxWidth) return MOE_ERR_UNSUPPORTED_SHAPE;
-    // every expert's items fit an int: strips <= 512, chunks <= R / 32 + E
-    if ((int64_t(R) / 32 + E) * ((int64_t(N > K ? N : K) + kTileRows - 1) / kTileRows) > 2000000000ll ||
+    // every expert's items fit an int: strips <= 1024, chunks <= R / 64 + E
+    if ((int64_t(R) / 64 + E) * ((int64_t(N > K ? N : K) + kTileRows - 1) / kTileRows) > 2000000000ll ||
         int64_t(E) * ((N + 255) / 256) * ((K + 255) / 256) > 2000000000ll)
         return MOE_ERR_UNSUPPORTED_SHAPE;
     return MOE_OK;
@@ -790,19 +899,12 @@ moe_status_t run_rows(bool grad, const void *rows, const void *w, const int32_t 
     a.C = grad ? N : K;
     a.K = K;
     a.zero_unused = zero_unused;
-    // columns of an item by the mean load: about the mean and three deviations of
-    // a uniform routing, so that most experts' weights are read by one item
-    const int64_t mean = R / E;
-    const int kn = mean <= 16 ? 32 : mean <= 40 ? 64 : mean <= 136 ? 160 : 256;
     CUtensorMap tm, tn;
     if (!encode_bf16_3d(&tm, w, uint64_t(K), uint64_t(N), uint64_t(E), grad ? kBlockK : kTileRows) ||
         !encode_bf16_rows(&tn, rows, uint64_t(a.C), uint64_t(R), kRowBox))
         return MOE_ERR_CUDA;
-    const int64_t chunks = int64_t(R) / kn + (R < E ? R : E);
-    const int64_t items = chunks * ((a.D + kTileRows - 1) / kTileRows);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = grad ? launch_rows<kGradInput>(kn, tm, tn, a, items, st)
-                               : launch_rows<kProduct>(kn, tm, tn, a, items, st);
+    const cudaError_t e = grad ? launch_rows<kGradInput>(tm, tn, a, st) : launch_rows<kProduct>(tm, tn, a, st);
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -862,8 +964,12 @@ moe_status_t moe_grouped_matmul_grad_weight(const void *dy_bf16, const void *x_b
         !encode_bf16_rows(&tn, x_bf16, uint64_t(K), uint64_t(R), kBlockK) ||
         !encode_bf16_3d(&to, dw_bf16, uint64_t(K), uint64_t(N), uint64_t(E), 32, 32))
         return MOE_ERR_CUDA;
-    const int64_t items = int64_t(E) * ((N + kTileRows - 1) / kTileRows) * ((K + 255) / 256);
-    const cudaError_t e = launch_grouped<kGradWeight, 256, 2>(tm, tn, to, a, items, st);
+    a.split = 1;
+    // strips of 512 rows of dW per pair, or of 256 while they would leave most pairs
+    // idle (2 experts of 512 x 512, 4096 rows: 26.3 -> 20.9 us; at 64 items 11.6 against 12.5)
+    const int64_t items = int64_t(E) * ((N + 511) / 512) * ((K + 255) / 256);
+    const cudaError_t e = items <= 32 ? launch_grouped<kGradWeight, 256, 1>(tm, tn, to, a, 2 * items, st)
+                                      : launch_grouped<kGradWeight, 256, 2>(tm, tn, to, a, items, st);
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
