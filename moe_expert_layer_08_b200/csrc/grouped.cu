@@ -808,47 +808,48 @@ struct Choice {
 };
 
 // The one of the shortest time by an estimate in SM cycles from the sizes alone (the
-// groups are on the device: rows are taken as spread evenly over the experts).  A
-// stage costs the longest of its MMAs (2 cycles a column and tile), of the ring's
-// round trip (4500 cycles over its stages), and of what L2 delivers to all CTAs at
-// work (5300 bytes a cycle); an item its stages and the fill, longer with one
-// accumulator.  On 24 shapes from 1 x 1024 x 1024 to 16384 x 4096 x 2048, both
-// directions, its choice took 1.6 % more time than the best one in the mean and 25 %
-// at most.  Examples, product: 8 experts, 2048 rows, 1024 x 1024: 12.8 us with 160
-// columns and one tile, 19.8 with 256 and two; 48 experts, 6144 rows, 4096 x 7168:
-// 497 and 515; 16 experts, 16384 rows, 4096 x 2048: 313 and 203; 48 experts, 8 rows,
-// 4096 x 7168: 86 and 78, and 70 with 64 columns and two tiles.  A contraction in
-// parts: 16 rows, 4096 x 4096: 26.6 us whole, 16.9 in two, 12.7 in four.
+// groups are on the device: half of the experts are taken to have 3/4 of the mean
+// load, half 5/4).  A stage costs the longest of its MMAs (2 cycles a column and
+// tile), of the ring's round trip (4000 cycles over its stages), and of what L2
+// delivers to all CTAs at work (4840 bytes a cycle); an item its stages and the fill,
+// longer with one accumulator.  On 37 loads, even and Zipf-like, from 1 x 1024 x 1024
+// to 16384 x 4096 x 2048, both directions, its choice took 2.3 % more time than the
+// best one in the mean and 25 % at most.  Examples, product: 8 experts, 2048 rows,
+// 1024 x 1024: 12.8 us with 160 columns and one tile, 19.8 with 256 and two; 16
+// experts, 16384 rows, 4096 x 2048: 313 and 203; 48 experts, 8 rows, 4096 x 7168: 86
+// and 78, and 70 with 64 columns and two tiles.  A contraction in parts: 16 rows,
+// 4096 x 4096: 26.6 us whole, 16.9 in two, 12.7 in four.
 Choice choose(int R, int E, int D, int contraction) {
     const int sms = num_sms(), kblocks = (contraction + kBlockK - 1) / kBlockK, experts = R < E ? R : E;
     const double mean = double(R) / experts;
+    auto larger = [](double a, double b) { return a > b ? a : b; };
     Choice best = {};
     double best_time = 0;
-    for (int kn : {64, 160, 256})
+    for (int kn : {64, 160, 256}) {
+        if (kn > 64 && mean <= 16) break;  // 48 experts, 8 rows, Zipf-like: 46.0 us, 54.9 with 160 columns
         for (int tiles = 1; tiles <= 2; ++tiles) {
             const int ctas = kn >= 160 ? 2 : 1, units = sms / ctas;
             const int64_t strips = (D + kTileRows * tiles * ctas - 1) / (kTileRows * tiles * ctas);
             const int64_t most = (R + int64_t(experts) * (kn - 1)) / kn * strips;
-            const double chunks = mean <= kn ? 1.0 : mean / kn;
-            const double cols = mean / chunks < 16 ? 16 : mean / chunks;
-            const double items = experts * chunks * double(strips);
-            const double bytes = tiles * 16384.0 + ceil(cols / 32) * 4096 / ctas;
-            const double ring = floor(214000.0 / (tiles * 16384.0 + kn * 128.0 / ctas));
-            const double mma = 2.0 * tiles * cols < 280 ? 280 : 2.0 * tiles * cols;
+            const double chunks =
+                experts == 1 ? (R + int64_t(kn) - 1) / kn : (larger(1.0, 0.75 * mean / kn) + larger(1.0, 1.25 * mean / kn)) / 2;
+            const double cols = larger(16.0, mean / chunks), items = experts * chunks * double(strips);
+            const double bytes = tiles * 16384 + int((cols + 31) / 32) * 4096.0 / ctas;
+            const int ring = 214000 / (tiles * 16384 + kn * 128 / ctas);
+            const double mma = larger(280.0, 2.0 * tiles * cols);
             for (int split = 1; split <= 8; split *= 2) {
                 // one item per cluster, and stages enough in each part
                 if (split > 1 && (kn > 64 || tiles > 1 || most * split > units || kblocks < 4 * split)) break;
-                const double at_work = items * split < units ? items * split : units;
-                const double l2 = bytes * at_work * ctas / 5300, trip = 4500 / ring;
-                const double stage = mma > l2 ? (mma > trip ? mma : trip) : (l2 > trip ? l2 : trip);
-                const double time = 3000 + ceil(items * split / units) * (stage * kblocks / split + (tiles * kn > 256 ? 2000 : 1000)) +
-                                    (split > 1 ? 2500 : 0);
+                const double rounds = larger(1.0, items * split / units), at_work = items * split < units ? items * split : units;
+                const double stage = larger(larger(mma, 4000.0 / ring), bytes * at_work * ctas / 4840);
+                const double time = 3000 + rounds * (stage * kblocks / split + (tiles * kn > 256 ? 2000 : 1000)) + (split > 1 ? 2500 : 0);
                 if (best.kn == 0 || time < best_time) {
                     best_time = time;
                     best = {kn, tiles, split, most};
                 }
             }
         }
+    }
     return best;
 }
 

@@ -87,12 +87,12 @@ def test_products_and_gradients(moe, sizes, N, K, before, behind):
 
 @pytest.mark.parametrize("turned", [False, True])  # for the input gradient as for the product
 @pytest.mark.parametrize("sizes,N,K", [
-    # the product's contraction in 8, 4, 4 and 2 parts
+    # the contraction in 8 and in 4 parts (in 2: [10] * 20, turned)
     ([33], 264, 2056), ([1], 264, 1032), ([9, 0, 5, 26], 264, 1032), ([70, 1], 1032, 520),
     # 64, 160 and 256 columns, each with one tile a strip and with two
     ([50, 0, 250], 520, 264), ([10] * 20, 1032, 136),
-    ([90, 0, 210], 4096, 264), ([130] * 19 + [131], 1032, 136),
-    ([190, 0, 150, 300, 200, 260, 300], 2056, 136), ([250, 150] * 10, 1032, 136),
+    ([90, 0, 210], 4096, 264), ([130] * 19 + [131], 1032, 136), ([80, 130, 50, 0, 88, 110, 100, 42], 4096, 264),
+    ([190, 0, 150, 300, 200, 260, 300], 2056, 136), ([250, 150] * 10, 1032, 136), ([1990, 0], 4096, 136),
 ])
 def test_every_shape_of_a_work_item(moe, sizes, N, K, turned):
     check_all(moe, sizes, *((K, N) if turned else (N, K)), before=3, behind=9, seed=3)
