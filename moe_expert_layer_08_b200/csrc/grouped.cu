@@ -429,16 +429,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         if (lane == 0) {
             // ------------------------------------------------------------ loads
-            // the M side of product and input gradient is the weights: one expert's
-            // are read by the row chunks of a block at about the same time
-            const uint64_t pol_m = kN < 256 ? policy_evict_first() : policy_evict_last();
-            const uint64_t pol_n = policy_evict_last();
+            const uint64_t pol_once = policy_evict_first(), pol_n = policy_evict_last();
             int stage = 0;
             uint32_t phase = 0, filled = 0, fill_parity = 0;
             bool ok = true;
             for (int u = first; ok && u < num_items; u += step) {
                 const Item it = walk.at(u);
                 const int tiles_m = two_tiles(it) ? 2 : 1;
+                // the weights are read once, or by an expert's row chunks at about the same
+                // time (64 experts of 32 rows, 1024 x 1024: 29.8 us, 33.4 with all to be kept)
+                const uint64_t pol_m = row_of[it.e + 1] - row_of[it.e] <= kN ? pol_once : pol_n;
                 const int n_part = part(it), n0 = it.n0 + rank * n_part;
                 const int boxes_n = kNMn ? (n_part + 63) / 64 : (n_part + kRowBox - 1) / kRowBox;
                 const uint32_t bytes = uint32_t(tiles_m * kTileRows * 128 + boxes_n * (kNMn ? 64 : kRowBox) * 128);
@@ -812,8 +812,8 @@ struct Choice {
 // load, half 5/4).  A stage costs the longest of its MMAs (2 cycles a column and
 // tile), of the ring's round trip (4000 cycles over its stages), and of what L2
 // delivers to all CTAs at work (4840 bytes a cycle); an item its stages and the fill,
-// longer with one accumulator.  On 37 loads, even and Zipf-like, from 1 x 1024 x 1024
-// to 16384 x 4096 x 2048, both directions, its choice took 2.3 % more time than the
+// longer with one accumulator.  On 40 loads, even and Zipf-like, from 1 x 1024 x 1024
+// to 16384 x 4096 x 2048, both directions, its choice took 1.5 % more time than the
 // best one in the mean and 25 % at most.  Examples, product: 8 experts, 2048 rows,
 // 1024 x 1024: 12.8 us with 160 columns and one tile, 19.8 with 256 and two; 16
 // experts, 16384 rows, 4096 x 2048: 313 and 203; 48 experts, 8 rows, 4096 x 7168: 86
@@ -827,7 +827,7 @@ Choice choose(int R, int E, int D, int contraction) {
     double best_time = 0;
     for (int kn : {64, 160, 256}) {
         if (kn > 64 && mean <= 16) break;  // 48 experts, 8 rows, Zipf-like: 46.0 us, 54.9 with 160 columns
-        for (int tiles = 1; tiles <= 2; ++tiles) {
+        for (int tiles = 1; tiles <= (kn == 160 ? 1 : 2); ++tiles) {
             const int ctas = kn >= 160 ? 2 : 1, units = sms / ctas;
             const int64_t strips = (D + kTileRows * tiles * ctas - 1) / (kTileRows * tiles * ctas);
             const int64_t most = (R + int64_t(experts) * (kn - 1)) / kn * strips;
@@ -861,7 +861,6 @@ cudaError_t launch_rows(const CUtensorMap &tm, const CUtensorMap &tn, GroupedArg
         case 64 + 1: return launch_grouped<kMode, 64, 1>(tm, tn, tm, a, c.items, stream);
         case 64 + 2: return launch_grouped<kMode, 64, 2>(tm, tn, tm, a, c.items, stream);
         case 160 + 1: return launch_grouped<kMode, 160, 1>(tm, tn, tm, a, c.items, stream);
-        case 160 + 2: return launch_grouped<kMode, 160, 2>(tm, tn, tm, a, c.items, stream);
         case 256 + 1: return launch_grouped<kMode, 256, 1>(tm, tn, tm, a, c.items, stream);
         default: return launch_grouped<kMode, 256, 2>(tm, tn, tm, a, c.items, stream);
     }
