@@ -87,6 +87,8 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
+}  // namespace
+
 // FP4 weight bodies as a 4D tensor of 4-bit elements (128 K, rows, tile a,
 // K block b); a box (128, box_rows, box_a, kblocks) lands in shared memory as
 // 128-row slots b * 2 + a, each element expanded to one byte, 128-byte
@@ -107,6 +109,8 @@ bool encode_weights4(CUtensorMap *m, const void *base, uint64_t rows, uint64_t r
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+namespace {
 
 // NVFP4 packets: bodies as bytes (128 B, 128 rows, slot, K-tile pair), box
 // (128, 128, 2, 1) = both tiles of one 256-K block; their scale images as
@@ -238,6 +242,34 @@ cudaError_t set_max_dynamic_smem(const void *kernel, int bytes) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess) done.push_back({kernel, dev, bytes});
     return e;
+}
+
+int resident_clusters(const void *kernel, int size, int threads, int smem) {
+    static std::mutex mu;
+    static int cache[64][9] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const int all = num_sms() / size;
+    if (size < 2 || size > 8 || dev < 0 || dev >= 64) return all;
+    std::lock_guard<std::mutex> g(mu);
+    int &n = cache[dev][size];
+    if (n == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(unsigned(all * size));
+        cfg.blockDim = dim3(unsigned(threads));
+        cfg.dynamicSmemBytes = size_t(smem);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = unsigned(size);
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int found = 0;
+        if (cudaOccupancyMaxActiveClusters(&found, kernel, &cfg) != cudaSuccess) cudaGetLastError();
+        n = found > 0 && found < all ? found : all;
+    }
+    return n;
 }
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }

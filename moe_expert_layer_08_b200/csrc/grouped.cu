@@ -819,6 +819,7 @@ struct Choice {
 // experts, 16384 rows, 4096 x 2048: 313 and 203; 48 experts, 8 rows, 4096 x 7168: 86
 // and 78, and 70 with 64 columns and two tiles.  A contraction in parts: 16 rows,
 // 4096 x 4096: 26.6 us whole, 16.9 in two, 12.7 in four.
+template <int kMode>
 Choice choose(int R, int E, int D, int contraction) {
     const int sms = num_sms(), kblocks = (contraction + kBlockK - 1) / kBlockK, experts = R < E ? R : E;
     const double mean = double(R) / experts;
@@ -839,7 +840,10 @@ Choice choose(int R, int E, int D, int contraction) {
             const double mma = larger(280.0, 2.0 * tiles * cols);
             for (int split = 1; split <= 8; split *= 2) {
                 // one item per cluster, and stages enough in each part
-                if (split > 1 && (kn > 64 || tiles > 1 || most * split > units || kblocks < 4 * split)) break;
+                if (split > 1 && (kn > 64 || tiles > 1 || kblocks < 4 * split ||
+                                  most > resident_clusters(reinterpret_cast<const void *>(grouped_kernel<kMode, 64, 1>), split,
+                                                           kThreads, kMaxSmem)))
+                    break;
                 const double rounds = larger(1.0, items * split / units), at_work = items * split < units ? items * split : units;
                 const double stage = larger(larger(mma, 4000.0 / ring), bytes * at_work * ctas / 4840);
                 const double time = 3000 + rounds * (stage * kblocks / split + (tiles * kn > 256 ? 2000 : 1000)) + (split > 1 ? 2500 : 0);
@@ -855,7 +859,9 @@ Choice choose(int R, int E, int D, int contraction) {
 
 template <int kMode>
 cudaError_t launch_rows(const CUtensorMap &tm, const CUtensorMap &tn, GroupedArgs a, cudaStream_t stream) {
-    const Choice c = choose(a.R, a.E, a.D, a.C);
+    const cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(grouped_kernel<kMode, 64, 1>), kMaxSmem);
+    if (e != cudaSuccess) return e;
+    const Choice c = choose<kMode>(a.R, a.E, a.D, a.C);
     a.split = c.split;
     switch (c.kn + c.tiles) {
         case 64 + 1: return launch_grouped<kMode, 64, 1>(tm, tn, tm, a, c.items, stream);

@@ -425,6 +425,10 @@ extern "C" moe_status_t moe_fp4_matvec(const void *x_bf16, const void *w_fp4, co
         return MOE_ERR_INVALID_ARG;
     DeviceScope dev(y_bf16);
     if (dev.status != MOE_OK) return dev.status;
+    cudaError_t e = cudaSuccess;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (format == MOE_FP4_MX && fp4_matvec_mx(x_bf16, w_fp4, w_sf, y_bf16, T, N, K, st, &e))
+        return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     MatvecArgs a{};
     a.x = static_cast<const __nv_bfloat16 *>(x_bf16);
     a.w = static_cast<const uint8_t *>(w_fp4);
@@ -444,10 +448,9 @@ extern "C" moe_status_t moe_fp4_matvec(const void *x_bf16, const void *w_fp4, co
     const dim3 grid(unsigned(tiles < sms ? tiles : sms), unsigned((T + a.tokens - 1) / a.tokens));
     CUtensorMap tm;
     if (!encode_bytes_rows(&tm, w_fp4, uint64_t(K / 2), uint64_t(N), kMvRows)) return MOE_ERR_CUDA;
-    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     // as many stages in flight as the tokens leave room for
-    const cudaError_t e = a.tokens <= fits(4)   ? (nv ? launch_matvec<true, 4>(tm, a, grid, st) : launch_matvec<false, 4>(tm, a, grid, st))
-                          : a.tokens <= fits(3) ? (nv ? launch_matvec<true, 3>(tm, a, grid, st) : launch_matvec<false, 3>(tm, a, grid, st))
-                                                : (nv ? launch_matvec<true, 2>(tm, a, grid, st) : launch_matvec<false, 2>(tm, a, grid, st));
+    e = a.tokens <= fits(4)   ? (nv ? launch_matvec<true, 4>(tm, a, grid, st) : launch_matvec<false, 4>(tm, a, grid, st))
+        : a.tokens <= fits(3) ? (nv ? launch_matvec<true, 3>(tm, a, grid, st) : launch_matvec<false, 3>(tm, a, grid, st))
+                              : (nv ? launch_matvec<true, 2>(tm, a, grid, st) : launch_matvec<false, 2>(tm, a, grid, st));
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

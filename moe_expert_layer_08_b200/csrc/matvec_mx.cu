@@ -1,0 +1,504 @@
+// matvec_mx.cu -- the product of a few bf16 token vectors with an MX weight
+// matrix (E2M1 codes, one UE8M0 scale per 32) for K a multiple of 128:
+//   y[t, n] = sum_k x[t, k] * s[n, k / 32] * c[n, k]
+// bound by the HBM stream of N K (1/2 + 1/32) bytes once nothing is done per
+// weight.  (Decoding the codes in registers for mma.sync is bound by the integer
+// pipe, at a third of that stream.)  So the tensor cores take the codes and their
+// scales as they are: tcgen05.mma.kind::mxf8f6f4 with the weights as its 128-row
+// E2M1 operand, and everything else is per token, once.
+//
+// The tokens are the E4M3 operand, each element as four columns whose scales carry
+// the piece's weight: with 2^e the smallest power with max|x| <= 448 * 2^e over the
+// element's 32,
+//   x 2^-e = p0 + 2^-4 p1 + 2^-22 p2 + 2^-26 p3,
+// each piece the rounding of what the ones before it left.  p0 and p1 hold an
+// element of at least 2^-6 exactly (four bits each of bf16's eight), p2 and p3 what
+// is below E4M3's subnormals: an element is off by at most 2^-36 * 2^e, 2^-43 of the
+// largest of its 32.  Exponents are taken relative to the token's largest element in
+// this block's part of K, whose power of two multiplies the fp32 sums at the end.
+// E4M3 has no infinities: an element that is not finite enters as zero and its
+// token's results are computed again by definition.
+//
+// A block streams tiles of up to 128 rows and a part of K, 128 elements a stage, in
+// its shared memory by TMA (which spreads the 4-bit codes to bytes) with the stage's
+// scales by cp.async beside them; blocks of a cluster have the parts of K of the same
+// rows, add their fp32 sums in part order through distributed shared memory, and have
+// their part of the tokens prepared once, for all their tiles.  A tcgen05 instruction
+// costs its thread about 70 cycles, so four threads issue, each a quarter of a tile's
+// stages into an accumulator of its own.  The rows of a tile are as few as fill every
+// cluster equally often.
+// N = 14336, K = 7168: 19.7 us for one token, 27.0 for eight (26.0 and 30.6 by mma.sync).
+#include "moe_common.cuh"
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int kMxBlockK = 128;       // K elements of a stage
+constexpr int kMxStageBytes = kTileRows * 128;  // codes, a byte each
+constexpr int kMxPieces = 4;         // of a token's element: MMA columns
+constexpr int kMxTokens = 8;         // of a pass
+constexpr int kMxIssuers = 4;
+constexpr int kMxMaxStages = 12;    // a multiple of the issuers: a ring slot is always the same one's
+constexpr int kMxMaxParts = 8;
+constexpr int kMxSmem = 232448;
+// warps: 0 loads codes, 1-4 scales (a thread a row), 5-19 prepare the tokens, then
+// 5-8 issue and 16-19 drain
+constexpr int kMxThreads = 20 * 32;
+constexpr int kMxPrepWarp = 5, kMxPrepWarps = 15, kMxEpiWarp = 16;
+constexpr int kMxHeld = 8;           // pieces of the tokens a preparing warp holds in registers
+// TMEM columns: two accumulators per issuer, the stages' scale images, the tokens'
+constexpr int kMxAccCols = kMxPieces * kMxTokens;  // a multiple of 16
+constexpr int kMxSfaCol = 2 * kMxIssuers * kMxAccCols;
+constexpr int kMxSfbCol = kMxSfaCol + 4 * kMxMaxStages;
+constexpr int kMxMaxBlocks = (512 - kMxSfbCol) / 4;  // stages of a part
+static_assert(kMxEpiWarp % 4 == 0 && kMxMaxBlocks >= 52, "TMEM");
+constexpr int kMxMisc = 512;
+
+struct MxArgs {
+    const __nv_bfloat16 *x;   // [T, K]
+    const uint8_t *w;         // [N, K / 2]
+    const uint8_t *sf;        // [N, K / 32]
+    __nv_bfloat16 *y;         // [T, N]
+    int T, N, K;
+    int tokens;               // of a pass (blockIdx.y), <= kMxTokens
+    int cols;                 // of the tokens' operand in shared memory, a multiple of 8
+    int rows;                 // of a tile, a multiple of 8
+    int parts;                // of K: blocks of a cluster
+    int blocks;               // stages of a part, at most
+    int rounds;               // tiles of a cluster, at most
+    int stages;
+};
+int mx_smem_bytes(const MxArgs &a, int stages) {
+    return 1024 + stages * (kMxStageBytes + kSfBlockBytes) + a.blocks * (a.cols * 128 + kSfBlockBytes) +
+           a.rounds * a.tokens * kTileRows * 4 + kMxMisc;
+}
+
+__device__ int g_matvec_mx_err[8];  // where a wait that gave up leaves its mark (the outputs become NaN)
+
+__device__ __forceinline__ uint32_t cluster_rank_of() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_word(uint32_t at, int cta) {
+    uint32_t remote, v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(at), "r"(cta));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_meet() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_ld_4(uint32_t addr, float (&r)[4]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ bool mx_warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int where) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait_cycles(bar, parity, abort, g_matvec_mx_err, where));
+}
+// The four bf16 of two words; elements that are not finite as zeros.
+__device__ __forceinline__ bool finite4(uint2 u, float (&v)[4]) {
+    v[0] = __uint_as_float(u.x << 16), v[1] = __uint_as_float(u.x & 0xFFFF0000u);
+    v[2] = __uint_as_float(u.y << 16), v[3] = __uint_as_float(u.y & 0xFFFF0000u);
+    bool fine = true;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (!(fabsf(v[i]) <= 3.4e38f)) {
+            v[i] = 0.0f;
+            fine = false;
+        }
+    return fine;
+}
+__device__ __forceinline__ float largest4(const float (&v)[4]) {
+    return fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+}
+// E4M3 codes of v, and v - codes in v.
+__device__ __forceinline__ uint32_t take_piece(float (&v)[4]) {
+    const uint32_t p = to_e4m3x4(v);
+    const __half2 a = __half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(p & 0xFFFFu), __NV_E4M3));
+    const __half2 b = __half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(p >> 16), __NV_E4M3));
+    v[0] -= __low2float(a), v[1] -= __high2float(a), v[2] -= __low2float(b), v[3] -= __high2float(b);
+    return p;
+}
+// Token exponents are at least this: bf16's smallest subnormal is exact in the pieces there.
+constexpr int kMxLowExponent = -101;
+
+__global__ void __launch_bounds__(kMxThreads, 1)
+    fp4_matvec_mx_kernel(const __grid_constant__ CUtensorMap tmap_w, const MxArgs args) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int kStages = args.stages;
+    uint8_t *toks = ring + kStages * kMxStageBytes;                    // [block][column] 128 bytes, swizzled
+    uint8_t *sfa = toks + args.blocks * args.cols * 128;               // [stage] images
+    uint8_t *sfb = sfa + kStages * kSfBlockBytes;                      // [block] images
+    float *sums = reinterpret_cast<float *>(sfb + args.blocks * kSfBlockBytes);  // [round][token][row]
+    uint64_t *full = reinterpret_cast<uint64_t *>(sums + args.rounds * args.tokens * kTileRows);
+    uint64_t *empty = full + kMxMaxStages;
+    uint64_t *tmem_full = empty + kMxMaxStages;   // [2]
+    uint64_t *tmem_empty = tmem_full + 2;         // [2]
+    uint64_t *mma_done = tmem_empty + 2;          // [issuer]
+    uint64_t *sfb_done = mma_done + kMxIssuers;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(sfb_done + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+    uint32_t *bad = tmem_holder + 2;              // tokens with an element that is not finite
+    uint32_t *tok_max = bad + 1;                  // [token]
+    static_assert((2 * kMxMaxStages + 4 + kMxIssuers + 1) * 8 + (3 + kMxTokens) * 4 <= kMxMisc, "barriers and flags");
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int parts = args.parts, part = parts > 1 ? int(cluster_rank_of()) : 0;
+    const int all_blocks = args.K / kMxBlockK;
+    const int kb0 = part * all_blocks / parts, blocks = (part + 1) * all_blocks / parts - kb0;
+    const int tiles = (args.N + args.rows - 1) / args.rows;
+    const int first = int(blockIdx.x) / parts, step = int(gridDim.x) / parts;
+    const int tok0 = int(blockIdx.y) * args.tokens, ntok = min(args.tokens, args.T - tok0);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1 + 128);  // the codes' copy, the threads that bring scales
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tmem_full[b], kMxIssuers);
+            mbar_init(&tmem_empty[b], 4);
+        }
+        for (int i = 0; i < kMxIssuers; ++i) mbar_init(&mma_done[i], 1);
+        mbar_init(sfb_done, 1);
+        *abort_flag = 0;
+        *bad = 0;
+        for (int t = 0; t < kMxTokens; ++t) tok_max[t] = 0;
+        fence_mbar_init();
+        prefetch_tmap(&tmap_w);
+    }
+    if (warp == kMxPrepWarp) {
+        tmem_alloc(tmem_holder, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    pdl_wait();
+    if (threadIdx.x == 0) pdl_trigger();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ------------------------------------------------------------ codes
+            const uint64_t pol = policy_evict_first();
+            int stage = 0, used = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int tile = first; ok && tile < tiles; tile += step)
+                for (int kb = 0; kb < blocks; ++kb) {
+                    if (!mbar_wait_cycles(&empty[stage], phase ^ 1u, abort_flag, g_matvec_mx_err, 71)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&full[stage], uint32_t(args.rows * 64));
+                    tma_load_4d(ring + stage * kMxStageBytes, &tmap_w, &full[stage], 0, tile * args.rows, 0, kb0 + kb, pol);
+                    if (used < kStages) ++used;
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            // Every copy has landed once its stage is consumed; after a wait that gave
+            // up nothing consumes them: a quarter of a second, in which copies land.
+            for (int i = 0; i < used; ++i) {
+                if (--stage < 0) {
+                    stage = kStages - 1;
+                    phase ^= 1u;
+                }
+                mbar_wait_cycles(&empty[stage], phase, abort_flag, g_matvec_mx_err, 72);
+            }
+            if (*abort_flag) {
+                const long long t0 = clock64();
+                while (clock64() - t0 < kWaitTimeoutCycles / 8) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp < kMxPrepWarp) {
+        // ---------------------------------------------------------------- scales: thread = row
+        // four bytes a stage, to row r's place in the image: (r % 32) * 16 + (r / 32) * 4
+        const int r = int(threadIdx.x) - 32;
+        const int64_t ld = args.K / 32;
+        const uint32_t dst = smem_u32(sfa) + uint32_t((r & 31) * 16 + (r >> 5) * 4);
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int tile = first; ok && tile < tiles; tile += step) {
+            const int n = tile * args.rows + r;
+            const bool real = r < args.rows && n < args.N;
+            const uint8_t *src = args.sf + (real ? n * ld : 0) + kb0 * 4;
+            for (int kb = 0; kb < blocks; ++kb) {
+                if (!mx_warp_wait(&empty[stage], phase ^ 1u, abort_flag, 73)) {
+                    ok = false;
+                    break;
+                }
+                if (real)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + stage * kSfBlockBytes), "l"(src + kb * 4)
+                                 : "memory");
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&full[stage])) : "memory");
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+        // ---------------------------------------------------------------- tokens
+        // a unit is a stage's 128 elements of a token, four per lane
+        const int units = blocks * ntok, w0 = warp - kMxPrepWarp;
+        auto fetch = [&](int u) {
+            return __ldg(reinterpret_cast<const uint2 *>(args.x + int64_t(tok0 + u % ntok) * args.K +
+                                                         (kb0 + u / ntok) * kMxBlockK + lane * 4));
+        };
+        auto note = [&](int u, uint2 raw) {
+            float v[4];
+            const bool fine = finite4(raw, v);
+            const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(largest4(v)));
+            const bool all_fine = __all_sync(0xFFFFFFFFu, fine);
+            if (lane == 0) {
+                atomicMax(&tok_max[u % ntok], top);
+                if (!all_fine) atomicOr(bad, 1u << (u % ntok));
+            }
+        };
+        auto put = [&](int u, uint2 raw) {
+            const int t = u % ntok, kb = u / ntok;
+            float v[4];
+            finite4(raw, v);
+            float amax = largest4(v);
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+            const int shift = max(scale_exponent<true>(__uint_as_float(tok_max[t])), kMxLowExponent);
+            // never more than 101 below the token's, where the last piece's scale is 2^-127
+            const int e = amax > 0.0f ? max(max(scale_exponent<true>(amax), kMxLowExponent), shift - 101) : shift;
+            const float m = exp2_neg(e);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] *= m;
+            uint8_t *to = toks + kb * args.cols * 128 + (lane & 3) * 4;
+            uint8_t *image = sfb + kb * kSfBlockBytes + (lane >> 3);
+#pragma unroll
+            for (int p = 0; p < kMxPieces; ++p) {
+                const int col = kMxPieces * t + p;
+                *reinterpret_cast<uint32_t *>(to + col * 128 + (((lane >> 2) ^ (col & 7)) << 4)) = take_piece(v);
+                const float next = p == 1 ? 262144.0f : 16.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] *= next;
+                if ((lane & 7) == 0) image[col * 16] = uint8_t(e - shift + 127 - (p == 0 ? 0 : p == 1 ? 4 : p == 2 ? 22 : 26));
+            }
+        };
+        uint2 held[kMxHeld];
+#pragma unroll
+        for (int i = 0; i < kMxHeld; ++i)
+            if (w0 + i * kMxPrepWarps < units) held[i] = fetch(w0 + i * kMxPrepWarps);
+#pragma unroll
+        for (int i = 0; i < kMxHeld; ++i)
+            if (w0 + i * kMxPrepWarps < units) note(w0 + i * kMxPrepWarps, held[i]);
+        for (int u = w0 + kMxHeld * kMxPrepWarps; u < units; u += kMxPrepWarps) note(u, fetch(u));
+        asm volatile("bar.sync 1, %0;" ::"n"(kMxPrepWarps * 32) : "memory");
+#pragma unroll
+        for (int i = 0; i < kMxHeld; ++i)
+            if (w0 + i * kMxPrepWarps < units) put(w0 + i * kMxPrepWarps, held[i]);
+        for (int u = w0 + kMxHeld * kMxPrepWarps; u < units; u += kMxPrepWarps) put(u, fetch(u));
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"(kMxPrepWarps * 32) : "memory");
+
+        if (w0 < kMxIssuers) {
+            if (lane == 0) {
+                // -------------------------------------------------------- MMA issuer of every fourth stage
+                if (w0 == 0) {
+                    for (int kb = 0; kb < blocks; ++kb)
+                        tc_cp_sf(tmem + uint32_t(kMxSfbCol + 4 * kb), smem_desc_sf(smem_u32(sfb + kb * kSfBlockBytes)));
+                    tc_commit(sfb_done);
+                }
+                bool ok = mbar_wait_cycles(sfb_done, 0, abort_flag, g_matvec_mx_err, 74);
+                tc_fence_after();
+                // N goes in steps of 16; columns past the last token's are some other bytes of
+                // this block's memory, and nobody reads what becomes of them
+                const uint32_t mma_n = uint32_t((args.cols + 15) / 16 * 16);
+                int stage = w0, li = 0, kb = w0;  // kb: this issuer's next stage, counted in the tile
+                uint32_t phase = 0;
+                for (int tile = first; ok && tile < tiles; tile += step, ++li, kb -= blocks) {
+                    const int buf = li & 1, kb_first = kb;
+                    if (!mbar_wait_cycles(&tmem_empty[buf], (uint32_t(li >> 1) & 1u) ^ 1u, abort_flag, g_matvec_mx_err, 75)) break;
+                    tc_fence_after();
+                    const uint32_t acc = tmem + uint32_t((buf * kMxIssuers + w0) * kMxAccCols);
+                    for (; kb < blocks; kb += kMxIssuers) {
+                        ok = mbar_wait_cycles(&full[stage], phase, abort_flag, g_matvec_mx_err, 76);
+                        if (!ok) break;
+                        // the scales were written by ordinary accesses of other threads
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        tc_fence_after();
+                        const uint32_t col = tmem + uint32_t(kMxSfaCol + 4 * stage);
+                        tc_cp_sf(col, smem_desc_sf(smem_u32(sfa + stage * kSfBlockBytes)));
+                        const uint64_t ad = smem_desc_sw128(smem_u32(ring + stage * kMxStageBytes));
+                        const uint64_t bd = smem_desc_sw128(smem_u32(toks + kb * args.cols * 128));
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            tc_mma_mxf8f6f4(acc, ad + uint64_t(2 * ks), bd + uint64_t(2 * ks),
+                                            idesc_mxf8f6f4(mma_n, uint32_t(ks)), col,
+                                            tmem + uint32_t(kMxSfbCol + 4 * kb), kb > kb_first || ks ? 1u : 0u);
+                        tc_commit(&empty[stage]);
+                        stage += kMxIssuers;
+                        if (stage >= kStages) {
+                            stage -= kStages;
+                            phase ^= 1u;
+                        }
+                    }
+                    if (!ok) break;
+                    tc_commit(&tmem_full[buf]);
+                }
+                // all issued MMAs must be finished before TMEM is released
+                tc_commit(&mma_done[w0]);
+                const long long t0 = clock64();
+                while (!mbar_try_wait(&mma_done[w0], 0) && clock64() - t0 < kWaitTimeoutCycles) {
+                }
+            }
+            __syncwarp();
+        } else if (warp >= kMxEpiWarp) {
+            // ------------------------------------------------------------ sums: thread = row
+            const int q = warp & 3;
+            int li = 0;
+            for (int tile = first; tile < tiles; tile += step, ++li) {
+                const int buf = li & 1;
+                if (!mx_warp_wait(&tmem_full[buf], uint32_t(li >> 1) & 1u, abort_flag, 77)) break;
+                tc_fence_after();
+                // issuer i has stages of this tile if its first one is before the tile's end
+                const int before = li * blocks;
+                auto has = [&](int i) { return ((i - before) & (kMxIssuers - 1)) < blocks; };
+                float *to = sums + li * args.tokens * kTileRows + q * 32 + lane;
+                const uint32_t acc = tmem + (uint32_t(q * 32) << 16) + uint32_t(buf * kMxIssuers * kMxAccCols);
+                for (int t = 0; t < ntok; ++t) {
+                    float r[kMxIssuers][4], v = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < kMxIssuers; ++i)
+                        if (has(i)) tmem_ld_4(acc + uint32_t(i * kMxAccCols + kMxPieces * t), r[i]);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < kMxIssuers; ++i)
+                        if (has(i)) v += r[i][0] + (r[i][1] + (r[i][2] + r[i][3]));
+                    const int shift = max(scale_exponent<true>(__uint_as_float(tok_max[t])), kMxLowExponent);
+                    to[t * kTileRows] = v * exp2_neg(-shift);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tmem_empty[buf]);
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    if (parts > 1) cluster_meet();
+    else __syncthreads();
+    tc_fence_after();
+
+    // The parts' sums in part order; of the cluster's results every parts-th piece here.
+    uint32_t wrong = 0;
+    bool gave_up = false;
+    for (int p = 0; p < parts; ++p) {
+        wrong |= cluster_word(smem_u32(bad), p);
+        gave_up |= cluster_word(smem_u32(tmem_holder + 1), p) != 0u;
+    }
+    const int rounds = first < tiles ? (tiles - first + step - 1) / step : 0;
+    const int per_tile = args.rows * ntok;
+    for (int i = part * kMxThreads + int(threadIdx.x); i < rounds * per_tile; i += parts * kMxThreads) {
+        const int li = i / per_tile, t = (i - li * per_tile) / args.rows, r = i - li * per_tile - t * args.rows;
+        const int n = (first + li * step) * args.rows + r;
+        if (n >= args.N || (wrong >> t & 1u)) continue;
+        const uint32_t at = smem_u32(sums + (li * args.tokens + t) * kTileRows + r);
+        float v = 0.0f;
+        for (int p = 0; p < parts; ++p) v += __uint_as_float(cluster_word(at, p));
+        if (gave_up) v = __uint_as_float(0x7FC00000u);
+        args.y[int64_t(tok0 + t) * args.N + n] = __float2bfloat16_rn(v);
+    }
+    if (wrong) {
+        // tokens with infinities or NaN: the definition, a warp per result
+        constexpr float kMag[8] = {0.0f, 0.5f, 1.0f, 1.5f, 2.0f, 3.0f, 4.0f, 6.0f};
+        for (int i = part * (kMxThreads / 32) + warp; i < rounds * per_tile; i += parts * (kMxThreads / 32)) {
+            const int li = i / per_tile, t = (i - li * per_tile) / args.rows, r = i - li * per_tile - t * args.rows;
+            const int n = (first + li * step) * args.rows + r;
+            if (n >= args.N || !(wrong >> t & 1u)) continue;
+            float v = 0.0f;
+            for (int k = lane; k < args.K; k += 32) {
+                const uint32_t c = args.w[int64_t(n) * (args.K / 2) + k / 2] >> (4 * (k & 1)) & 15u;
+                const uint32_t s = args.sf[int64_t(n) * (args.K / 32) + k / 32];
+                const float scale = __uint_as_float(s == 255u ? 0x7FC00000u : max(s << 23, 0x00400000u));
+                v += __bfloat162float(args.x[int64_t(tok0 + t) * args.K + k]) * (c & 8u ? -kMag[c & 7u] : kMag[c & 7u]) * scale;
+            }
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+            if (lane == 0) args.y[int64_t(tok0 + t) * args.N + n] = __float2bfloat16_rn(v);
+        }
+    }
+    __syncwarp();
+    if (parts > 1) cluster_meet();  // the other blocks have read this one's sums
+    if (warp == kMxPrepWarp) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace
+
+bool fp4_matvec_mx(const void *x, const void *w, const void *sf, void *y, int T, int N, int K, cudaStream_t stream,
+                   cudaError_t *status) {
+    if (K % kMxBlockK || !aligned(w, 32)) return false;
+    const void *kernel = reinterpret_cast<const void *>(fp4_matvec_mx_kernel);
+    *status = set_max_dynamic_smem(kernel, kMxSmem);
+    if (*status != cudaSuccess) return true;
+    const int all_blocks = K / kMxBlockK;
+    MxArgs a{}, best{};
+    a.x = static_cast<const __nv_bfloat16 *>(x);
+    a.w = static_cast<const uint8_t *>(w);
+    a.sf = static_cast<const uint8_t *>(sf);
+    a.y = static_cast<__nv_bfloat16 *>(y);
+    a.T = T;
+    a.N = N;
+    a.K = K;
+    a.tokens = T < kMxTokens ? T : kMxTokens;
+    a.cols = (kMxPieces * a.tokens + 7) / 8 * 8;
+    // The parts of K that leave a block the fewest bytes to stream, while its tokens
+    // and sums leave room for eight stages.
+    int64_t best_rows = 0, clusters = 0;
+    for (a.parts = 1; a.parts <= kMxMaxParts && a.parts <= all_blocks; a.parts *= 2) {
+        const int64_t units = resident_clusters(kernel, a.parts, kMxThreads, kMxSmem);
+        a.rounds = int((N + kTileRows * units - 1) / (kTileRows * units));
+        a.rows = int((N + a.rounds * units - 1) / (a.rounds * units) + 7) / 8 * 8;
+        a.blocks = (all_blocks + a.parts - 1) / a.parts;
+        if (a.blocks > kMxMaxBlocks || int64_t(a.rounds) * a.tokens * kTileRows * 4 > 64 * 1024) continue;
+        a.stages = mx_smem_bytes(a, kMxMaxStages) <= kMxSmem ? kMxMaxStages : kMxMaxStages - kMxIssuers;
+        if (mx_smem_bytes(a, a.stages) > kMxSmem) continue;
+        const int64_t stream_rows = int64_t(a.rounds) * a.rows * a.blocks;
+        if (best.parts == 0 || stream_rows < best_rows) {
+            best = a;
+            best_rows = stream_rows;
+            const int64_t tiles = (N + a.rows - 1) / a.rows;
+            clusters = tiles < units ? tiles : units;
+        }
+    }
+    if (best.parts == 0) return false;
+    CUtensorMap tm;
+    *status = cudaErrorUnknown;
+    if (!encode_weights4(&tm, w, uint64_t(N), uint64_t(K / 2), 1, uint64_t(K / 2), uint64_t(all_blocks), kMxBlockK / 2,
+                         best.rows, 1, 1))
+        return true;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(clusters * best.parts), unsigned((T + best.tokens - 1) / best.tokens));
+    cfg.blockDim = dim3(kMxThreads);
+    cfg.dynamicSmemBytes = size_t(mx_smem_bytes(best, best.stages));
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(best.parts);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    *status = cudaLaunchKernelEx(&cfg, fp4_matvec_mx_kernel, tm, best);
+    return true;
+}
+
+}  // namespace moe

@@ -115,10 +115,25 @@ bool encode_bf16_3d(CUtensorMap *m, const void *base, uint64_t cols, uint64_t ro
 // 128 columns (128-byte swizzle) x box_rows rows.
 bool encode_bytes_rows(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, int box_rows);
 
+// FP4 weights as boxes of 128 K elements, a byte each in shared memory (defined with
+// the layouts it describes).
+bool encode_weights4(CUtensorMap *m, const void *base, uint64_t rows, uint64_t row_stride, uint64_t a_dim,
+                     uint64_t a_stride, uint64_t b_dim, uint64_t b_stride, int box_rows, int box_a, int kblocks);
+
+// The product of a few tokens with an MX matrix on the block-scaled tensor cores
+// (K a multiple of 128): false if these sizes are not its own; else launched, or
+// *status says why not.
+bool fp4_matvec_mx(const void *x, const void *w, const void *sf, void *y, int T, int N, int K, cudaStream_t stream,
+                   cudaError_t *status);
+
 constexpr int kGroupedMaxWidth = 131072;  // features of a grouped product's operands, at most
 
 // Multiprocessors of the current device (cached per device).
 int num_sms();
+// Clusters of `size` blocks that the current device holds at once, of a kernel with one
+// block to an SM (whose largest dynamic shared memory has been set): fewer than its SMs
+// allow where they do not come in groups of `size`.
+int resident_clusters(const void *kernel, int size, int threads, int smem);
 // Opts `kernel` in to `bytes` of dynamic shared memory on the current device,
 // once per (kernel, device); safe to call from several host threads.
 cudaError_t set_max_dynamic_smem(const void *kernel, int bytes);

@@ -76,6 +76,40 @@ def test_sizes(moe, T, N, K, fmt):
     check(moe, *random_case(T, N, K, fmt, T * 7 + N), fmt)
 
 
+@pytest.mark.parametrize("T,N,K", [
+    (1, 1, 128), (3, 200, 384), (5, 129, 640),              # fewer than four stages of 128, and five
+    (1, 4099, 7168), (8, 4099, 7168), (12, 1000, 2048),     # tiles of any number of rows, two passes
+    (2, 40000, 256), (8, 20011, 512), (6, 19000, 1152),     # several tiles to a block
+    (1, 260, 26624), (4, 65, 53248),                        # as many stages as a part may have
+])
+def test_whole_stages(moe, T, N, K):
+    """MX with K a multiple of 128, which the block-scaled tensor cores take."""
+    check(moe, *random_case(T, N, K, "mx", T * 11 + N), "mx")
+
+
+def test_infinities_by_definition(moe):
+    """Tokens that are not finite give what the sum of their products gives."""
+    x, w, sf = random_case(7, 300, 1280, "mx", 51)
+    x[1, 7], x[3, 1279], x[5, 0], x[5, 900] = float("inf"), float("-inf"), float("inf"), float("inf")
+    y = moe.fp4_matvec(x, w, sf)
+    exact = x.to(F64) @ decode(w, sf, "mx").T
+    for t in (1, 3, 5):
+        assert torch.equal(torch.isnan(y[t]), torch.isnan(exact[t]))
+        inf = torch.isinf(exact[t])
+        assert bool(inf.any()) and torch.equal(y[t][inf].to(F64), exact[t][inf])
+    check(moe, x[[0, 2, 4, 6]].contiguous(), w, sf, "mx")
+
+
+def test_weights_at_16_bytes(moe):
+    x, w, sf = random_case(2, 130, 512, "mx", 61)
+    room = torch.empty(w.numel() + 64, dtype=torch.uint8, device="cuda")
+    at = (16 - room.data_ptr()) % 32
+    moved = room[at:at + w.numel()].view(w.shape)
+    assert moved.data_ptr() % 32 == 16
+    moved.copy_(w)
+    check(moe, x, moved, sf, "mx")
+
+
 @pytest.mark.parametrize("fmt", ["mx", "nvfp4"])
 def test_quantised_weights(moe, fmt):
     """Weights as the framework's quantisers write them."""
