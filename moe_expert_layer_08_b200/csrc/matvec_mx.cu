@@ -14,16 +14,15 @@
 // each piece the rounding of what the ones before it left.  p0 and p1 hold an
 // element of at least 2^-6 exactly (four bits each of bf16's eight), p2 and p3 what
 // is below E4M3's subnormals: an element is off by at most 2^-36 * 2^e, 2^-43 of the
-// largest of its 32.  Exponents are taken relative to the token's largest element in
-// this block's part of K, whose power of two multiplies the fp32 sums at the end.
-// E4M3 has no infinities: an element that is not finite enters as zero and its
-// token's results are computed again by definition.
+// largest of its 32.  E4M3 has no infinities: an element that is not finite enters as
+// zero and its token's results are computed again by definition.
 //
 // A block streams tiles of up to 128 rows and a part of K, 128 elements a stage, in
 // its shared memory by TMA (which spreads the 4-bit codes to bytes) with the stage's
 // scales by cp.async beside them; blocks of a cluster have the parts of K of the same
-// rows, add their fp32 sums in part order through distributed shared memory, and have
-// their part of the tokens prepared once, for all their tiles.  A tcgen05 instruction
+// rows, write their fp32 sums to the block that adds a row's (in part order) through
+// distributed shared memory, and prepare their part of the tokens once, for all their
+// tiles.  A tcgen05 instruction
 // costs its thread about 70 cycles, so four threads issue, each a quarter of a tile's
 // stages into an accumulator of its own.  The rows of a tile are as few as fill every
 // cluster equally often.
@@ -35,7 +34,6 @@ namespace moe {
 namespace {
 
 constexpr int kMxBlockK = 128;       // K elements of a stage
-constexpr int kMxStageBytes = kTileRows * 128;  // codes, a byte each
 constexpr int kMxPieces = 4;         // of a token's element: MMA columns
 constexpr int kMxTokens = 8;         // of a pass
 constexpr int kMxIssuers = 4;
@@ -47,12 +45,11 @@ constexpr int kMxSmem = 232448;
 constexpr int kMxThreads = 20 * 32;
 constexpr int kMxPrepWarp = 5, kMxPrepWarps = 15, kMxEpiWarp = 16;
 constexpr int kMxHeld = 8;           // pieces of the tokens a preparing warp holds in registers
-// TMEM columns: two accumulators per issuer, the stages' scale images, the tokens'
+// TMEM columns: two accumulators per issuer, the stages' scale images of both operands
 constexpr int kMxAccCols = kMxPieces * kMxTokens;  // a multiple of 16
 constexpr int kMxSfaCol = 2 * kMxIssuers * kMxAccCols;
 constexpr int kMxSfbCol = kMxSfaCol + 4 * kMxMaxStages;
-constexpr int kMxMaxBlocks = (512 - kMxSfbCol) / 4;  // stages of a part
-static_assert(kMxEpiWarp % 4 == 0 && kMxMaxBlocks >= 52, "TMEM");
+static_assert(kMxEpiWarp % 4 == 0 && kMxSfbCol + 4 * kMxMaxStages <= 512, "TMEM");
 constexpr int kMxMisc = 512;
 
 struct MxArgs {
@@ -69,9 +66,17 @@ struct MxArgs {
     int rounds;               // tiles of a cluster, at most
     int stages;
 };
+// The MMA reads 128 rows of a stage, N in steps of 16 of the tokens and 32 rows of a
+// scale image, whatever of them is in use: the rest are other bytes of the block's
+// memory, in rows and columns that nobody reads.  So a stage holds a tile's rows, a
+// block of tokens its columns, and the regions lie in an order in which no such read
+// leaves them.
+__host__ __device__ inline int mx_stage_bytes(const MxArgs &a) { return a.rows * 128; }
 int mx_smem_bytes(const MxArgs &a, int stages) {
-    return 1024 + stages * (kMxStageBytes + kSfBlockBytes) + a.blocks * (a.cols * 128 + kSfBlockBytes) +
-           a.rounds * a.tokens * kTileRows * 4 + kMxMisc;
+    const int ring = stages * mx_stage_bytes(a), rest = a.blocks * a.cols * (128 + 16) + stages * kSfBlockBytes +
+                                                        a.rounds * a.tokens * kTileRows * 4 + kMxMisc;
+    // the last stage's 128 rows end inside
+    return 1024 + ring + (rest > kTileRows * 128 ? rest : kTileRows * 128);
 }
 
 __device__ int g_matvec_mx_err[8];  // where a wait that gave up leaves its mark (the outputs become NaN)
@@ -81,15 +86,14 @@ __device__ __forceinline__ uint32_t cluster_rank_of() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ uint32_t cluster_word(uint32_t at, int cta) {
-    uint32_t remote, v;
+// To this block's shared address `at` in block `cta` of the cluster.
+__device__ __forceinline__ void cluster_put(uint32_t at, int cta, uint32_t v) {
+    uint32_t remote;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(at), "r"(cta));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
-    return v;
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(v) : "memory");
 }
-__device__ __forceinline__ void cluster_meet() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_ld_4(uint32_t addr, float (&r)[4]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
@@ -122,29 +126,27 @@ __device__ __forceinline__ uint32_t take_piece(float (&v)[4]) {
     v[0] -= __low2float(a), v[1] -= __high2float(a), v[2] -= __low2float(b), v[3] -= __high2float(b);
     return p;
 }
-// Token exponents are at least this: bf16's smallest subnormal is exact in the pieces there.
-constexpr int kMxLowExponent = -101;
 
 __global__ void __launch_bounds__(kMxThreads, 1)
     fp4_matvec_mx_kernel(const __grid_constant__ CUtensorMap tmap_w, const MxArgs args) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int kStages = args.stages;
-    uint8_t *toks = ring + kStages * kMxStageBytes;                    // [block][column] 128 bytes, swizzled
+    const int stage_bytes = mx_stage_bytes(args);
+    uint8_t *toks = ring + kStages * stage_bytes;                      // [block][column] 128 bytes, swizzled
     uint8_t *sfa = toks + args.blocks * args.cols * 128;               // [stage] images
-    uint8_t *sfb = sfa + kStages * kSfBlockBytes;                      // [block] images
-    float *sums = reinterpret_cast<float *>(sfb + args.blocks * kSfBlockBytes);  // [round][token][row]
+    uint8_t *sfb = sfa + kStages * kSfBlockBytes;                      // [block][column] 16 bytes, 4 of them scales
+    float *sums = reinterpret_cast<float *>(sfb + args.blocks * args.cols * 16);  // [part][round][token][this block's rows]
     uint64_t *full = reinterpret_cast<uint64_t *>(sums + args.rounds * args.tokens * kTileRows);
     uint64_t *empty = full + kMxMaxStages;
     uint64_t *tmem_full = empty + kMxMaxStages;   // [2]
     uint64_t *tmem_empty = tmem_full + 2;         // [2]
     uint64_t *mma_done = tmem_empty + 2;          // [issuer]
-    uint64_t *sfb_done = mma_done + kMxIssuers;
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(sfb_done + 1);
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(mma_done + kMxIssuers);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     uint32_t *bad = tmem_holder + 2;              // tokens with an element that is not finite
-    uint32_t *tok_max = bad + 1;                  // [token]
-    static_assert((2 * kMxMaxStages + 4 + kMxIssuers + 1) * 8 + (3 + kMxTokens) * 4 <= kMxMisc, "barriers and flags");
+    uint32_t *flags = bad + 1;                    // [part] its bad tokens; bit 31: a wait of its gave up
+    static_assert((2 * kMxMaxStages + 4 + kMxIssuers) * 8 + (3 + kMxMaxParts) * 4 <= kMxMisc, "barriers and flags");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int parts = args.parts, part = parts > 1 ? int(cluster_rank_of()) : 0;
@@ -152,6 +154,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     const int kb0 = part * all_blocks / parts, blocks = (part + 1) * all_blocks / parts - kb0;
     const int tiles = (args.N + args.rows - 1) / args.rows;
     const int first = int(blockIdx.x) / parts, step = int(gridDim.x) / parts;
+    const int own_rows = kTileRows / parts;  // of a tile, added and written by this block
     const int tok0 = int(blockIdx.y) * args.tokens, ntok = min(args.tokens, args.T - tok0);
 
     if (threadIdx.x == 0) {
@@ -164,10 +167,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             mbar_init(&tmem_empty[b], 4);
         }
         for (int i = 0; i < kMxIssuers; ++i) mbar_init(&mma_done[i], 1);
-        mbar_init(sfb_done, 1);
         *abort_flag = 0;
         *bad = 0;
-        for (int t = 0; t < kMxTokens; ++t) tok_max[t] = 0;
         fence_mbar_init();
         prefetch_tmap(&tmap_w);
     }
@@ -178,6 +179,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    cluster_arrive();  // waited for before this block's first write to another: they have all begun
     const uint32_t tmem = *tmem_holder;
     pdl_wait();
     if (threadIdx.x == 0) pdl_trigger();
@@ -196,7 +198,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                         break;
                     }
                     mbar_arrive_expect_tx(&full[stage], uint32_t(args.rows * 64));
-                    tma_load_4d(ring + stage * kMxStageBytes, &tmap_w, &full[stage], 0, tile * args.rows, 0, kb0 + kb, pol);
+                    tma_load_4d(ring + stage * stage_bytes, &tmap_w, &full[stage], 0, tile * args.rows, 0, kb0 + kb, pol);
                     if (used < kStages) ++used;
                     if (++stage == kStages) {
                         stage = 0;
@@ -256,50 +258,41 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             return __ldg(reinterpret_cast<const uint2 *>(args.x + int64_t(tok0 + u % ntok) * args.K +
                                                          (kb0 + u / ntok) * kMxBlockK + lane * 4));
         };
-        auto note = [&](int u, uint2 raw) {
-            float v[4];
-            const bool fine = finite4(raw, v);
-            const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(largest4(v)));
-            const bool all_fine = __all_sync(0xFFFFFFFFu, fine);
-            if (lane == 0) {
-                atomicMax(&tok_max[u % ntok], top);
-                if (!all_fine) atomicOr(bad, 1u << (u % ntok));
-            }
-        };
         auto put = [&](int u, uint2 raw) {
             const int t = u % ntok, kb = u / ntok;
             float v[4];
-            finite4(raw, v);
+            if (!finite4(raw, v)) atomicOr(bad, 1u << t);
             float amax = largest4(v);
 #pragma unroll
             for (int d = 1; d < 8; d <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
-            const int shift = max(scale_exponent<true>(__uint_as_float(tok_max[t])), kMxLowExponent);
-            // never more than 101 below the token's, where the last piece's scale is 2^-127
-            const int e = amax > 0.0f ? max(max(scale_exponent<true>(amax), kMxLowExponent), shift - 101) : shift;
+            // at least -101: the last piece's scale is 2^-127 there, and bf16's smallest
+            // subnormal a multiple of its step
+            const int e = max(scale_exponent<true>(amax), -101);
             const float m = exp2_neg(e);
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] *= m;
             uint8_t *to = toks + kb * args.cols * 128 + (lane & 3) * 4;
-            uint8_t *image = sfb + kb * kSfBlockBytes + (lane >> 3);
+            uint8_t *image = sfb + (kb * args.cols + kMxPieces * t) * 16 + (lane >> 3);
+            bool left = true;  // (of any lane)
 #pragma unroll
             for (int p = 0; p < kMxPieces; ++p) {
                 const int col = kMxPieces * t + p;
-                *reinterpret_cast<uint32_t *>(to + col * 128 + (((lane >> 2) ^ (col & 7)) << 4)) = take_piece(v);
-                const float next = p == 1 ? 262144.0f : 16.0f;
+                uint32_t piece = 0;
+                if (left) {
+                    piece = take_piece(v);
+                    const float next = p == 1 ? 262144.0f : 16.0f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] *= next;
-                if ((lane & 7) == 0) image[col * 16] = uint8_t(e - shift + 127 - (p == 0 ? 0 : p == 1 ? 4 : p == 2 ? 22 : 26));
+                    for (int i = 0; i < 4; ++i) v[i] *= next;
+                    if (p == 1) left = __any_sync(0xFFFFFFFFu, largest4(v) > 0.0f);
+                }
+                *reinterpret_cast<uint32_t *>(to + col * 128 + (((lane >> 2) ^ (col & 7)) << 4)) = piece;
+                if ((lane & 7) == 0) image[p * 16] = uint8_t(e + 127 - (p == 0 ? 0 : p == 1 ? 4 : p == 2 ? 22 : 26));
             }
         };
         uint2 held[kMxHeld];
 #pragma unroll
         for (int i = 0; i < kMxHeld; ++i)
             if (w0 + i * kMxPrepWarps < units) held[i] = fetch(w0 + i * kMxPrepWarps);
-#pragma unroll
-        for (int i = 0; i < kMxHeld; ++i)
-            if (w0 + i * kMxPrepWarps < units) note(w0 + i * kMxPrepWarps, held[i]);
-        for (int u = w0 + kMxHeld * kMxPrepWarps; u < units; u += kMxPrepWarps) note(u, fetch(u));
-        asm volatile("bar.sync 1, %0;" ::"n"(kMxPrepWarps * 32) : "memory");
 #pragma unroll
         for (int i = 0; i < kMxHeld; ++i)
             if (w0 + i * kMxPrepWarps < units) put(w0 + i * kMxPrepWarps, held[i]);
@@ -310,15 +303,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         if (w0 < kMxIssuers) {
             if (lane == 0) {
                 // -------------------------------------------------------- MMA issuer of every fourth stage
-                if (w0 == 0) {
-                    for (int kb = 0; kb < blocks; ++kb)
-                        tc_cp_sf(tmem + uint32_t(kMxSfbCol + 4 * kb), smem_desc_sf(smem_u32(sfb + kb * kSfBlockBytes)));
-                    tc_commit(sfb_done);
-                }
-                bool ok = mbar_wait_cycles(sfb_done, 0, abort_flag, g_matvec_mx_err, 74);
-                tc_fence_after();
-                // N goes in steps of 16; columns past the last token's are some other bytes of
-                // this block's memory, and nobody reads what becomes of them
+                bool ok = true;
                 const uint32_t mma_n = uint32_t((args.cols + 15) / 16 * 16);
                 int stage = w0, li = 0, kb = w0;  // kb: this issuer's next stage, counted in the tile
                 uint32_t phase = 0;
@@ -333,15 +318,15 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                         // the scales were written by ordinary accesses of other threads
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         tc_fence_after();
-                        const uint32_t col = tmem + uint32_t(kMxSfaCol + 4 * stage);
+                        const uint32_t col = tmem + uint32_t(kMxSfaCol + 4 * stage), colb = tmem + uint32_t(kMxSfbCol + 4 * stage);
                         tc_cp_sf(col, smem_desc_sf(smem_u32(sfa + stage * kSfBlockBytes)));
-                        const uint64_t ad = smem_desc_sw128(smem_u32(ring + stage * kMxStageBytes));
+                        tc_cp_sf(colb, smem_desc_sf(smem_u32(sfb + kb * args.cols * 16)));
+                        const uint64_t ad = smem_desc_sw128(smem_u32(ring + stage * stage_bytes));
                         const uint64_t bd = smem_desc_sw128(smem_u32(toks + kb * args.cols * 128));
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
                             tc_mma_mxf8f6f4(acc, ad + uint64_t(2 * ks), bd + uint64_t(2 * ks),
-                                            idesc_mxf8f6f4(mma_n, uint32_t(ks)), col,
-                                            tmem + uint32_t(kMxSfbCol + 4 * kb), kb > kb_first || ks ? 1u : 0u);
+                                            idesc_mxf8f6f4(mma_n, uint32_t(ks)), col, colb, kb > kb_first || ks ? 1u : 0u);
                         tc_commit(&empty[stage]);
                         stage += kMxIssuers;
                         if (stage >= kStages) {
@@ -361,8 +346,9 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             __syncwarp();
         } else if (warp >= kMxEpiWarp) {
             // ------------------------------------------------------------ sums: thread = row
-            const int q = warp & 3;
+            const int q = warp & 3, row = q * 32 + lane, adds = row / own_rows;  // the block that adds this row's
             int li = 0;
+            cluster_wait();
             for (int tile = first; tile < tiles; tile += step, ++li) {
                 const int buf = li & 1;
                 if (!mx_warp_wait(&tmem_full[buf], uint32_t(li >> 1) & 1u, abort_flag, 77)) break;
@@ -370,7 +356,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                 // issuer i has stages of this tile if its first one is before the tile's end
                 const int before = li * blocks;
                 auto has = [&](int i) { return ((i - before) & (kMxIssuers - 1)) < blocks; };
-                float *to = sums + li * args.tokens * kTileRows + q * 32 + lane;
+                const uint32_t to = smem_u32(sums + (part * args.rounds + li) * args.tokens * own_rows + row % own_rows);
                 const uint32_t acc = tmem + (uint32_t(q * 32) << 16) + uint32_t(buf * kMxIssuers * kMxAccCols);
                 for (int t = 0; t < ntok; ++t) {
                     float r[kMxIssuers][4], v = 0.0f;
@@ -381,8 +367,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
 #pragma unroll
                     for (int i = 0; i < kMxIssuers; ++i)
                         if (has(i)) v += r[i][0] + (r[i][1] + (r[i][2] + r[i][3]));
-                    const int shift = max(scale_exponent<true>(__uint_as_float(tok_max[t])), kMxLowExponent);
-                    to[t * kTileRows] = v * exp2_neg(-shift);
+                    cluster_put(to + uint32_t(t * own_rows * 4), adds, __float_as_uint(v));
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -391,37 +376,38 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         }
     }
     __syncwarp();
+    if (warp < kMxEpiWarp) cluster_wait();
+    __syncthreads();
+    if (threadIdx.x < parts) cluster_put(smem_u32(flags + part), int(threadIdx.x), *bad | (*abort_flag ? 1u << 31 : 0u));
+    __syncwarp();
     tc_fence_before();
-    if (parts > 1) cluster_meet();
-    else __syncthreads();
+    cluster_arrive();
+    cluster_wait();
     tc_fence_after();
+    if (warp == kMxPrepWarp) tmem_dealloc(tmem, 512);
 
-    // The parts' sums in part order; of the cluster's results every parts-th piece here.
+    // The parts' sums of this block's rows, in part order.
     uint32_t wrong = 0;
-    bool gave_up = false;
-    for (int p = 0; p < parts; ++p) {
-        wrong |= cluster_word(smem_u32(bad), p);
-        gave_up |= cluster_word(smem_u32(tmem_holder + 1), p) != 0u;
-    }
+    for (int p = 0; p < parts; ++p) wrong |= flags[p];
     const int rounds = first < tiles ? (tiles - first + step - 1) / step : 0;
-    const int per_tile = args.rows * ntok;
-    for (int i = part * kMxThreads + int(threadIdx.x); i < rounds * per_tile; i += parts * kMxThreads) {
-        const int li = i / per_tile, t = (i - li * per_tile) / args.rows, r = i - li * per_tile - t * args.rows;
-        const int n = (first + li * step) * args.rows + r;
-        if (n >= args.N || (wrong >> t & 1u)) continue;
-        const uint32_t at = smem_u32(sums + (li * args.tokens + t) * kTileRows + r);
+    const int per_tile = own_rows * ntok;
+    for (int i = threadIdx.x; i < rounds * per_tile; i += kMxThreads) {
+        const int li = i / per_tile, t = (i - li * per_tile) / own_rows, own = i - li * per_tile - t * own_rows;
+        const int r = part * own_rows + own, n = (first + li * step) * args.rows + r;
+        if (r >= args.rows || n >= args.N || (wrong >> t & 1u)) continue;
+        const float *at = sums + (li * args.tokens + t) * own_rows + own;
         float v = 0.0f;
-        for (int p = 0; p < parts; ++p) v += __uint_as_float(cluster_word(at, p));
-        if (gave_up) v = __uint_as_float(0x7FC00000u);
+        for (int p = 0; p < parts; ++p) v += at[p * args.rounds * args.tokens * own_rows];
+        if (wrong >> 31) v = __uint_as_float(0x7FC00000u);
         args.y[int64_t(tok0 + t) * args.N + n] = __float2bfloat16_rn(v);
     }
-    if (wrong) {
+    if (wrong & 0x7FFFFFFFu) {
         // tokens with infinities or NaN: the definition, a warp per result
         constexpr float kMag[8] = {0.0f, 0.5f, 1.0f, 1.5f, 2.0f, 3.0f, 4.0f, 6.0f};
-        for (int i = part * (kMxThreads / 32) + warp; i < rounds * per_tile; i += parts * (kMxThreads / 32)) {
-            const int li = i / per_tile, t = (i - li * per_tile) / args.rows, r = i - li * per_tile - t * args.rows;
-            const int n = (first + li * step) * args.rows + r;
-            if (n >= args.N || !(wrong >> t & 1u)) continue;
+        for (int i = warp; i < rounds * per_tile; i += kMxThreads / 32) {
+            const int li = i / per_tile, t = (i - li * per_tile) / own_rows, own = i - li * per_tile - t * own_rows;
+            const int r = part * own_rows + own, n = (first + li * step) * args.rows + r;
+            if (r >= args.rows || n >= args.N || !(wrong >> t & 1u)) continue;
             float v = 0.0f;
             for (int k = lane; k < args.K; k += 32) {
                 const uint32_t c = args.w[int64_t(n) * (args.K / 2) + k / 2] >> (4 * (k & 1)) & 15u;
@@ -434,9 +420,6 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             if (lane == 0) args.y[int64_t(tok0 + t) * args.N + n] = __float2bfloat16_rn(v);
         }
     }
-    __syncwarp();
-    if (parts > 1) cluster_meet();  // the other blocks have read this one's sums
-    if (warp == kMxPrepWarp) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace
@@ -466,7 +449,7 @@ bool fp4_matvec_mx(const void *x, const void *w, const void *sf, void *y, int T,
         a.rounds = int((N + kTileRows * units - 1) / (kTileRows * units));
         a.rows = int((N + a.rounds * units - 1) / (a.rounds * units) + 7) / 8 * 8;
         a.blocks = (all_blocks + a.parts - 1) / a.parts;
-        if (a.blocks > kMxMaxBlocks || int64_t(a.rounds) * a.tokens * kTileRows * 4 > 64 * 1024) continue;
+        if (a.blocks > 1024 || a.rounds > 1024) continue;
         a.stages = mx_smem_bytes(a, kMxMaxStages) <= kMxSmem ? kMxMaxStages : kMxMaxStages - kMxIssuers;
         if (mx_smem_bytes(a, a.stages) > kMxSmem) continue;
         const int64_t stream_rows = int64_t(a.rounds) * a.rows * a.blocks;
