@@ -17,14 +17,15 @@
 // largest of its 32.  E4M3 has no infinities: an element that is not finite enters as
 // zero and its token's results are computed again by definition.
 //
-// A block streams tiles of up to 128 rows and a part of K, 128 elements a stage, in
-// its shared memory by TMA (which spreads the 4-bit codes to bytes) with the stage's
+// A block streams tiles of up to 128 rows and a part of K, 256 elements a stage (with
+// 128 the loading thread, at 340 cycles a stage, held everything up), to its shared
+// memory by TMA (which spreads the 4-bit codes to bytes) with the stage's
 // scales by cp.async beside them; blocks of a cluster have the parts of K of the same
 // rows, write their fp32 sums to the block that adds a row's (in part order) through
 // distributed shared memory, and prepare their part of the tokens once, for all their
 // tiles.  A tcgen05 instruction
-// costs its thread about 70 cycles, so four threads issue, each a quarter of a tile's
-// stages into an accumulator of its own.  The rows of a tile are as few as fill every
+// costs its thread about 70 cycles, so three or four threads issue, each every third or
+// fourth stage into an accumulator of its own.  The rows of a tile are as few as fill every
 // cluster equally often.
 // N = 14336, K = 7168: 19.7 us for one token, 27.0 for eight (26.0 and 30.6 by mma.sync).
 #include "moe_common.cuh"
@@ -33,23 +34,25 @@
 namespace moe {
 namespace {
 
-constexpr int kMxBlockK = 128;       // K elements of a stage
+constexpr int kMxBlockK = 128;       // K elements of a block of codes and its scale image
+constexpr int kMxStageBlocks = 2;    // blocks of a stage
 constexpr int kMxPieces = 4;         // of a token's element: MMA columns
 constexpr int kMxTokens = 8;         // of a pass
-constexpr int kMxIssuers = 4;
-constexpr int kMxMaxStages = 12;    // a multiple of the issuers: a ring slot is always the same one's
+constexpr int kMxIssuers = 4;        // at most
+constexpr int kMxMaxStages = 6;
 constexpr int kMxMaxParts = 8;
 constexpr int kMxSmem = 232448;
 // warps: 0 loads codes, 1-4 scales (a thread a row), 5-19 prepare the tokens, then
 // 5-8 issue and 16-19 drain
 constexpr int kMxThreads = 20 * 32;
 constexpr int kMxPrepWarp = 5, kMxPrepWarps = 15, kMxEpiWarp = 16;
-constexpr int kMxHeld = 8;           // pieces of the tokens a preparing warp holds in registers
+constexpr int kMxHeld = 4;           // pieces of the tokens a preparing warp holds in registers
 // TMEM columns: two accumulators per issuer, the stages' scale images of both operands
 constexpr int kMxAccCols = kMxPieces * kMxTokens;  // a multiple of 16
 constexpr int kMxSfaCol = 2 * kMxIssuers * kMxAccCols;
-constexpr int kMxSfbCol = kMxSfaCol + 4 * kMxMaxStages;
-static_assert(kMxEpiWarp % 4 == 0 && kMxSfbCol + 4 * kMxMaxStages <= 512, "TMEM");
+constexpr int kMxSfCols = 4 * kMxStageBlocks;  // of a stage and operand
+constexpr int kMxSfbCol = kMxSfaCol + kMxSfCols * kMxMaxStages;
+static_assert(kMxEpiWarp % 4 == 0 && kMxSfbCol + kMxSfCols * kMxMaxStages <= 512, "TMEM");
 constexpr int kMxMisc = 512;
 
 struct MxArgs {
@@ -62,18 +65,18 @@ struct MxArgs {
     int cols;                 // of the tokens' operand in shared memory, a multiple of 8
     int rows;                 // of a tile, a multiple of 8
     int parts;                // of K: blocks of a cluster
-    int blocks;               // stages of a part, at most
+    int blocks;               // of 128 elements of a part, at most
     int rounds;               // tiles of a cluster, at most
-    int stages;
+    int stages, issuers;      // the first a multiple of the second: a ring slot is always the same issuer's
 };
 // The MMA reads 128 rows of a stage, N in steps of 16 of the tokens and 32 rows of a
 // scale image, whatever of them is in use: the rest are other bytes of the block's
 // memory, in rows and columns that nobody reads.  So a stage holds a tile's rows, a
 // block of tokens its columns, and the regions lie in an order in which no such read
 // leaves them.
-__host__ __device__ inline int mx_stage_bytes(const MxArgs &a) { return a.rows * 128; }
+__host__ __device__ inline int mx_stage_bytes(const MxArgs &a) { return kMxStageBlocks * a.rows * 128; }
 int mx_smem_bytes(const MxArgs &a, int stages) {
-    const int ring = stages * mx_stage_bytes(a), rest = a.blocks * a.cols * (128 + 16) + stages * kSfBlockBytes +
+    const int ring = stages * mx_stage_bytes(a), rest = a.blocks * a.cols * (128 + 16) + stages * kMxStageBlocks * kSfBlockBytes +
                                                         a.rounds * a.tokens * kTileRows * 4 + kMxMisc;
     // the last stage's 128 rows end inside
     return 1024 + ring + (rest > kTileRows * 128 ? rest : kTileRows * 128);
@@ -92,6 +95,8 @@ __device__ __forceinline__ void cluster_put(uint32_t at, int cta, uint32_t v) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(at), "r"(cta));
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(v) : "memory");
 }
+// (without an order of this thread's accesses: for the others' having begun alone)
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_ld_4(uint32_t addr, float (&r)[4]) {
@@ -102,29 +107,36 @@ __device__ __forceinline__ void tmem_ld_4(uint32_t addr, float (&r)[4]) {
 __device__ __forceinline__ bool mx_warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int where) {
     return __all_sync(0xFFFFFFFFu, mbar_wait_cycles(bar, parity, abort, g_matvec_mx_err, where));
 }
-// The four bf16 of two words; elements that are not finite as zeros.
-__device__ __forceinline__ bool finite4(uint2 u, float (&v)[4]) {
-    v[0] = __uint_as_float(u.x << 16), v[1] = __uint_as_float(u.x & 0xFFFF0000u);
-    v[2] = __uint_as_float(u.y << 16), v[3] = __uint_as_float(u.y & 0xFFFF0000u);
+// Eight bf16; elements that are not finite as zeros.
+__device__ __forceinline__ bool finite8(uint4 u, float (&v)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
     bool fine = true;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 8; ++i) {
+        v[i] = __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
         if (!(fabsf(v[i]) <= 3.4e38f)) {
             v[i] = 0.0f;
             fine = false;
         }
+    }
     return fine;
 }
-__device__ __forceinline__ float largest4(const float (&v)[4]) {
-    return fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+// E4M3 codes of v.
+__device__ __forceinline__ uint2 piece_of(const float (&v)[8]) {
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+    return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
 }
-// E4M3 codes of v, and v - codes in v.
-__device__ __forceinline__ uint32_t take_piece(float (&v)[4]) {
-    const uint32_t p = to_e4m3x4(v);
-    const __half2 a = __half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(p & 0xFFFFu), __NV_E4M3));
-    const __half2 b = __half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(p >> 16), __NV_E4M3));
-    v[0] -= __low2float(a), v[1] -= __high2float(a), v[2] -= __low2float(b), v[3] -= __high2float(b);
-    return p;
+// What the codes left of v, times `next`.
+__device__ __forceinline__ void leave(float (&v)[8], uint2 piece, float next) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t two = (i & 2 ? piece.y : piece.x) >> (16 * (i & 1)) & 0xFFFFu;
+        const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(two), __NV_E4M3));
+        v[2 * i] = (v[2 * i] - __low2float(h)) * next;
+        v[2 * i + 1] = (v[2 * i + 1] - __high2float(h)) * next;
+    }
 }
 
 __global__ void __launch_bounds__(kMxThreads, 1)
@@ -135,7 +147,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     const int stage_bytes = mx_stage_bytes(args);
     uint8_t *toks = ring + kStages * stage_bytes;                      // [block][column] 128 bytes, swizzled
     uint8_t *sfa = toks + args.blocks * args.cols * 128;               // [stage] images
-    uint8_t *sfb = sfa + kStages * kSfBlockBytes;                      // [block][column] 16 bytes, 4 of them scales
+    uint8_t *sfb = sfa + kStages * kMxStageBlocks * kSfBlockBytes;                      // [block][column] 16 bytes, 4 of them scales
     float *sums = reinterpret_cast<float *>(sfb + args.blocks * args.cols * 16);  // [part][round][token][this block's rows]
     uint64_t *full = reinterpret_cast<uint64_t *>(sums + args.rounds * args.tokens * kTileRows);
     uint64_t *empty = full + kMxMaxStages;
@@ -150,8 +162,11 @@ __global__ void __launch_bounds__(kMxThreads, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int parts = args.parts, part = parts > 1 ? int(cluster_rank_of()) : 0;
-    const int all_blocks = args.K / kMxBlockK;
-    const int kb0 = part * all_blocks / parts, blocks = (part + 1) * all_blocks / parts - kb0;
+    const int all_blocks = args.K / kMxBlockK, all_pairs = (all_blocks + 1) / 2;
+    const int pair0 = part * all_pairs / parts, kb0 = pair0 * kMxStageBlocks;
+    const int pairs = (part + 1) * all_pairs / parts - pair0;  // stages of a tile
+    const int blocks = min(pairs * kMxStageBlocks, all_blocks - kb0);
+    const int issuers = args.issuers;
     const int tiles = (args.N + args.rows - 1) / args.rows;
     const int first = int(blockIdx.x) / parts, step = int(gridDim.x) / parts;
     const int own_rows = kTileRows / parts;  // of a tile, added and written by this block
@@ -163,7 +178,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(&tmem_full[b], kMxIssuers);
+            mbar_init(&tmem_full[b], issuers);
             mbar_init(&tmem_empty[b], 4);
         }
         for (int i = 0; i < kMxIssuers; ++i) mbar_init(&mma_done[i], 1);
@@ -179,7 +194,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    cluster_arrive();  // waited for before this block's first write to another: they have all begun
+    cluster_arrive_relaxed();  // waited for before this block's first write to another: they have all begun
     const uint32_t tmem = *tmem_holder;
     pdl_wait();
     if (threadIdx.x == 0) pdl_trigger();
@@ -188,42 +203,26 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         if (lane == 0) {
             // ------------------------------------------------------------ codes
             const uint64_t pol = policy_evict_first();
-            int stage = 0, used = 0;
+            int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
             for (int tile = first; ok && tile < tiles; tile += step)
-                for (int kb = 0; kb < blocks; ++kb) {
-                    if (!mbar_wait_cycles(&empty[stage], phase ^ 1u, abort_flag, g_matvec_mx_err, 71)) {
-                        ok = false;
-                        break;
-                    }
-                    mbar_arrive_expect_tx(&full[stage], uint32_t(args.rows * 64));
-                    tma_load_4d(ring + stage * stage_bytes, &tmap_w, &full[stage], 0, tile * args.rows, 0, kb0 + kb, pol);
-                    if (used < kStages) ++used;
+                for (int s = 0; s < pairs; ++s) {
+                    ok = mbar_wait_cycles(&empty[stage], phase ^ 1u, abort_flag, g_matvec_mx_err, 71);
+                    if (!ok) break;
+                    // (a block past K is filled with zeros, and its bytes count)
+                    mbar_arrive_expect_tx(&full[stage], uint32_t(kMxStageBlocks * args.rows * 64));
+                    tma_load_4d(ring + stage * stage_bytes, &tmap_w, &full[stage], 0, tile * args.rows, 0, kb0 + s * kMxStageBlocks, pol);
                     if (++stage == kStages) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
-            // Every copy has landed once its stage is consumed; after a wait that gave
-            // up nothing consumes them: a quarter of a second, in which copies land.
-            for (int i = 0; i < used; ++i) {
-                if (--stage < 0) {
-                    stage = kStages - 1;
-                    phase ^= 1u;
-                }
-                mbar_wait_cycles(&empty[stage], phase, abort_flag, g_matvec_mx_err, 72);
-            }
-            if (*abort_flag) {
-                const long long t0 = clock64();
-                while (clock64() - t0 < kWaitTimeoutCycles / 8) {
-                }
-            }
         }
         __syncwarp();
     } else if (warp < kMxPrepWarp) {
         // ---------------------------------------------------------------- scales: thread = row
-        // four bytes a stage, to row r's place in the image: (r % 32) * 16 + (r / 32) * 4
+        // four bytes a block, to row r's place in the image: (r % 32) * 16 + (r / 32) * 4
         const int r = int(threadIdx.x) - 32;
         const int64_t ld = args.K / 32;
         const uint32_t dst = smem_u32(sfa) + uint32_t((r & 31) * 16 + (r >> 5) * 4);
@@ -234,14 +233,16 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             const int n = tile * args.rows + r;
             const bool real = r < args.rows && n < args.N;
             const uint8_t *src = args.sf + (real ? n * ld : 0) + kb0 * 4;
-            for (int kb = 0; kb < blocks; ++kb) {
-                if (!mx_warp_wait(&empty[stage], phase ^ 1u, abort_flag, 73)) {
-                    ok = false;
-                    break;
-                }
-                if (real)
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + stage * kSfBlockBytes), "l"(src + kb * 4)
-                                 : "memory");
+            for (int s = 0; s < pairs; ++s) {
+                ok = mx_warp_wait(&empty[stage], phase ^ 1u, abort_flag, 73);
+                if (!ok) break;
+#pragma unroll
+                for (int b = 0; b < kMxStageBlocks; ++b)
+                    if (real && kMxStageBlocks * s + b < blocks)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                                         dst + (stage * kMxStageBlocks + b) * kSfBlockBytes),
+                                     "l"(src + (kMxStageBlocks * s + b) * 4)
+                                     : "memory");
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&full[stage])) : "memory");
                 if (++stage == kStages) {
                     stage = 0;
@@ -252,83 +253,113 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
         // ---------------------------------------------------------------- tokens
-        // a unit is a stage's 128 elements of a token, four per lane
-        const int units = blocks * ntok, w0 = warp - kMxPrepWarp;
-        auto fetch = [&](int u) {
-            return __ldg(reinterpret_cast<const uint2 *>(args.x + int64_t(tok0 + u % ntok) * args.K +
-                                                         (kb0 + u / ntok) * kMxBlockK + lane * 4));
+        // a unit is a stage's 256 elements of a token, eight per lane
+        const int w0 = warp - kMxPrepWarp, block = lane >> 4;
+        const int s_step = kMxPrepWarps / ntok, t_step = kMxPrepWarps - s_step * ntok;
+        struct Unit {
+            int s, t;
         };
-        auto put = [&](int u, uint2 raw) {
-            const int t = u % ntok, kb = u / ntok;
-            float v[4];
-            if (!finite4(raw, v)) atomicOr(bad, 1u << t);
-            float amax = largest4(v);
+        auto next = [&](Unit &u) {  // kMxPrepWarps further, stage by stage over the tokens
+            u.s += s_step;
+            u.t += t_step;
+            if (u.t >= ntok) {
+                u.t -= ntok;
+                ++u.s;
+            }
+        };
+        auto inside = [&](Unit u) { return kMxStageBlocks * u.s + block < blocks; };
+        auto fetch = [&](Unit u) {
+            const int64_t at = int64_t(tok0 + u.t) * args.K + (kb0 + kMxStageBlocks * u.s) * kMxBlockK + lane * 8;
+            return inside(u) ? __ldg(reinterpret_cast<const uint4 *>(args.x + at)) : make_uint4(0, 0, 0, 0);
+        };
+        auto put = [&](Unit u, uint4 raw) {
+            float v[8], amax = 0.0f;
+            if (!finite8(raw, v)) atomicOr(bad, 1u << u.t);
 #pragma unroll
-            for (int d = 1; d < 8; d <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
             // at least -101: the last piece's scale is 2^-127 there, and bf16's smallest
             // subnormal a multiple of its step
             const int e = max(scale_exponent<true>(amax), -101);
             const float m = exp2_neg(e);
+            bool low = false;  // an element below 2^-6 may need the last two pieces
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] *= m;
-            uint8_t *to = toks + kb * args.cols * 128 + (lane & 3) * 4;
-            uint8_t *image = sfb + (kb * args.cols + kMxPieces * t) * 16 + (lane >> 3);
-            bool left = true;  // (of any lane)
+            for (int i = 0; i < 8; ++i) {
+                v[i] *= m;
+                low |= v[i] != 0.0f && fabsf(v[i]) < 0.015625f;
+            }
+            low = __any_sync(0xFFFFFFFFu, low);
+            const int kb = kMxStageBlocks * u.s + block, col = kMxPieces * u.t;
+            uint8_t *to = toks + (kb * args.cols + col) * 128 + (lane & 1) * 8;
+            const int slot = (lane & 15) >> 1;
+            uint8_t *image = sfb + (kb * args.cols + col) * 16 + (lane >> 2 & 3);
+            uint2 piece[kMxPieces];
+            piece[0] = piece_of(v);
+            leave(v, piece[0], 16.0f);
+            piece[1] = piece_of(v);
+            piece[2] = piece[3] = make_uint2(0, 0);
+            if (low) {
+                leave(v, piece[1], 262144.0f);
+                piece[2] = piece_of(v);
+                leave(v, piece[2], 16.0f);
+                piece[3] = piece_of(v);
+            }
+            if (inside(u)) {
 #pragma unroll
-            for (int p = 0; p < kMxPieces; ++p) {
-                const int col = kMxPieces * t + p;
-                uint32_t piece = 0;
-                if (left) {
-                    piece = take_piece(v);
-                    const float next = p == 1 ? 262144.0f : 16.0f;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] *= next;
-                    if (p == 1) left = __any_sync(0xFFFFFFFFu, largest4(v) > 0.0f);
+                for (int p = 0; p < kMxPieces; ++p) {
+                    *reinterpret_cast<uint2 *>(to + p * 128 + ((slot ^ ((col + p) & 7)) << 4)) = piece[p];
+                    if ((lane & 3) == 0) image[p * 16] = uint8_t(e + 127 - (p == 0 ? 0 : p == 1 ? 4 : p == 2 ? 22 : 26));
                 }
-                *reinterpret_cast<uint32_t *>(to + col * 128 + (((lane >> 2) ^ (col & 7)) << 4)) = piece;
-                if ((lane & 7) == 0) image[p * 16] = uint8_t(e + 127 - (p == 0 ? 0 : p == 1 ? 4 : p == 2 ? 22 : 26));
             }
         };
-        uint2 held[kMxHeld];
+        uint4 held[kMxHeld];
+        Unit u = {w0 / ntok, w0 % ntok}, v = u;
 #pragma unroll
-        for (int i = 0; i < kMxHeld; ++i)
-            if (w0 + i * kMxPrepWarps < units) held[i] = fetch(w0 + i * kMxPrepWarps);
+        for (int i = 0; i < kMxHeld; ++i, next(v))
+            if (v.s < pairs) held[i] = fetch(v);
 #pragma unroll
-        for (int i = 0; i < kMxHeld; ++i)
-            if (w0 + i * kMxPrepWarps < units) put(w0 + i * kMxPrepWarps, held[i]);
-        for (int u = w0 + kMxHeld * kMxPrepWarps; u < units; u += kMxPrepWarps) put(u, fetch(u));
+        for (int i = 0; i < kMxHeld; ++i, next(u))
+            if (u.s < pairs) put(u, held[i]);
+        for (; u.s < pairs; next(u)) put(u, fetch(u));
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         asm volatile("bar.sync 1, %0;" ::"n"(kMxPrepWarps * 32) : "memory");
 
-        if (w0 < kMxIssuers) {
+        if (w0 < issuers) {
             if (lane == 0) {
-                // -------------------------------------------------------- MMA issuer of every fourth stage
+                // -------------------------------------------------------- MMA issuer
                 bool ok = true;
                 const uint32_t mma_n = uint32_t((args.cols + 15) / 16 * 16);
-                int stage = w0, li = 0, kb = w0;  // kb: this issuer's next stage, counted in the tile
+                int stage = w0, li = 0, s = w0;  // s: this issuer's next stage, counted in the tile
                 uint32_t phase = 0;
-                for (int tile = first; ok && tile < tiles; tile += step, ++li, kb -= blocks) {
-                    const int buf = li & 1, kb_first = kb;
+                for (int tile = first; ok && tile < tiles; tile += step, ++li, s -= pairs) {
+                    const int buf = li & 1, s_first = s;
                     if (!mbar_wait_cycles(&tmem_empty[buf], (uint32_t(li >> 1) & 1u) ^ 1u, abort_flag, g_matvec_mx_err, 75)) break;
                     tc_fence_after();
                     const uint32_t acc = tmem + uint32_t((buf * kMxIssuers + w0) * kMxAccCols);
-                    for (; kb < blocks; kb += kMxIssuers) {
+                    for (; s < pairs; s += issuers) {
                         ok = mbar_wait_cycles(&full[stage], phase, abort_flag, g_matvec_mx_err, 76);
                         if (!ok) break;
                         // the scales were written by ordinary accesses of other threads
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         tc_fence_after();
-                        const uint32_t col = tmem + uint32_t(kMxSfaCol + 4 * stage), colb = tmem + uint32_t(kMxSfbCol + 4 * stage);
-                        tc_cp_sf(col, smem_desc_sf(smem_u32(sfa + stage * kSfBlockBytes)));
-                        tc_cp_sf(colb, smem_desc_sf(smem_u32(sfb + kb * args.cols * 16)));
-                        const uint64_t ad = smem_desc_sw128(smem_u32(ring + stage * stage_bytes));
-                        const uint64_t bd = smem_desc_sw128(smem_u32(toks + kb * args.cols * 128));
+                        const uint32_t col = tmem + uint32_t(kMxSfaCol + kMxSfCols * stage);
+                        const uint32_t colb = tmem + uint32_t(kMxSfbCol + kMxSfCols * stage);
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            tc_mma_mxf8f6f4(acc, ad + uint64_t(2 * ks), bd + uint64_t(2 * ks),
-                                            idesc_mxf8f6f4(mma_n, uint32_t(ks)), col, colb, kb > kb_first || ks ? 1u : 0u);
+                        for (int b = 0; b < kMxStageBlocks; ++b) {
+                            const int kb = kMxStageBlocks * s + b;
+                            if (kb >= blocks) break;
+                            tc_cp_sf(col + 4 * b, smem_desc_sf(smem_u32(sfa + (stage * kMxStageBlocks + b) * kSfBlockBytes)));
+                            tc_cp_sf(colb + 4 * b, smem_desc_sf(smem_u32(sfb + kb * args.cols * 16)));
+                            const uint64_t ad = smem_desc_sw128(smem_u32(ring + stage * stage_bytes + b * args.rows * 128));
+                            const uint64_t bd = smem_desc_sw128(smem_u32(toks + kb * args.cols * 128));
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                tc_mma_mxf8f6f4(acc, ad + uint64_t(2 * ks), bd + uint64_t(2 * ks), idesc_mxf8f6f4(mma_n, uint32_t(ks)),
+                                                col + 4 * b, colb + 4 * b, s > s_first || b || ks ? 1u : 0u);
+                        }
                         tc_commit(&empty[stage]);
-                        stage += kMxIssuers;
+                        stage += issuers;
                         if (stage >= kStages) {
                             stage -= kStages;
                             phase ^= 1u;
@@ -354,8 +385,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                 if (!mx_warp_wait(&tmem_full[buf], uint32_t(li >> 1) & 1u, abort_flag, 77)) break;
                 tc_fence_after();
                 // issuer i has stages of this tile if its first one is before the tile's end
-                const int before = li * blocks;
-                auto has = [&](int i) { return ((i - before) & (kMxIssuers - 1)) < blocks; };
+                const int lead = li * pairs % issuers;
+                auto has = [&](int i) { return i < issuers && (i >= lead ? i - lead : i + issuers - lead) < pairs; };
                 const uint32_t to = smem_u32(sums + (part * args.rounds + li) * args.tokens * own_rows + row % own_rows);
                 const uint32_t acc = tmem + (uint32_t(q * 32) << 16) + uint32_t(buf * kMxIssuers * kMxAccCols);
                 for (int t = 0; t < ntok; ++t) {
@@ -384,6 +415,12 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     cluster_arrive();
     cluster_wait();
     tc_fence_after();
+    if (*abort_flag && threadIdx.x == 0) {
+        // a wait gave up (else every copy has been consumed): a quarter of a second, in which copies land
+        const long long t0 = clock64();
+        while (clock64() - t0 < kWaitTimeoutCycles / 8) {
+        }
+    }
     if (warp == kMxPrepWarp) tmem_dealloc(tmem, 512);
 
     // The parts' sums of this block's rows, in part order.
@@ -441,18 +478,19 @@ bool fp4_matvec_mx(const void *x, const void *w, const void *sf, void *y, int T,
     a.K = K;
     a.tokens = T < kMxTokens ? T : kMxTokens;
     a.cols = (kMxPieces * a.tokens + 7) / 8 * 8;
-    // The parts of K that leave a block the fewest bytes to stream, while its tokens
-    // and sums leave room for eight stages.
+    // The parts of K that leave a block the least to stream (the rows of a stage count as
+    // 72 at least: what its instructions take), while its tokens and sums leave room.
     int64_t best_rows = 0, clusters = 0;
-    for (a.parts = 1; a.parts <= kMxMaxParts && a.parts <= all_blocks; a.parts *= 2) {
+    for (a.parts = 1; a.parts <= kMxMaxParts && 2 * a.parts <= all_blocks + 1; a.parts *= 2) {
         const int64_t units = resident_clusters(kernel, a.parts, kMxThreads, kMxSmem);
         a.rounds = int((N + kTileRows * units - 1) / (kTileRows * units));
         a.rows = int((N + a.rounds * units - 1) / (a.rounds * units) + 7) / 8 * 8;
-        a.blocks = (all_blocks + a.parts - 1) / a.parts;
+        a.blocks = ((all_blocks + 1) / 2 + a.parts - 1) / a.parts * 2;
         if (a.blocks > 1024 || a.rounds > 1024) continue;
-        a.stages = mx_smem_bytes(a, kMxMaxStages) <= kMxSmem ? kMxMaxStages : kMxMaxStages - kMxIssuers;
+        a.stages = mx_smem_bytes(a, kMxMaxStages) <= kMxSmem ? kMxMaxStages : 4;
         if (mx_smem_bytes(a, a.stages) > kMxSmem) continue;
-        const int64_t stream_rows = int64_t(a.rounds) * a.rows * a.blocks;
+        a.issuers = a.stages == 4 ? 4 : 3;
+        const int64_t stream_rows = int64_t(a.rounds) * (a.rows > 72 ? a.rows : 72) * a.blocks;
         if (best.parts == 0 || stream_rows < best_rows) {
             best = a;
             best_rows = stream_rows;
@@ -464,7 +502,7 @@ bool fp4_matvec_mx(const void *x, const void *w, const void *sf, void *y, int T,
     CUtensorMap tm;
     *status = cudaErrorUnknown;
     if (!encode_weights4(&tm, w, uint64_t(N), uint64_t(K / 2), 1, uint64_t(K / 2), uint64_t(all_blocks), kMxBlockK / 2,
-                         best.rows, 1, 1))
+                         best.rows, 1, kMxStageBlocks))
         return true;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(clusters * best.parts), unsigned((T + best.tokens - 1) / best.tokens));
