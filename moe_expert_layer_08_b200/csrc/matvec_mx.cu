@@ -27,7 +27,10 @@
 // costs its thread about 70 cycles, so three or four threads issue, each every third or
 // fourth stage into an accumulator of its own.  The rows of a tile are as few as fill every
 // cluster equally often.
-// N = 14336, K = 7168: 19.7 us for one token, 27.0 for eight (26.0 and 30.6 by mma.sync).
+// N = 14336, K = 7168: 14.4 us for one token and 20.6 for eight (26.0 and 30.6 by
+// mma.sync), N = 4096: 8.3.  While it streams, one token's blocks take the HBM's rate;
+// 2.4 us pass before (the tokens) and 2.5 after (sums, the cluster).  Eight tokens'
+// operand leaves room for four stages, which are too few to cover a load's latency.
 #include "moe_common.cuh"
 #include "moe_internal.h"
 
@@ -46,9 +49,9 @@ constexpr int kMxSmem = 232448;
 // 5-8 issue and 16-19 drain
 constexpr int kMxThreads = 20 * 32;
 constexpr int kMxPrepWarp = 5, kMxPrepWarps = 15, kMxEpiWarp = 16;
-constexpr int kMxHeld = 4;           // pieces of the tokens a preparing warp holds in registers
 // TMEM columns: two accumulators per issuer, the stages' scale images of both operands
-constexpr int kMxAccCols = kMxPieces * kMxTokens;  // a multiple of 16
+constexpr int kMxAccCols = kMxPieces * kMxTokens;
+static_assert(kMxAccCols == 32, "one load of an accumulator");
 constexpr int kMxSfaCol = 2 * kMxIssuers * kMxAccCols;
 constexpr int kMxSfCols = 4 * kMxStageBlocks;  // of a stage and operand
 constexpr int kMxSfbCol = kMxSfaCol + kMxSfCols * kMxMaxStages;
@@ -99,11 +102,6 @@ __device__ __forceinline__ void cluster_put(uint32_t at, int cta, uint32_t v) {
 __device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_ld_4(uint32_t addr, float (&r)[4]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
-                 : "r"(addr));
-}
 __device__ __forceinline__ bool mx_warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int where) {
     return __all_sync(0xFFFFFFFFu, mbar_wait_cycles(bar, parity, abort, g_matvec_mx_err, where));
 }
@@ -313,15 +311,18 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                 }
             }
         };
-        uint4 held[kMxHeld];
-        Unit u = {w0 / ntok, w0 % ntok}, v = u;
+        // (one copy of the code, which every block fetches anew: units come three ahead)
+        Unit u = {w0 / ntok, w0 % ntok}, ahead = u;
+        uint4 raw[3];
 #pragma unroll
-        for (int i = 0; i < kMxHeld; ++i, next(v))
-            if (v.s < pairs) held[i] = fetch(v);
-#pragma unroll
-        for (int i = 0; i < kMxHeld; ++i, next(u))
-            if (u.s < pairs) put(u, held[i]);
-        for (; u.s < pairs; next(u)) put(u, fetch(u));
+        for (int i = 0; i < 3; ++i, next(ahead)) raw[i] = fetch(ahead);
+#pragma unroll 1
+        for (; u.s < pairs; next(u), next(ahead)) {
+            put(u, raw[0]);
+            raw[0] = raw[1];
+            raw[1] = raw[2];
+            raw[2] = fetch(ahead);
+        }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         asm volatile("bar.sync 1, %0;" ::"n"(kMxPrepWarps * 32) : "memory");
 
@@ -389,17 +390,22 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                 auto has = [&](int i) { return i < issuers && (i >= lead ? i - lead : i + issuers - lead) < pairs; };
                 const uint32_t to = smem_u32(sums + (part * args.rounds + li) * args.tokens * own_rows + row % own_rows);
                 const uint32_t acc = tmem + (uint32_t(q * 32) << 16) + uint32_t(buf * kMxIssuers * kMxAccCols);
-                for (int t = 0; t < ntok; ++t) {
-                    float r[kMxIssuers][4], v = 0.0f;
+                float v[kMxTokens];
 #pragma unroll
-                    for (int i = 0; i < kMxIssuers; ++i)
-                        if (has(i)) tmem_ld_4(acc + uint32_t(i * kMxAccCols + kMxPieces * t), r[i]);
+                for (int t = 0; t < kMxTokens; ++t) v[t] = 0.0f;
+                for (int i = 0; i < issuers; ++i) {
+                    if (!has(i)) continue;
+                    uint32_t r[32];
+                    tmem_ld_32x32(acc + uint32_t(i * kMxAccCols), r);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < kMxIssuers; ++i)
-                        if (has(i)) v += r[i][0] + (r[i][1] + (r[i][2] + r[i][3]));
-                    cluster_put(to + uint32_t(t * own_rows * 4), adds, __float_as_uint(v));
+                    for (int t = 0; t < kMxTokens; ++t)
+                        v[t] += __uint_as_float(r[4 * t]) +
+                                (__uint_as_float(r[4 * t + 1]) + (__uint_as_float(r[4 * t + 2]) + __uint_as_float(r[4 * t + 3])));
                 }
+#pragma unroll
+                for (int t = 0; t < kMxTokens; ++t)
+                    if (t < ntok) cluster_put(to + uint32_t(t * own_rows * 4), adds, __float_as_uint(v[t]));
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&tmem_empty[buf]);
@@ -479,7 +485,8 @@ bool fp4_matvec_mx(const void *x, const void *w, const void *sf, void *y, int T,
     a.tokens = T < kMxTokens ? T : kMxTokens;
     a.cols = (kMxPieces * a.tokens + 7) / 8 * 8;
     // The parts of K that leave a block the least to stream (the rows of a stage count as
-    // 72 at least: what its instructions take), while its tokens and sums leave room.
+    // 72 at least, what its instructions take, and a block of a token as 14), while its
+    // tokens and sums leave room.
     int64_t best_rows = 0, clusters = 0;
     for (a.parts = 1; a.parts <= kMxMaxParts && 2 * a.parts <= all_blocks + 1; a.parts *= 2) {
         const int64_t units = resident_clusters(kernel, a.parts, kMxThreads, kMxSmem);
@@ -490,7 +497,7 @@ bool fp4_matvec_mx(const void *x, const void *w, const void *sf, void *y, int T,
         a.stages = mx_smem_bytes(a, kMxMaxStages) <= kMxSmem ? kMxMaxStages : 4;
         if (mx_smem_bytes(a, a.stages) > kMxSmem) continue;
         a.issuers = a.stages == 4 ? 4 : 3;
-        const int64_t stream_rows = int64_t(a.rounds) * (a.rows > 72 ? a.rows : 72) * a.blocks;
+        const int64_t stream_rows = (int64_t(a.rounds) * (a.rows > 72 ? a.rows : 72) + 14 * a.tokens) * a.blocks;
         if (best.parts == 0 || stream_rows < best_rows) {
             best = a;
             best_rows = stream_rows;
