@@ -2,6 +2,10 @@
 step (norm -> routed experts and a shared expert held in 4 bits -> norm into the
 residual stream) and a training step over unquantised experts with its
 gradients."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -131,3 +135,68 @@ def test_training_step(moe):
         off = float((got.to(F64) - want).norm() / want.norm())
         assert off <= room, (name, off)
     assert not bool(dw1[E - 1].any()) and not bool(dw2[E - 1].any())
+
+
+def test_two_streams_at_once(moe):
+    """Calls of the same shapes under way on two streams, a graph's among them."""
+    x, w = normal(1, 16, 2048), normal(2, 2, 520, 2048)
+    off = torch.tensor([0, 7, 16], dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    codes = torch.randint(0, 256, (9000, 1024), dtype=torch.uint8, device="cuda", generator=g)
+    scales = torch.randint(120, 130, (9000, 64), dtype=torch.uint8, device="cuda", generator=g)
+    inputs = [(x, x[:8].contiguous()), (x * 2, (x[:8] * 3).contiguous())]
+    expect = [(moe.grouped_matmul(a, w, off), moe.fp4_matvec(b, codes, scales)) for a, b in inputs]
+    graph_out = torch.empty_like(expect[0][1])
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        moe.fp4_matvec(inputs[0][1], codes, scales, out=graph_out)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append((moe.grouped_matmul(inputs[i][0], w, off), moe.fp4_matvec(inputs[i][1], codes, scales)))
+        graph.replay()
+    torch.cuda.synchronize()
+    for i in range(2):
+        for y, z in got[i]:
+            assert torch.equal(y, expect[i][0]) and torch.equal(z, expect[i][1])
+    assert torch.equal(graph_out, expect[0][1])
+    del graph
+
+
+FIRST = """
+import torch
+import moe_expert_layer_08_b200 as moe
+torch.manual_seed(0)
+B = torch.bfloat16
+x, w = torch.randn((16, 2048), dtype=B, device="cuda"), torch.randn((2, 520, 2048), dtype=B, device="cuda")
+off = torch.tensor([0, 7, 16], dtype=torch.int32, device="cuda")
+codes = torch.randint(0, 256, (520, 1024), dtype=torch.uint8, device="cuda")
+scales = torch.randint(120, 130, (520, 64), dtype=torch.uint8, device="cuda")
+gain = torch.randn(2048, dtype=B, device="cuda")
+y, z = torch.empty((16, 520), dtype=B, device="cuda"), torch.empty((8, 520), dtype=B, device="cuda")
+ws = torch.empty(moe.grouped_workspace_bytes(), dtype=torch.uint8, device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    n = moe.norm_before(x, gain).y
+    moe.grouped_matmul(n, w, off, out=y, workspace=ws)
+    moe.fp4_matvec(n[:8], codes, scales, out=z)
+graph.replay()
+torch.cuda.synchronize()
+n2 = moe.norm_before(x, gain).y
+assert torch.equal(n, n2)
+assert torch.equal(y, moe.grouped_matmul(n2, w, off)) and torch.equal(z, moe.fp4_matvec(n2[:8], codes, scales))
+assert moe.check_device_error(ws) == 0
+print("same")
+"""
+
+
+def test_first_calls_inside_a_capture(moelib):
+    """A process whose first use of the operators is captured into a graph."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0 and done.stdout.strip() == "same", done.stderr[-2000:]
