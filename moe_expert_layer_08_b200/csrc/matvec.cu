@@ -18,8 +18,9 @@
 // that largest one (it is then off by at most 2^-40 of it, less than a rounding
 // of the fp32 sum).  The group scale multiplies the fp32 sum of its group.  The
 // slices' sums meet in shared memory and are added in slice order.
-// MX weights with K a multiple of 128 have a kernel of their own, without decoding;
-// this one takes NVFP4, other K, and tokens too long for that one's shared memory.
+// With K a multiple of 128 the block-scaled tensor cores take MX weights, and NVFP4
+// weights for one or two tokens, in a kernel without decoding; this one takes the rest,
+// and tokens too long for that one's shared memory.
 // What bounds it is the decoding: about 50 instructions per warp and 512 weights,
 // half of them on the integer pipe, against 11 cycles of an SM's share of HBM.
 #include <cuda_fp16.h>
@@ -429,7 +430,7 @@ extern "C" moe_status_t moe_fp4_matvec(const void *x_bf16, const void *w_fp4, co
     if (dev.status != MOE_OK) return dev.status;
     cudaError_t e = cudaSuccess;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (format == MOE_FP4_MX && fp4_matvec_mx(x_bf16, w_fp4, w_sf, y_bf16, T, N, K, st, &e))
+    if (fp4_matvec_tc(format == MOE_FP4_NVFP4, x_bf16, w_fp4, w_sf, y_bf16, T, N, K, st, &e))
         return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     MatvecArgs a{};
     a.x = static_cast<const __nv_bfloat16 *>(x_bf16);

@@ -1,11 +1,11 @@
-// matvec_mx.cu -- the product of a few bf16 token vectors with an MX weight
-// matrix (E2M1 codes, one UE8M0 scale per 32) for K a multiple of 128:
-//   y[t, n] = sum_k x[t, k] * s[n, k / 32] * c[n, k]
-// bound by the HBM stream of N K (1/2 + 1/32) bytes once nothing is done per
-// weight.  (Decoding the codes in registers for mma.sync is bound by the integer
-// pipe, at a third of that stream.)  So the tensor cores take the codes and their
-// scales as they are: tcgen05.mma.kind::mxf8f6f4 with the weights as its 128-row
-// E2M1 operand, and everything else is per token, once.
+// matvec_tc.cu -- the product of a few bf16 token vectors with a weight matrix held in
+// 4 bits, on the block-scaled tensor cores, for K a multiple of 128:
+//   y[t, n] = sum_k x[t, k] * s[n, k / G] * c[n, k]
+// c E2M1, s UE8M0 with G = 32 (MX) or UE4M3 with G = 16 (NVFP4, one or two tokens);
+// bound by the HBM stream of N K (1/2 + 1/G) bytes once nothing is done per weight.
+// (Decoding the codes in registers for mma.sync is bound by the integer pipe, at a
+// third of that stream.)  So tcgen05.mma.kind::mxf8f6f4 takes the codes as they are, as
+// its 128-row E2M1 operand, and everything else is per token or per group.
 //
 // The tokens are the E4M3 operand, each element as four columns whose scales carry
 // the piece's weight: with 2^e the smallest power with max|x| <= 448 * 2^e over the
@@ -17,20 +17,26 @@
 // largest of its 32.  E4M3 has no infinities: an element that is not finite enters as
 // zero and its token's results are computed again by definition.
 //
+// MX: the weights' scales go to the tensor cores too, and a tile's sums stay in TMEM
+// over all of K.  NVFP4: its scales are no power of two, so the weights' scales are
+// ones there, each MMA (32 elements) has columns of its own, twice the pieces (the
+// halves of the 32 apart, zeros elsewhere), and the draining warps multiply a group's
+// sum by its row's scale: with more than two tokens that is more work than decoding.
+//
 // A block streams tiles of up to 128 rows and a part of K, 256 elements a stage (with
 // 128 the loading thread, at 340 cycles a stage, held everything up), to its shared
-// memory by TMA (which spreads the 4-bit codes to bytes) with the stage's
-// scales by cp.async beside them; blocks of a cluster have the parts of K of the same
-// rows, write their fp32 sums to the block that adds a row's (in part order) through
-// distributed shared memory, and prepare their part of the tokens once, for all their
-// tiles.  A tcgen05 instruction
-// costs its thread about 70 cycles, so three or four threads issue, each every third or
-// fourth stage into an accumulator of its own.  The rows of a tile are as few as fill every
-// cluster equally often.
-// N = 14336, K = 7168: 14.4 us for one token and 20.6 for eight (26.0 and 30.6 by
-// mma.sync), N = 4096: 8.3.  While it streams, one token's blocks take the HBM's rate;
-// 2.4 us pass before (the tokens) and 2.5 after (sums, the cluster).  Eight tokens'
-// operand leaves room for four stages, which are too few to cover a load's latency.
+// memory by TMA (which spreads the 4-bit codes to bytes) with the stage's scales by
+// cp.async beside them; blocks of a cluster have the parts of K of the same rows, write
+// their fp32 sums to the block that adds a row's (in part order) through distributed
+// shared memory, and prepare their part of the tokens once, for all their tiles.  A
+// tcgen05 instruction costs its thread about 75 cycles, so two to four threads issue,
+// each every second to fourth stage, with sums of its own.  The rows of a tile are as
+// few as fill every cluster equally often.
+// N = 14336, K = 7168: MX 14.4 us for one token and 20.5 for eight, NVFP4 18.9 for one
+// and 23.7 for two (by mma.sync 26.0, 30.6, 31.7 and 32.4).  While it streams, one MX
+// token's blocks take the HBM's rate; 2.4 us pass before (the tokens) and 2.5 after
+// (sums, the cluster).  Eight tokens' operand leaves room for four stages, which are too
+// few to cover a load's latency; NVFP4 is bound by its two issuers, 900 cycles a stage.
 #include "moe_common.cuh"
 #include "moe_internal.h"
 
@@ -43,28 +49,35 @@ constexpr int kMxPieces = 4;         // of a token's element: MMA columns
 constexpr int kMxTokens = 8;         // of a pass
 constexpr int kMxIssuers = 4;        // at most
 constexpr int kMxMaxStages = 6;
+constexpr int kMxNvTokens = 2;       // of a pass with NVFP4 weights
+constexpr int kMxSets = 2;           // NVFP4: issuers, each with four draining warps of its own
 constexpr int kMxMaxParts = 8;
 constexpr int kMxSmem = 232448;
 // warps: 0 loads codes, 1-4 scales (a thread a row), 5-19 prepare the tokens, then
-// 5-8 issue and 16-19 drain
+// 5-8 issue and 16-19 (NVFP4: 12-19) drain
 constexpr int kMxThreads = 20 * 32;
-constexpr int kMxPrepWarp = 5, kMxPrepWarps = 15, kMxEpiWarp = 16;
+constexpr int kMxPrepWarp = 5, kMxPrepWarps = 15;
 // TMEM columns: two accumulators per issuer, the stages' scale images of both operands
 constexpr int kMxAccCols = kMxPieces * kMxTokens;
 static_assert(kMxAccCols == 32, "one load of an accumulator");
 constexpr int kMxSfaCol = 2 * kMxIssuers * kMxAccCols;
 constexpr int kMxSfCols = 4 * kMxStageBlocks;  // of a stage and operand
 constexpr int kMxSfbCol = kMxSfaCol + kMxSfCols * kMxMaxStages;
-static_assert(kMxEpiWarp % 4 == 0 && kMxSfbCol + kMxSfCols * kMxMaxStages <= 512, "TMEM");
+static_assert(kMxSfbCol + kMxSfCols * kMxMaxStages <= 512, "TMEM");
 constexpr int kMxMisc = 512;
+// TMEM columns with NVFP4: the sums of a stage's eight MMAs, 16 columns each of which
+// one token uses 8 (the next MMA's lie over the others); scales as above
+constexpr int kNvBufCols = 128, kNvShortBufCols = 80;
+constexpr int kNvSfaCol = 4 * kNvShortBufCols, kNvSfbCol = kNvSfaCol + 4 * kMxSets;
+static_assert(kNvSfaCol >= kMxSets * kNvBufCols && kNvSfbCol + kMxSfCols * kMxMaxStages <= 512, "TMEM");
 
 struct MxArgs {
     const __nv_bfloat16 *x;   // [T, K]
     const uint8_t *w;         // [N, K / 2]
-    const uint8_t *sf;        // [N, K / 32]
+    const uint8_t *sf;        // [N, K / 32] or [N, K / 16]
     __nv_bfloat16 *y;         // [T, N]
     int T, N, K;
-    int tokens;               // of a pass (blockIdx.y), <= kMxTokens
+    int tokens;               // of a pass (blockIdx.y)
     int cols;                 // of the tokens' operand in shared memory, a multiple of 8
     int rows;                 // of a tile, a multiple of 8
     int parts;                // of K: blocks of a cluster
@@ -78,14 +91,17 @@ struct MxArgs {
 // block of tokens its columns, and the regions lie in an order in which no such read
 // leaves them.
 __host__ __device__ inline int mx_stage_bytes(const MxArgs &a) { return kMxStageBlocks * a.rows * 128; }
-int mx_smem_bytes(const MxArgs &a, int stages) {
-    const int ring = stages * mx_stage_bytes(a), rest = a.blocks * a.cols * (128 + 16) + stages * kMxStageBlocks * kSfBlockBytes +
-                                                        a.rounds * a.tokens * kTileRows * 4 + kMxMisc;
+// scales of a stage: an image a block, or 16 bytes a row
+__host__ __device__ constexpr int mx_scale_bytes(bool nv) { return nv ? kTileRows * 16 : kMxStageBlocks * kSfBlockBytes; }
+int mx_smem_bytes(bool nv, const MxArgs &a, int stages) {
+    const int ring = stages * mx_stage_bytes(a);
+    const int rest = a.blocks * a.cols * (128 + 16) + stages * mx_scale_bytes(nv) + (nv ? kSfBlockBytes : 0) +
+                     a.rounds * a.tokens * kTileRows * 4 * (nv ? kMxSets : 1) + kMxMisc;
     // the last stage's 128 rows end inside
     return 1024 + ring + (rest > kTileRows * 128 ? rest : kTileRows * 128);
 }
 
-__device__ int g_matvec_mx_err[8];  // where a wait that gave up leaves its mark (the outputs become NaN)
+__device__ int g_matvec_tc_err[8];  // where a wait that gave up leaves its mark (the outputs become NaN)
 
 __device__ __forceinline__ uint32_t cluster_rank_of() {
     uint32_t r;
@@ -103,7 +119,7 @@ __device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ bool mx_warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int where) {
-    return __all_sync(0xFFFFFFFFu, mbar_wait_cycles(bar, parity, abort, g_matvec_mx_err, where));
+    return __all_sync(0xFFFFFFFFu, mbar_wait_cycles(bar, parity, abort, g_matvec_tc_err, where));
 }
 // Eight bf16; elements that are not finite as zeros.
 __device__ __forceinline__ bool finite8(uint4 u, float (&v)[8]) {
@@ -137,26 +153,31 @@ __device__ __forceinline__ void leave(float (&v)[8], uint2 piece, float next) {
     }
 }
 
+template <bool kNv>
 __global__ void __launch_bounds__(kMxThreads, 1)
-    fp4_matvec_mx_kernel(const __grid_constant__ CUtensorMap tmap_w, const MxArgs args) {
+    fp4_matvec_tc_kernel(const __grid_constant__ CUtensorMap tmap_w, const MxArgs args) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int kStages = args.stages;
+    constexpr int kEpiWarp = kNv ? 12 : 16, kSets = kNv ? kMxSets : 1, kTokenCols = kNv ? 2 * kMxPieces : kMxPieces;
+    constexpr int kScaleBytes = mx_scale_bytes(kNv), kGroup = kNv ? 16 : 32;
     const int stage_bytes = mx_stage_bytes(args);
     uint8_t *toks = ring + kStages * stage_bytes;                      // [block][column] 128 bytes, swizzled
-    uint8_t *sfa = toks + args.blocks * args.cols * 128;               // [stage] images
-    uint8_t *sfb = sfa + kStages * kMxStageBlocks * kSfBlockBytes;                      // [block][column] 16 bytes, 4 of them scales
-    float *sums = reinterpret_cast<float *>(sfb + args.blocks * args.cols * 16);  // [part][round][token][this block's rows]
-    uint64_t *full = reinterpret_cast<uint64_t *>(sums + args.rounds * args.tokens * kTileRows);
+    uint8_t *sfa = toks + args.blocks * args.cols * 128;               // [stage] images, or rows of 16 bytes
+    uint8_t *sfb = sfa + kStages * kScaleBytes;                        // [block][column] 16 bytes, 4 of them scales
+    uint8_t *ones = sfb + args.blocks * args.cols * 16;                // NVFP4: an image of ones
+    // [part][set][round][token][this block's rows]
+    float *sums = reinterpret_cast<float *>(ones + (kNv ? kSfBlockBytes : 0));
+    uint64_t *full = reinterpret_cast<uint64_t *>(sums + kSets * args.rounds * args.tokens * kTileRows);
     uint64_t *empty = full + kMxMaxStages;
-    uint64_t *tmem_full = empty + kMxMaxStages;   // [2]
-    uint64_t *tmem_empty = tmem_full + 2;         // [2]
-    uint64_t *mma_done = tmem_empty + 2;          // [issuer]
+    uint64_t *tmem_full = empty + kMxMaxStages;   // [2]; NVFP4: [issuer][2]
+    uint64_t *tmem_empty = tmem_full + 4;
+    uint64_t *mma_done = tmem_empty + 4;          // [issuer]
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(mma_done + kMxIssuers);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     uint32_t *bad = tmem_holder + 2;              // tokens with an element that is not finite
     uint32_t *flags = bad + 1;                    // [part] its bad tokens; bit 31: a wait of its gave up
-    static_assert((2 * kMxMaxStages + 4 + kMxIssuers) * 8 + (3 + kMxMaxParts) * 4 <= kMxMisc, "barriers and flags");
+    static_assert((2 * kMxMaxStages + 8 + kMxIssuers) * 8 + (3 + kMxMaxParts) * 4 <= kMxMisc, "barriers and flags");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int parts = args.parts, part = parts > 1 ? int(cluster_rank_of()) : 0;
@@ -173,10 +194,10 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1 + 128);  // the codes' copy, the threads that bring scales
-            mbar_init(&empty[s], 1);
+            mbar_init(&empty[s], kNv ? 1 + 4 : 1);  // the MMAs, the warps that read scales
         }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(&tmem_full[b], issuers);
+        for (int b = 0; b < 4; ++b) {
+            mbar_init(&tmem_full[b], kNv ? 1 : issuers);
             mbar_init(&tmem_empty[b], 4);
         }
         for (int i = 0; i < kMxIssuers; ++i) mbar_init(&mma_done[i], 1);
@@ -206,7 +227,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             bool ok = true;
             for (int tile = first; ok && tile < tiles; tile += step)
                 for (int s = 0; s < pairs; ++s) {
-                    ok = mbar_wait_cycles(&empty[stage], phase ^ 1u, abort_flag, g_matvec_mx_err, 71);
+                    ok = mbar_wait_cycles(&empty[stage], phase ^ 1u, abort_flag, g_matvec_tc_err, 71);
                     if (!ok) break;
                     // (a block past K is filled with zeros, and its bytes count)
                     mbar_arrive_expect_tx(&full[stage], uint32_t(kMxStageBlocks * args.rows * 64));
@@ -220,27 +241,42 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         __syncwarp();
     } else if (warp < kMxPrepWarp) {
         // ---------------------------------------------------------------- scales: thread = row
-        // four bytes a block, to row r's place in the image: (r % 32) * 16 + (r / 32) * 4
+        // MX: four bytes a block, to row r's place in the image, (r % 32) * 16 + (r / 32) * 4;
+        // NVFP4: eight a block, both at once where they are aligned
         const int r = int(threadIdx.x) - 32;
-        const int64_t ld = args.K / 32;
-        const uint32_t dst = smem_u32(sfa) + uint32_t((r & 31) * 16 + (r >> 5) * 4);
+        const int64_t ld = args.K / kGroup;
+        const uint32_t dst = smem_u32(sfa) + uint32_t(kNv ? r * 16 : (r & 31) * 16 + (r >> 5) * 4);
+        const bool whole = args.K % (kMxStageBlocks * kMxBlockK) == 0;
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
         for (int tile = first; ok && tile < tiles; tile += step) {
             const int n = tile * args.rows + r;
             const bool real = r < args.rows && n < args.N;
-            const uint8_t *src = args.sf + (real ? n * ld : 0) + kb0 * 4;
+            const uint8_t *src = args.sf + (real ? n * ld : 0) + kb0 * (kMxBlockK / kGroup);
             for (int s = 0; s < pairs; ++s) {
                 ok = mx_warp_wait(&empty[stage], phase ^ 1u, abort_flag, 73);
                 if (!ok) break;
+                if constexpr (kNv) {
+                    const uint32_t to = dst + stage * kScaleBytes;
+                    const uint8_t *from = src + s * 16;
+                    if (real && whole)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+                    else if (real) {
 #pragma unroll
-                for (int b = 0; b < kMxStageBlocks; ++b)
-                    if (real && kMxStageBlocks * s + b < blocks)
-                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
-                                         dst + (stage * kMxStageBlocks + b) * kSfBlockBytes),
-                                     "l"(src + (kMxStageBlocks * s + b) * 4)
-                                     : "memory");
+                        for (int b = 0; b < kMxStageBlocks; ++b)
+                            if (kMxStageBlocks * s + b < blocks)
+                                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to + b * 8), "l"(from + b * 8) : "memory");
+                    }
+                } else {
+#pragma unroll
+                    for (int b = 0; b < kMxStageBlocks; ++b)
+                        if (real && kMxStageBlocks * s + b < blocks)
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                                             dst + (stage * kMxStageBlocks + b) * kSfBlockBytes),
+                                         "l"(src + (kMxStageBlocks * s + b) * 4)
+                                         : "memory");
+                }
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&full[stage])) : "memory");
                 if (++stage == kStages) {
                     stage = 0;
@@ -288,7 +324,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                 low |= v[i] != 0.0f && fabsf(v[i]) < 0.015625f;
             }
             low = __any_sync(0xFFFFFFFFu, low);
-            const int kb = kMxStageBlocks * u.s + block, col = kMxPieces * u.t;
+            const int kb = kMxStageBlocks * u.s + block, col = kTokenCols * u.t;
             uint8_t *to = toks + (kb * args.cols + col) * 128 + (lane & 1) * 8;
             const int slot = (lane & 15) >> 1;
             uint8_t *image = sfb + (kb * args.cols + col) * 16 + (lane >> 2 & 3);
@@ -304,10 +340,17 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                 piece[3] = piece_of(v);
             }
             if (inside(u)) {
+                const int half = kNv ? lane >> 1 & 1 : 0;  // of a group of 32 the 16 this lane's are in
 #pragma unroll
                 for (int p = 0; p < kMxPieces; ++p) {
-                    *reinterpret_cast<uint2 *>(to + p * 128 + ((slot ^ ((col + p) & 7)) << 4)) = piece[p];
-                    if ((lane & 3) == 0) image[p * 16] = uint8_t(e + 127 - (p == 0 ? 0 : p == 1 ? 4 : p == 2 ? 22 : 26));
+                    auto place = [&](int c) { return reinterpret_cast<uint2 *>(to + c * 128 + ((slot ^ ((col + c) & 7)) << 4)); };
+                    *place(half * kMxPieces + p) = piece[p];
+                    if (kNv) *place((1 - half) * kMxPieces + p) = make_uint2(0, 0);
+                    if ((lane & 3) == 0) {
+                        const uint8_t scale = uint8_t(e + 127 - (p == 0 ? 0 : p == 1 ? 4 : p == 2 ? 22 : 26));
+                        image[p * 16] = scale;
+                        if (kNv) image[(kMxPieces + p) * 16] = scale;
+                    }
                 }
             }
         };
@@ -323,6 +366,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             raw[1] = raw[2];
             raw[2] = fetch(ahead);
         }
+        if (kNv && w0 == 0) reinterpret_cast<uint4 *>(ones)[lane] = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         asm volatile("bar.sync 1, %0;" ::"n"(kMxPrepWarps * 32) : "memory");
 
@@ -330,17 +374,52 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             if (lane == 0) {
                 // -------------------------------------------------------- MMA issuer
                 bool ok = true;
+                // NVFP4: a stage's MMAs each have columns of their own, two buffers of them
+                // for one token, one for two; the weights' scales are for the draining warps
+                const int bufs = args.tokens == 1 ? 2 : 1, each = args.tokens == 1 ? 8 : 16;
+                const uint32_t unit = tmem + uint32_t(kNvSfaCol + 4 * w0);
+                if constexpr (kNv) tc_cp_sf(unit, smem_desc_sf(smem_u32(ones)));
                 const uint32_t mma_n = uint32_t((args.cols + 15) / 16 * 16);
-                int stage = w0, li = 0, s = w0;  // s: this issuer's next stage, counted in the tile
+                int stage = w0, li = 0, s = w0, used = 0;  // s: this issuer's next stage, counted in the tile
                 uint32_t phase = 0;
                 for (int tile = first; ok && tile < tiles; tile += step, ++li, s -= pairs) {
                     const int buf = li & 1, s_first = s;
-                    if (!mbar_wait_cycles(&tmem_empty[buf], (uint32_t(li >> 1) & 1u) ^ 1u, abort_flag, g_matvec_mx_err, 75)) break;
+                    if (!kNv && !mbar_wait_cycles(&tmem_empty[buf], (uint32_t(li >> 1) & 1u) ^ 1u, abort_flag, g_matvec_tc_err, 75))
+                        break;
                     tc_fence_after();
                     const uint32_t acc = tmem + uint32_t((buf * kMxIssuers + w0) * kMxAccCols);
                     for (; s < pairs; s += issuers) {
-                        ok = mbar_wait_cycles(&full[stage], phase, abort_flag, g_matvec_mx_err, 76);
+                        ok = mbar_wait_cycles(&full[stage], phase, abort_flag, g_matvec_tc_err, 76);
                         if (!ok) break;
+                        if constexpr (kNv) {
+                            const int b = used % bufs;
+                            ok = mbar_wait_cycles(&tmem_empty[2 * w0 + b], (uint32_t(used / bufs) & 1u) ^ 1u, abort_flag, g_matvec_tc_err, 78);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint32_t d = tmem + uint32_t(bufs == 2 ? (2 * w0 + b) * kNvShortBufCols : w0 * kNvBufCols);
+                            const uint32_t colb = tmem + uint32_t(kNvSfbCol + kMxSfCols * stage);
+#pragma unroll
+                            for (int h = 0; h < kMxStageBlocks; ++h) {
+                                const int kb = kMxStageBlocks * s + h;
+                                if (kb >= blocks) break;
+                                tc_cp_sf(colb + 4 * h, smem_desc_sf(smem_u32(sfb + kb * args.cols * 16)));
+                                const uint64_t ad = smem_desc_sw128(smem_u32(ring + stage * stage_bytes + h * args.rows * 128));
+                                const uint64_t bd = smem_desc_sw128(smem_u32(toks + kb * args.cols * 128));
+#pragma unroll
+                                for (int ks = 0; ks < 4; ++ks)
+                                    tc_mma_mxf8f6f4(d + uint32_t((4 * h + ks) * each), ad + uint64_t(2 * ks), bd + uint64_t(2 * ks),
+                                                    idesc_mxf8f6f4(16u, uint32_t(ks)), unit, colb + 4 * h, 0u);
+                            }
+                            tc_commit(&empty[stage]);
+                            tc_commit(&tmem_full[2 * w0 + b]);
+                            ++used;
+                            stage += issuers;
+                            if (stage >= kStages) {
+                                stage -= kStages;
+                                phase ^= 1u;
+                            }
+                            continue;
+                        }
                         // the scales were written by ordinary accesses of other threads
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         tc_fence_after();
@@ -367,7 +446,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                         }
                     }
                     if (!ok) break;
-                    tc_commit(&tmem_full[buf]);
+                    if (!kNv) tc_commit(&tmem_full[buf]);
                 }
                 // all issued MMAs must be finished before TMEM is released
                 tc_commit(&mma_done[w0]);
@@ -376,12 +455,87 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                 }
             }
             __syncwarp();
-        } else if (warp >= kMxEpiWarp) {
+        } else if (warp >= kEpiWarp) {
             // ------------------------------------------------------------ sums: thread = row
             const int q = warp & 3, row = q * 32 + lane, adds = row / own_rows;  // the block that adds this row's
             int li = 0;
             cluster_wait();
-            for (int tile = first; tile < tiles; tile += step, ++li) {
+            if constexpr (kNv) {
+                // every second stage: the sums of its 16 groups of 16 times the row's scales
+                const int set = (warp - kEpiWarp) >> 2, bufs = args.tokens == 1 ? 2 : 1;
+                int s = set, stage = set, used = 0;
+                uint32_t phase = 0;
+                bool ok = true;
+                for (int tile = first; ok && tile < tiles; tile += step, ++li, s -= pairs) {
+                    float acc[kMxNvTokens] = {};
+                    bool nan = false;
+                    for (; s < pairs; s += kMxSets, ++used) {
+                        const int b = used % bufs;
+                        ok = mx_warp_wait(&full[stage], phase, abort_flag, 79) &&
+                             mx_warp_wait(&tmem_full[2 * set + b], uint32_t(used / bufs) & 1u, abort_flag, 77);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint4 sc = *reinterpret_cast<const uint4 *>(sfa + stage * kScaleBytes + row * 16);
+                        const uint32_t scales[4] = {sc.x, sc.y, sc.z, sc.w};
+                        const int groups = min(kMxStageBlocks, blocks - kMxStageBlocks * s) * 8;  // of 16 elements
+                        const uint32_t d = tmem + (uint32_t(q * 32) << 16) +
+                                           uint32_t(bufs == 2 ? (2 * set + b) * kNvShortBufCols : set * kNvBufCols);
+                        auto scale = [&](int g) {
+                            // 2^-8 times a UE4M3 byte's value: its bits are those of an fp16 number of another bias
+                            const uint32_t byte = scales[g >> 2] >> (8 * (g & 3)) & 0x7Fu;
+                            if (g < groups) nan |= byte == 0x7Fu;
+                            __half_raw h;
+                            h.x = static_cast<unsigned short>(byte << 7);
+                            return __half2float(__half(h));
+                        };
+                        auto four = [](const uint32_t *r) {
+                            return __uint_as_float(r[0]) + (__uint_as_float(r[1]) + (__uint_as_float(r[2]) + __uint_as_float(r[3])));
+                        };
+                        if (bufs == 2) {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {  // eight groups of four columns
+                                if (8 * h >= groups) break;
+                                uint32_t r[32];
+                                tmem_ld_32x32(d + uint32_t(32 * h), r);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int g = 0; g < 8; ++g) acc[0] = fmaf(four(r + 4 * g), scale(8 * h + g), acc[0]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int h = 0; h < 4; ++h) {  // two MMAs: of each two tokens' two groups
+                                if (4 * h >= groups) break;
+                                uint32_t r[32];
+                                tmem_ld_32x32(d + uint32_t(32 * h), r);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int g = 0; g < 4; ++g)
+#pragma unroll
+                                    for (int t = 0; t < kMxNvTokens; ++t)
+                                        acc[t] = fmaf(four(r + 16 * (g >> 1) + 8 * t + 4 * (g & 1)), scale(4 * h + g), acc[t]);
+                            }
+                        }
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&tmem_empty[2 * set + b]);
+                            mbar_arrive(&empty[stage]);
+                        }
+                        stage += kMxSets;
+                        if (stage >= kStages) {
+                            stage -= kStages;
+                            phase ^= 1u;
+                        }
+                    }
+                    const uint32_t to =
+                        smem_u32(sums + ((part * kMxSets + set) * args.rounds + li) * args.tokens * own_rows + row % own_rows);
+#pragma unroll
+                    for (int t = 0; t < kMxNvTokens; ++t)
+                        if (t < ntok)
+                            cluster_put(to + uint32_t(t * own_rows * 4), adds, nan ? 0x7FC00000u : __float_as_uint(acc[t] * 256.0f));
+                }
+            }
+            for (int tile = first; !kNv && tile < tiles; tile += step, ++li) {
                 const int buf = li & 1;
                 if (!mx_warp_wait(&tmem_full[buf], uint32_t(li >> 1) & 1u, abort_flag, 77)) break;
                 tc_fence_after();
@@ -413,7 +567,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         }
     }
     __syncwarp();
-    if (warp < kMxEpiWarp) cluster_wait();
+    if (warp < kEpiWarp) cluster_wait();
     __syncthreads();
     if (threadIdx.x < parts) cluster_put(smem_u32(flags + part), int(threadIdx.x), *bad | (*abort_flag ? 1u << 31 : 0u));
     __syncwarp();
@@ -440,7 +594,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         if (r >= args.rows || n >= args.N || (wrong >> t & 1u)) continue;
         const float *at = sums + (li * args.tokens + t) * own_rows + own;
         float v = 0.0f;
-        for (int p = 0; p < parts; ++p) v += at[p * args.rounds * args.tokens * own_rows];
+        for (int p = 0; p < parts * kSets; ++p) v += at[p * args.rounds * args.tokens * own_rows];
         if (wrong >> 31) v = __uint_as_float(0x7FC00000u);
         args.y[int64_t(tok0 + t) * args.N + n] = __float2bfloat16_rn(v);
     }
@@ -454,8 +608,13 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             float v = 0.0f;
             for (int k = lane; k < args.K; k += 32) {
                 const uint32_t c = args.w[int64_t(n) * (args.K / 2) + k / 2] >> (4 * (k & 1)) & 15u;
-                const uint32_t s = args.sf[int64_t(n) * (args.K / 32) + k / 32];
-                const float scale = __uint_as_float(s == 255u ? 0x7FC00000u : max(s << 23, 0x00400000u));
+                const uint32_t s = args.sf[int64_t(n) * (args.K / kGroup) + k / kGroup];
+                float scale = __uint_as_float(s == 255u ? 0x7FC00000u : max(s << 23, 0x00400000u));
+                if constexpr (kNv) {
+                    __half_raw h;
+                    h.x = static_cast<unsigned short>((s & 0x7Fu) << 7);
+                    scale = (s & 0x7Fu) == 0x7Fu ? __uint_as_float(0x7FC00000u) : __half2float(__half(h)) * 256.0f;
+                }
                 v += __bfloat162float(args.x[int64_t(tok0 + t) * args.K + k]) * (c & 8u ? -kMag[c & 7u] : kMag[c & 7u]) * scale;
             }
 #pragma unroll
@@ -467,10 +626,11 @@ __global__ void __launch_bounds__(kMxThreads, 1)
 
 }  // namespace
 
-bool fp4_matvec_mx(const void *x, const void *w, const void *sf, void *y, int T, int N, int K, cudaStream_t stream,
+bool fp4_matvec_tc(bool nv, const void *x, const void *w, const void *sf, void *y, int T, int N, int K, cudaStream_t stream,
                    cudaError_t *status) {
-    if (K % kMxBlockK || !aligned(w, 32)) return false;
-    const void *kernel = reinterpret_cast<const void *>(fp4_matvec_mx_kernel);
+    if (K % kMxBlockK || !aligned(w, 32) || (nv && T > kMxNvTokens)) return false;
+    const auto run = nv ? fp4_matvec_tc_kernel<true> : fp4_matvec_tc_kernel<false>;
+    const void *kernel = reinterpret_cast<const void *>(run);
     *status = set_max_dynamic_smem(kernel, kMxSmem);
     if (*status != cudaSuccess) return true;
     const int all_blocks = K / kMxBlockK;
@@ -483,7 +643,7 @@ bool fp4_matvec_mx(const void *x, const void *w, const void *sf, void *y, int T,
     a.N = N;
     a.K = K;
     a.tokens = T < kMxTokens ? T : kMxTokens;
-    a.cols = (kMxPieces * a.tokens + 7) / 8 * 8;
+    a.cols = nv ? 2 * kMxPieces * a.tokens : (kMxPieces * a.tokens + 7) / 8 * 8;
     // The parts of K that leave a block the least to stream (the rows of a stage count as
     // 72 at least, what its instructions take, and a block of a token as 14), while its
     // tokens and sums leave room.
@@ -494,9 +654,9 @@ bool fp4_matvec_mx(const void *x, const void *w, const void *sf, void *y, int T,
         a.rows = int((N + a.rounds * units - 1) / (a.rounds * units) + 7) / 8 * 8;
         a.blocks = ((all_blocks + 1) / 2 + a.parts - 1) / a.parts * 2;
         if (a.blocks > 1024 || a.rounds > 1024) continue;
-        a.stages = mx_smem_bytes(a, kMxMaxStages) <= kMxSmem ? kMxMaxStages : 4;
-        if (mx_smem_bytes(a, a.stages) > kMxSmem) continue;
-        a.issuers = a.stages == 4 ? 4 : 3;
+        a.stages = mx_smem_bytes(nv, a, kMxMaxStages) <= kMxSmem ? kMxMaxStages : 4;
+        if (mx_smem_bytes(nv, a, a.stages) > kMxSmem) continue;
+        a.issuers = nv ? kMxSets : a.stages == 4 ? 4 : 3;
         const int64_t stream_rows = (int64_t(a.rounds) * (a.rows > 72 ? a.rows : 72) + 14 * a.tokens) * a.blocks;
         if (best.parts == 0 || stream_rows < best_rows) {
             best = a;
@@ -514,7 +674,7 @@ bool fp4_matvec_mx(const void *x, const void *w, const void *sf, void *y, int T,
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(clusters * best.parts), unsigned((T + best.tokens - 1) / best.tokens));
     cfg.blockDim = dim3(kMxThreads);
-    cfg.dynamicSmemBytes = size_t(mx_smem_bytes(best, best.stages));
+    cfg.dynamicSmemBytes = size_t(mx_smem_bytes(nv, best, best.stages));
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -525,7 +685,7 @@ bool fp4_matvec_mx(const void *x, const void *w, const void *sf, void *y, int T,
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    *status = cudaLaunchKernelEx(&cfg, fp4_matvec_mx_kernel, tm, best);
+    *status = cudaLaunchKernelEx(&cfg, run, tm, best);
     return true;
 }
 

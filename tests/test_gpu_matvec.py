@@ -76,28 +76,51 @@ def test_sizes(moe, T, N, K, fmt):
     check(moe, *random_case(T, N, K, fmt, T * 7 + N), fmt)
 
 
-@pytest.mark.parametrize("T,N,K", [
-    (1, 1, 128), (3, 200, 384), (5, 129, 640),              # fewer than four stages of 128, and five
-    (1, 4099, 7168), (8, 4099, 7168), (12, 1000, 2048),     # tiles of any number of rows, two passes
-    (2, 40000, 256), (8, 20011, 512), (6, 19000, 1152),     # several tiles to a block
-    (1, 260, 26624), (4, 65, 53248),                        # as many stages as a part may have
+@pytest.mark.parametrize("fmt,T,N,K", [
+    ("mx", 1, 1, 128), ("mx", 3, 200, 384), ("mx", 5, 129, 640),       # fewer than four stages, and an odd half
+    ("mx", 1, 4099, 7168), ("mx", 8, 4099, 7168), ("mx", 12, 1000, 2048),  # tiles of any number of rows, two passes
+    ("mx", 2, 40000, 256), ("mx", 8, 20011, 512), ("mx", 6, 19000, 1152),  # several tiles to a block
+    ("mx", 1, 260, 26624), ("mx", 4, 65, 53248),                        # long parts
+    ("nvfp4", 1, 1, 128), ("nvfp4", 2, 200, 384), ("nvfp4", 1, 129, 640), ("nvfp4", 2, 1000, 256),
+    ("nvfp4", 1, 4099, 7168), ("nvfp4", 2, 4099, 7168), ("nvfp4", 1, 40000, 256), ("nvfp4", 2, 19000, 1152),
+    ("nvfp4", 1, 260, 26624), ("nvfp4", 2, 65, 26752),
 ])
-def test_whole_stages(moe, T, N, K):
-    """MX with K a multiple of 128, which the block-scaled tensor cores take."""
-    check(moe, *random_case(T, N, K, "mx", T * 11 + N), "mx")
+def test_whole_stages(moe, fmt, T, N, K):
+    """K a multiple of 128, which the block-scaled tensor cores take (NVFP4: for
+    two tokens at most)."""
+    check(moe, *random_case(T, N, K, fmt, T * 11 + N), fmt)
 
 
-def test_infinities_by_definition(moe):
+@pytest.mark.parametrize("fmt,T,bad", [("mx", 7, (1, 3, 5)), ("nvfp4", 2, (1,)), ("nvfp4", 1, (0,))])
+def test_infinities_by_definition(moe, fmt, T, bad):
     """Tokens that are not finite give what the sum of their products gives."""
-    x, w, sf = random_case(7, 300, 1280, "mx", 51)
-    x[1, 7], x[3, 1279], x[5, 0], x[5, 900] = float("inf"), float("-inf"), float("inf"), float("inf")
-    y = moe.fp4_matvec(x, w, sf)
-    exact = x.to(F64) @ decode(w, sf, "mx").T
-    for t in (1, 3, 5):
+    x, w, sf = random_case(T, 300, 1280, fmt, 51)
+    if fmt == "nvfp4":
+        sf[sf == 127] = 0
+    for t, at in zip(bad, ([7], [1279], [0, 900])):
+        x[t, at] = float("-inf") if t == 3 else float("inf")
+    y = moe.fp4_matvec(x, w, sf, fmt=fmt)
+    exact = x.to(F64) @ decode(w, sf, fmt).T
+    for t in bad:
         assert torch.equal(torch.isnan(y[t]), torch.isnan(exact[t]))
         inf = torch.isinf(exact[t])
         assert bool(inf.any()) and torch.equal(y[t][inf].to(F64), exact[t][inf])
-    check(moe, x[[0, 2, 4, 6]].contiguous(), w, sf, "mx")
+    fine = [t for t in range(T) if t not in bad]
+    if fine:
+        check(moe, x[fine].contiguous(), w, sf, fmt)
+
+
+def test_nvfp4_scales_at_their_ends(moe):
+    x, w, sf = random_case(2, 40, 512, "nvfp4", 71)
+    sf[0], sf[1], sf[2] = 0, 126, 1
+    sf[3] |= 128                   # bit 7 is not read
+    sf[3][(sf[3] & 127) == 127] = 0
+    for T in (1, 2):
+        check(moe, x[:T].contiguous(), w, sf, "nvfp4")
+    sf[5, 31] = 127
+    for T in (1, 2):
+        y = moe.fp4_matvec(x[:T].contiguous(), w, sf, fmt="nvfp4")
+        assert bool(torch.isnan(y[:, 5]).all()) and bool(torch.isfinite(y[:, :5]).all() and torch.isfinite(y[:, 6:]).all())
 
 
 def test_weights_at_16_bytes(moe):
