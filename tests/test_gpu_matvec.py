@@ -77,12 +77,12 @@ def test_sizes(moe, T, N, K, fmt):
 
 
 @pytest.mark.parametrize("fmt,T,N,K", [
-    ("mx", 1, 1, 128), ("mx", 3, 200, 384), ("mx", 5, 129, 640),       # fewer than four stages, and an odd half
-    ("mx", 1, 4099, 7168), ("mx", 8, 4099, 7168), ("mx", 12, 1000, 2048),  # tiles of any number of rows, two passes
-    ("mx", 2, 40000, 256), ("mx", 8, 20011, 512), ("mx", 6, 19000, 1152),  # several tiles to a block
-    ("mx", 1, 260, 26624), ("mx", 4, 65, 53248),                        # long parts
-    ("nvfp4", 1, 1, 128), ("nvfp4", 2, 200, 384), ("nvfp4", 1, 129, 640), ("nvfp4", 2, 1000, 256),
-    ("nvfp4", 1, 4099, 7168), ("nvfp4", 2, 4099, 7168), ("nvfp4", 1, 40000, 256), ("nvfp4", 2, 19000, 1152),
+    ("mx", 8, 1, 128), ("mx", 8, 200, 384), ("mx", 8, 129, 640),           # fewer than four stages, and an odd half
+    ("mx", 1, 4099, 7168), ("mx", 8, 4099, 7168), ("mx", 12, 3100, 4096),  # tiles of any number of rows, two passes
+    ("mx", 1, 50000, 256), ("mx", 8, 20011, 512), ("mx", 6, 19000, 1152),  # several tiles to a block
+    ("mx", 1, 260, 26624), ("mx", 4, 65, 53248), ("mx", 2, 7, 8320),       # long parts
+    ("nvfp4", 1, 1, 8192), ("nvfp4", 2, 200, 8320), ("nvfp4", 1, 129, 16512), ("nvfp4", 2, 30000, 256),
+    ("nvfp4", 1, 4099, 7168), ("nvfp4", 2, 4099, 7168), ("nvfp4", 1, 40000, 384), ("nvfp4", 2, 19000, 1152),
     ("nvfp4", 1, 260, 26624), ("nvfp4", 2, 65, 26752),
 ])
 def test_whole_stages(moe, fmt, T, N, K):
@@ -94,10 +94,10 @@ def test_whole_stages(moe, fmt, T, N, K):
 @pytest.mark.parametrize("fmt,T,bad", [("mx", 7, (1, 3, 5)), ("nvfp4", 2, (1,)), ("nvfp4", 1, (0,))])
 def test_infinities_by_definition(moe, fmt, T, bad):
     """Tokens that are not finite give what the sum of their products gives."""
-    x, w, sf = random_case(T, 300, 1280, fmt, 51)
+    x, w, sf = random_case(T, 300, 8320, fmt, 51)
     if fmt == "nvfp4":
         sf[sf == 127] = 0
-    for t, at in zip(bad, ([7], [1279], [0, 900])):
+    for t, at in zip(bad, ([7], [8319], [0, 900])):
         x[t, at] = float("-inf") if t == 3 else float("inf")
     y = moe.fp4_matvec(x, w, sf, fmt=fmt)
     exact = x.to(F64) @ decode(w, sf, fmt).T
@@ -111,20 +111,20 @@ def test_infinities_by_definition(moe, fmt, T, bad):
 
 
 def test_nvfp4_scales_at_their_ends(moe):
-    x, w, sf = random_case(2, 40, 512, "nvfp4", 71)
+    x, w, sf = random_case(2, 40, 8192, "nvfp4", 71)
     sf[0], sf[1], sf[2] = 0, 126, 1
     sf[3] |= 128                   # bit 7 is not read
     sf[3][(sf[3] & 127) == 127] = 0
     for T in (1, 2):
         check(moe, x[:T].contiguous(), w, sf, "nvfp4")
-    sf[5, 31] = 127
+    sf[5, 511] = 127
     for T in (1, 2):
         y = moe.fp4_matvec(x[:T].contiguous(), w, sf, fmt="nvfp4")
         assert bool(torch.isnan(y[:, 5]).all()) and bool(torch.isfinite(y[:, :5]).all() and torch.isfinite(y[:, 6:]).all())
 
 
 def test_weights_at_16_bytes(moe):
-    x, w, sf = random_case(2, 130, 512, "mx", 61)
+    x, w, sf = random_case(2, 130, 8192, "mx", 61)
     room = torch.empty(w.numel() + 64, dtype=torch.uint8, device="cuda")
     at = (16 - room.data_ptr()) % 32
     moved = room[at:at + w.numel()].view(w.shape)
