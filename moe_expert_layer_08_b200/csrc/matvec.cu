@@ -40,7 +40,7 @@ constexpr int kMvChunk = 256;                      // K elements of a stage: 128
 constexpr int kMvCodeBytes = kMvRows * 128;        // of a stage
 constexpr int kMvScaleBytes = kMvRows * 32;        // of a stage: two aligned pieces around a row's scales
 constexpr int kMvSumBytes = 2 * kMvWarps * kMvRows * kMvTokens * 4;
-constexpr int kMvMaxBytes = (kMvWarps + 1) * kMvTokens * 4 + 96;  // the tokens' largest magnitudes and factors
+constexpr int kMvMaxBytes = kMvTokens * 4 + 96;  // the tokens' largest magnitudes
 constexpr int kMvMaxSmem = 232448;
 constexpr int kMvMaxK = 57344;
 // a stage's scales as fp32, per warp
@@ -144,12 +144,14 @@ __global__ void __launch_bounds__(kMvWarps * 32, 1)
     uint8_t *xs = after + kMvSumBytes + kMvWarps * kStages * 8 + kMvMaxBytes;
     const int64_t sf_ld = args.K / kGroup, sf_end = args.N * sf_ld;
 
-    if (threadIdx.x == 0) abort_flag = 0;  // (read by waits, which come after the block has met)
+    uint32_t *tops = reinterpret_cast<uint32_t *>(after + kMvSumBytes + kMvWarps * kStages * 8);  // [token]
+    if (threadIdx.x == 0) abort_flag = 0;
+    if (threadIdx.x < kMvTokens) tops[threadIdx.x] = 0;
     if (lane == 0) {
         for (int s = 0; s < kStages; ++s) mbar_init(&bars[s], 1);  // this warp's own
         fence_mbar_init();
     }
-    __syncwarp();
+    __syncthreads();
     pdl_wait();
     pdl_trigger();
     const uint64_t pol = policy_evict_first();
@@ -185,31 +187,37 @@ __global__ void __launch_bounds__(kMvWarps * 32, 1)
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) load_next();
 
-    // The tokens in fp16, a sixteenth of K per warp, in the order of the decoded
-    // weights: NVFP4 elements 0 and 2, 1 and 3, 4 and 6, 5 and 7, MX elements 0 and
-    // 4, 1 and 5, 2 and 6, 3 and 7.  First every token's largest magnitude, then
-    // the values.  A lane's first two 16-byte pieces of every token (all of it for K
-    // up to 8192) are asked for at once and stay in registers.
-    float *amaxs = reinterpret_cast<float *>(after + kMvSumBytes + kMvWarps * kStages * 8);  // [warp][token]
-    float *unscales = amaxs + kMvWarps * kMvTokens;                                            // [token]
-    {
-        const int x_lo = warp * units / kMvWarps * 32, x_hi = (warp + 1) * units / kMvWarps * 32;
-        const int k0 = x_lo + lane * 8, k1 = k0 + 256, rest = k0 + 512;
-        const auto piece = [&](int j, int k) {
-            return __ldg(reinterpret_cast<const uint4 *>(args.x + int64_t(tok0 + j) * args.K + k));
-        };
-        const auto largest = [](uint4 u, float amax) {
-            const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+    // The tokens in fp16, in the order of the decoded weights: NVFP4 elements 0 and 2, 1
+    // and 3, 4 and 6, 5 and 7, MX elements 0 and 4, 1 and 5, 2 and 6, 3 and 7.  First
+    // every token's largest finite magnitude, then the values; a warp has every so many
+    // 256 elements of one token.  (Little code: a block runs through it once, and
+    // fetching eight tokens' copies of it took 0.6 us each.)
+    const int x_tok = warp % ntok, x_step = (kMvWarps - x_tok + ntok - 1) / ntok * 256;
+    const __nv_bfloat16 *x = args.x + int64_t(tok0 + x_tok) * args.K;
+    uint32_t top = 0;
+#pragma unroll 4
+    for (int k = warp / ntok * 256 + lane * 8; k < args.K; k += x_step) {
+        const uint4 raw = __ldg(reinterpret_cast<const uint4 *>(x + k));
+        const uint32_t v[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float a = __uint_as_float((v[i] << 16) & 0x7FFFFFFFu), b = __uint_as_float(v[i] & 0x7FFF0000u);
-                if (a <= 3.4e38f) amax = fmaxf(amax, a);
-                if (b <= 3.4e38f) amax = fmaxf(amax, b);
-            }
-            return amax;
-        };
-        const auto put = [&](int j, int k, uint4 u, float mul) {
-            const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t a = v[i] & 0x7FFFu, b = v[i] >> 16 & 0x7FFFu;
+            if (a < 0x7F80u) top = max(top, a);
+            if (b < 0x7F80u) top = max(top, b);
+        }
+    }
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if (lane == 0) atomicMax(&tops[x_tok], top);
+    __syncthreads();
+    // 2^shift brings the largest magnitude into [2^14, 2^15); both factors are normal numbers
+    const auto shift_of = [&](int j) { return min(max(14 - (int(tops[j] >> 7) - 127), -113), 126); };
+    {
+        const float mul = tops[x_tok] ? __uint_as_float(uint32_t(127 + shift_of(x_tok)) << 23) : 1.0f;
+        uint8_t *to = xs + x_tok * args.x_stride;
+#pragma unroll 2
+        for (int k = warp / ntok * 256 + lane * 8; k < args.K; k += x_step) {
+            const uint4 raw = __ldg(reinterpret_cast<const uint4 *>(x + k));
+            const uint32_t v[4] = {raw.x, raw.y, raw.z, raw.w};
             uint32_t h[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -218,44 +226,16 @@ __global__ void __launch_bounds__(kMvWarps * 32, 1)
                 const __half2 p = __floats2half2_rn(value(lo) * mul, value(hi) * mul);
                 h[i] = *reinterpret_cast<const uint32_t *>(&p);
             }
-            *reinterpret_cast<uint4 *>(xs + j * args.x_stride + k * 2) = make_uint4(h[0], h[1], h[2], h[3]);
-        };
-        uint4 raw[kMvTokens][2];
-#pragma unroll
-        for (int j = 0; j < kMvTokens; ++j) {
-            raw[j][0] = raw[j][1] = make_uint4(0, 0, 0, 0);
-            if (j < ntok && k0 < x_hi) raw[j][0] = piece(j, k0);
-            if (j < ntok && k1 < x_hi) raw[j][1] = piece(j, k1);
-        }
-#pragma unroll
-        for (int j = 0; j < kMvTokens; ++j) {
-            if (j >= ntok) break;
-            float amax = largest(raw[j][1], largest(raw[j][0], 0.0f));
-            for (int k = rest; k < x_hi; k += 256) amax = largest(piece(j, k), amax);
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
-            if (lane == 0) amaxs[warp * kMvTokens + j] = amax;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < kMvTokens; ++j) {
-            if (j >= ntok) break;
-            float amax = amaxs[(lane & 15) * kMvTokens + j];
-#pragma unroll
-            for (int d = 8; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
-            // 2^shift brings amax into [2^14, 2^15); both factors are normal numbers
-            const int shift = min(max(14 - (int(__float_as_uint(amax) >> 23) - 127), -113), 126);
-            const float mul = amax > 0.0f ? __uint_as_float(uint32_t(127 + shift) << 23) : 1.0f;
-            if (warp == 0 && lane == 0) unscales[j] = amax > 0.0f ? __uint_as_float(uint32_t(127 - shift) << 23) : 1.0f;
-            if (k0 < x_hi) put(j, k0, raw[j][0], mul);
-            if (k1 < x_hi) put(j, k1, raw[j][1], mul);
-            for (int k = rest; k < x_hi; k += 256) put(j, k, piece(j, k), mul);
+            *reinterpret_cast<uint4 *>(to + k * 2) = make_uint4(h[0], h[1], h[2], h[3]);
         }
     }
     __syncthreads();
     float unscale[2];  // of tokens 2t and 2t + 1, the columns of this lane's sums
-    unscale[0] = 2 * t < ntok ? unscales[2 * t] : 0.0f;
-    unscale[1] = 2 * t + 1 < ntok ? unscales[2 * t + 1] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int j = 2 * t + i;
+        unscale[i] = j < ntok && tops[j] ? __uint_as_float(uint32_t(127 - shift_of(j)) << 23) : 1.0f;
+    }
 
     const uint8_t *xrow = xs + min(g, ntok - 1) * args.x_stride + (kNv ? t * 8 : t * 16);  // token g
     int slot = 0, buf = 0;
