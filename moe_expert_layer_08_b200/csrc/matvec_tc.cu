@@ -629,13 +629,16 @@ __global__ void __launch_bounds__(kMxThreads, 1)
 bool fp4_matvec_tc(bool nv, const void *x, const void *w, const void *sf, void *y, int T, int N, int K, cudaStream_t stream,
                    cudaError_t *status) {
     if (K % kMxBlockK || !aligned(w, 32) || (nv && T > kMxNvTokens)) return false;
-    // A launch of this kernel takes 5.5 us at least, one of the other 2.5 and 0.5 a token,
-    // but longer for its weights and for a long K (us, this / the other): 512 x 512, T = 1
-    // 5.5 / 3.0, T = 8 5.8 / 7.3; 4096 x 2048 5.8 / 4.5; 16384 x 1024 6.9 / 7.8; 2048 x
-    // 16384 10.6 / 11.5; T = 16 in two passes: 1000 x 512 11.4 / 7.6, 4096 x 4096 16.7 /
-    // 20.3; NVFP4: 4096 x 2048 6.4 / 5.0, T = 2 16384 x 512 6.5 / 8.9.
-    const int64_t worth = (nv ? 9000000 : 12000000) - (T <= kMxTokens ? 1750000 * int64_t(T - 1) : 0);
-    if (int64_t(N) * K < worth && !(K >= 8192 && T <= kMxTokens)) return false;
+    // A launch of this kernel takes 5.5 us at least, one of the other 2.7, but longer for
+    // its weights, a long K and many short rows; and this one reads the weights again for
+    // a second eight tokens.  us, this / the other, MX: 2048 x 2048, T = 1 6.3 / 3.2, T = 8
+    // 6.4 / 4.2; 4096 x 4096 7.0 / 6.6, 8.4 / 8.8; 16384 x 512 6.4 / 7.8; 1000 x 7168 6.5 /
+    // 6.7, 8.0 / 10.4; T = 16: 14336 x 2048 23.6 / 19.7, 14336 x 7168 39.9 / 55.8; NVFP4:
+    // 4096 x 4096 7.6 / 7.6.
+    const int64_t weights = int64_t(N) * K;
+    if (T > kMxTokens ? weights < 44000000
+                      : weights < 16000000 && K < 7168 && (N < 16384 || weights < 8000000))
+        return false;
     const auto run = nv ? fp4_matvec_tc_kernel<true> : fp4_matvec_tc_kernel<false>;
     const void *kernel = reinterpret_cast<const void *>(run);
     *status = set_max_dynamic_smem(kernel, kMxSmem);

@@ -174,10 +174,10 @@ torch.manual_seed(0)
 B = torch.bfloat16
 x, w = torch.randn((16, 2048), dtype=B, device="cuda"), torch.randn((2, 520, 2048), dtype=B, device="cuda")
 off = torch.tensor([0, 7, 16], dtype=torch.int32, device="cuda")
-codes = torch.randint(0, 256, (520, 1024), dtype=torch.uint8, device="cuda")
-scales = torch.randint(120, 130, (520, 64), dtype=torch.uint8, device="cuda")
+codes = torch.randint(0, 256, (9000, 1024), dtype=torch.uint8, device="cuda")
+scales = torch.randint(120, 130, (9000, 64), dtype=torch.uint8, device="cuda")
 gain = torch.randn(2048, dtype=B, device="cuda")
-y, z = torch.empty((16, 520), dtype=B, device="cuda"), torch.empty((8, 520), dtype=B, device="cuda")
+y, z = torch.empty((16, 520), dtype=B, device="cuda"), torch.empty((8, 9000), dtype=B, device="cuda")
 ws = torch.empty(moe.grouped_workspace_bytes(), dtype=torch.uint8, device="cuda")
 torch.cuda.synchronize()
 graph = torch.cuda.CUDAGraph()

@@ -77,12 +77,12 @@ def test_sizes(moe, T, N, K, fmt):
 
 
 @pytest.mark.parametrize("fmt,T,N,K", [
-    ("mx", 8, 1, 128), ("mx", 8, 200, 384), ("mx", 8, 129, 640),           # fewer than four stages, and an odd half
-    ("mx", 1, 4099, 7168), ("mx", 8, 4099, 7168), ("mx", 12, 3100, 4096),  # tiles of any number of rows, two passes
-    ("mx", 1, 50000, 256), ("mx", 8, 20011, 512), ("mx", 6, 19000, 1152),  # several tiles to a block
-    ("mx", 1, 260, 26624), ("mx", 4, 65, 53248), ("mx", 2, 7, 8320),       # long parts
-    ("nvfp4", 1, 1, 8192), ("nvfp4", 2, 200, 8320), ("nvfp4", 1, 129, 16512), ("nvfp4", 2, 30000, 256),
-    ("nvfp4", 1, 4099, 7168), ("nvfp4", 2, 4099, 7168), ("nvfp4", 1, 40000, 384), ("nvfp4", 2, 19000, 1152),
+    ("mx", 8, 65600, 128), ("mx", 8, 30000, 384), ("mx", 7, 20011, 640),    # fewer than four stages, and an odd half
+    ("mx", 1, 4099, 7168), ("mx", 8, 4099, 7168), ("mx", 12, 11000, 4096),  # tiles of any number of rows, two passes
+    ("mx", 1, 50000, 256), ("mx", 8, 20011, 512), ("mx", 6, 19000, 1152),   # several tiles to a block
+    ("mx", 1, 260, 26624), ("mx", 4, 65, 53248), ("mx", 2, 1, 7296),        # long parts
+    ("nvfp4", 1, 1, 8192), ("nvfp4", 2, 200, 8320), ("nvfp4", 1, 129, 16512), ("nvfp4", 2, 40000, 256),
+    ("nvfp4", 1, 4099, 7168), ("nvfp4", 2, 4099, 7168), ("nvfp4", 1, 65600, 128), ("nvfp4", 2, 19000, 1152),
     ("nvfp4", 1, 260, 26624), ("nvfp4", 2, 65, 26752),
 ])
 def test_whole_stages(moe, fmt, T, N, K):
