@@ -684,7 +684,10 @@ bool fp4_matvec_tc(bool nv, const void *x, const void *w, const void *sf, void *
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(clusters * best.parts), unsigned((T + best.tokens - 1) / best.tokens));
     cfg.blockDim = dim3(kMxThreads);
-    cfg.dynamicSmemBytes = size_t(mx_smem_bytes(nv, best, best.stages));
+    // All of an SM's, whatever is used: a block holds all of its TMEM until its cluster has
+    // met, so blocks of two clusters on two SMs, each with one waiting for the other's
+    // TMEM, would wait for good.
+    cfg.dynamicSmemBytes = size_t(kMxSmem);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -167,6 +167,28 @@ def test_two_streams_at_once(moe):
     del graph
 
 
+def test_small_clusters_of_two_streams(moe):
+    """Launches of a few clusters each, which would fit an SM side by side: no
+    block waits for what another cluster holds."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    cases = []
+    for N in (200, 130):
+        codes = torch.randint(0, 256, (N, 8192), dtype=torch.uint8, device="cuda", generator=g)
+        scales = torch.randint(120, 130, (N, 512), dtype=torch.uint8, device="cuda", generator=g)
+        cases.append((normal(N, 1, 16384), codes, scales))
+    expect = [moe.fp4_matvec(*c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(100):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append((i % 2, moe.fp4_matvec(*cases[i % 2])))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, expect[i]) for i, y in got)
+
+
 FIRST = """
 import torch
 import moe_expert_layer_08_b200 as moe
