@@ -733,13 +733,18 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream_on(stream, device):
-    """The given stream, or the current one of ``device``."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
-    if stream.device != device:
-        raise ValueError(f"stream must be on {device}, got {stream.device}")
-    return stream.cuda_stream
+def _stream_on(device):
+    """The current stream of ``device``."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _call_on(stream, fn, first, *args):
+    """``fn`` with ``stream`` as the current one: outputs and workspaces made there
+    belong to it, so their memory is not used again before its work is done."""
+    if isinstance(first, torch.Tensor) and stream.device != first.device:
+        raise ValueError(f"stream must be on {first.device}, got {stream.device}")
+    with torch.cuda.stream(stream):
+        return fn(first, *args)
 
 
 def grouped_workspace_bytes() -> int:
@@ -761,7 +766,7 @@ def _grouped_workspace(workspace, device):
     return workspace
 
 
-def _grouped_rows(fn, rows, w, offsets, out, workspace, stream, width_in, width_out):
+def _grouped_rows(fn, rows, w, offsets, out, workspace, width_in, width_out):
     E, N, K = w.shape
     R = rows.shape[0]
     dev = rows.device
@@ -777,7 +782,7 @@ def _grouped_rows(fn, rows, w, offsets, out, workspace, stream, width_in, width_
         _need_on(out, torch.bfloat16, "out", shape, dev)
     ws = _grouped_workspace(workspace, dev)
     _check(getattr(load(), fn)(_addr(rows), _addr(w), _addr(offsets), _addr(out), R, E, N, K, int(zero_unused), _addr(ws),
-                               ws.numel(), _stream_on(stream, dev)), fn)
+                               ws.numel(), _stream_on(dev)), fn)
     return out
 
 
@@ -789,18 +794,22 @@ def grouped_matmul(x, w, offsets, out=None, workspace=None, stream=None):
     ``out``.  ``workspace``: u8, grouped_workspace_bytes(); with one of your own
     check_device_error(workspace) reports offsets that decrease or leave [0, R]
     (read as their clamped running maximum)."""
+    if stream is not None:
+        return _call_on(stream, grouped_matmul, x, w, offsets, out, workspace)
     _need(x, torch.bfloat16, "x", 2)
     _need(w, torch.bfloat16, "w", 3)
-    return _grouped_rows("moe_grouped_matmul", x, w, offsets, out, workspace, stream, 0, 0)
+    return _grouped_rows("moe_grouped_matmul", x, w, offsets, out, workspace, 0, 0)
 
 
 def grouped_matmul_grad_input(dy, w, offsets, out=None, workspace=None, stream=None):
     """The gradient of grouped_matmul's rows: dy [R, N] bf16 -> dx [R, K] bf16,
     dx[r] = w[e].T @ dy[r].  Rows of no expert, ``out`` and ``workspace`` as
     there."""
+    if stream is not None:
+        return _call_on(stream, grouped_matmul_grad_input, dy, w, offsets, out, workspace)
     _need(dy, torch.bfloat16, "dy", 2)
     _need(w, torch.bfloat16, "w", 3)
-    return _grouped_rows("moe_grouped_matmul_grad_input", dy, w, offsets, out, workspace, stream, 1, 1)
+    return _grouped_rows("moe_grouped_matmul_grad_input", dy, w, offsets, out, workspace, 1, 1)
 
 
 def grouped_matmul_grad_weight(dy, x, offsets, out=None, workspace=None, stream=None):
@@ -808,6 +817,8 @@ def grouped_matmul_grad_weight(dy, x, offsets, out=None, workspace=None, stream=
     dw [E, N, K] bf16, dw[e] = dy[rows of e].T @ x[rows of e] (zero for an
     expert without rows).  ``out`` is overwritten; ``workspace`` as for
     grouped_matmul."""
+    if stream is not None:
+        return _call_on(stream, grouped_matmul_grad_weight, dy, x, offsets, out, workspace)
     _need(dy, torch.bfloat16, "dy", 2)
     _need(x, torch.bfloat16, "x", 2)
     (R, N), K, dev = dy.shape, x.shape[1], dy.device
@@ -822,7 +833,7 @@ def grouped_matmul_grad_weight(dy, x, offsets, out=None, workspace=None, stream=
         _need_on(out, torch.bfloat16, "out", (E, N, K), dev)
     ws = _grouped_workspace(workspace, dev)
     _check(load().moe_grouped_matmul_grad_weight(_addr(dy), _addr(x), _addr(offsets), _addr(out), R, E, N, K, _addr(ws),
-                                                 ws.numel(), _stream_on(stream, dev)),
+                                                 ws.numel(), _stream_on(dev)),
            "moe_grouped_matmul_grad_weight")
     return out
 
@@ -835,6 +846,8 @@ def fp4_matvec(x, w, w_sf, fmt: str = "mx", out=None, stream=None):
     (w [N, K/2], w_sf) as quantize_fp4 (``fmt`` "mx") or quantize_nvfp4
     ("nvfp4") returns them -> y [T, N] bf16.  The activations stay bf16.  For
     decode: the weights are read once per 8 tokens."""
+    if stream is not None:
+        return _call_on(stream, fp4_matvec, x, w, w_sf, fmt, out)
     _need(x, torch.bfloat16, "x", 2)
     _need(w, torch.uint8, "w", 2)
     if fmt not in _FP4_FORMATS:
@@ -847,7 +860,7 @@ def fp4_matvec(x, w, w_sf, fmt: str = "mx", out=None, stream=None):
         out = x.new_empty((T, N))
     else:
         _need_on(out, torch.bfloat16, "out", (T, N), dev)
-    _check(load().moe_fp4_matvec(_addr(x), _addr(w), _addr(w_sf), _addr(out), T, N, K, code, _stream_on(stream, dev)),
+    _check(load().moe_fp4_matvec(_addr(x), _addr(w), _addr(w_sf), _addr(out), T, N, K, code, _stream_on(dev)),
            "moe_fp4_matvec")
     return out
 
@@ -872,6 +885,8 @@ def norm_before(x, weight, eps: float = 1e-6, bf16: bool = True, fp8: bool = Fal
     a router, unquantised experts); ``fp8``: return the layer's quantised input,
     what quantize_fp8 makes of y, from the same pass; ``rstd``: return the
     reciprocal deviations, which norm_before_backward takes.  -> NormBefore."""
+    if stream is not None:
+        return _call_on(stream, norm_before, x, weight, eps, bf16, fp8, rstd)
     _need(x, torch.bfloat16, "x", 2)
     (T, H), dev = x.shape, x.device
     _need_on(weight, torch.bfloat16, "weight", (H,), dev)
@@ -882,7 +897,7 @@ def norm_before(x, weight, eps: float = 1e-6, bf16: bool = True, fp8: bool = Fal
     sf = x.new_empty((T, H // 32), dtype=torch.uint8) if fp8 else None
     r = x.new_empty(T, dtype=torch.float32) if rstd else None
     _check(load().moe_norm_before(_addr(x), _addr(weight), T, H, eps, _addr(y), _addr(q), _addr(sf), _addr(r),
-                                  _stream_on(stream, dev)), "moe_norm_before")
+                                  _stream_on(dev)), "moe_norm_before")
     return NormBefore(y, q, sf, r)
 
 
@@ -906,6 +921,8 @@ def norm_after(x, residual, weight, eps: float = 1e-6, gate=None, residual_scale
     * residual + gate * (x * rsqrt(mean(x^2) + eps) * weight), all bf16 with one
     rounding.  ``gate``: None, per channel [H], per token [T, 1] or per element
     [T, H].  ``out`` may be ``residual`` itself.  -> NormAfter."""
+    if stream is not None:
+        return _call_on(stream, norm_after, x, residual, weight, eps, gate, residual_scale, out, rstd)
     _need(x, torch.bfloat16, "x", 2)
     (T, H), dev = x.shape, x.device
     _need_on(residual, torch.bfloat16, "residual", (T, H), dev)
@@ -917,7 +934,7 @@ def norm_after(x, residual, weight, eps: float = 1e-6, gate=None, residual_scale
         _need_on(out, torch.bfloat16, "out", (T, H), dev)
     r = x.new_empty(T, dtype=torch.float32) if rstd else None
     _check(load().moe_norm_after(_addr(x), _addr(residual), _addr(weight), _addr(gate), kind, T, H, eps, residual_scale,
-                                 _addr(out), _addr(r), _stream_on(stream, dev)), "moe_norm_after")
+                                 _addr(out), _addr(r), _stream_on(dev)), "moe_norm_after")
     return NormAfter(out, r)
 
 
@@ -942,6 +959,8 @@ def norm_before_backward(dy, x, weight, rstd, dresidual=None, workspace=None, st
     returned: (dx [T, H] bf16, dweight [H] f32).  ``dresidual`` (bf16 [T, H]),
     the gradient that reaches x past the norm, is added to dx.  ``workspace``:
     u8, norm_workspace_bytes(T, H)."""
+    if stream is not None:
+        return _call_on(stream, norm_before_backward, dy, x, weight, rstd, dresidual, workspace)
     _need(dy, torch.bfloat16, "dy", 2)
     (T, H), dev = dy.shape, dy.device
     _need_on(x, torch.bfloat16, "x", (T, H), dev)
@@ -953,7 +972,7 @@ def norm_before_backward(dy, x, weight, rstd, dresidual=None, workspace=None, st
     dx = torch.empty_like(x)
     dweight = x.new_empty(H, dtype=torch.float32)
     _check(load().moe_norm_before_backward(_addr(dy), _addr(x), _addr(weight), _addr(rstd), _addr(dresidual), T, H,
-                                           _addr(dx), _addr(dweight), _addr(ws), ws.numel(), _stream_on(stream, dev)),
+                                           _addr(dx), _addr(dweight), _addr(ws), ws.numel(), _stream_on(dev)),
            "moe_norm_before_backward")
     return dx, dweight
 
@@ -964,6 +983,8 @@ def norm_after_backward(dout, x, weight, rstd, gate=None, residual_scale: float 
     f32, dgate), dgate None without a gate, f32 [H] (per channel), f32 [T, 1]
     (per token) or bf16 [T, H] (per element).  ``workspace`` as for
     norm_before_backward."""
+    if stream is not None:
+        return _call_on(stream, norm_after_backward, dout, x, weight, rstd, gate, residual_scale, workspace)
     _need(dout, torch.bfloat16, "dout", 2)
     (T, H), dev = dout.shape, dout.device
     _need_on(x, torch.bfloat16, "x", (T, H), dev)
@@ -978,5 +999,5 @@ def norm_after_backward(dout, x, weight, rstd, gate=None, residual_scale: float 
         dgate = torch.empty(gate.shape, dtype=torch.bfloat16 if kind == 3 else torch.float32, device=dev)
     _check(load().moe_norm_after_backward(_addr(dout), _addr(x), _addr(weight), _addr(rstd), _addr(gate), kind, T, H,
                                           residual_scale, _addr(dx), _addr(dresidual), _addr(dweight), _addr(dgate),
-                                          _addr(ws), ws.numel(), _stream_on(stream, dev)), "moe_norm_after_backward")
+                                          _addr(ws), ws.numel(), _stream_on(dev)), "moe_norm_after_backward")
     return dx, dresidual, dweight, dgate

@@ -189,6 +189,28 @@ def test_small_clusters_of_two_streams(moe):
     assert all(torch.equal(y, expect[i]) for i, y in got)
 
 
+def test_memory_of_calls_on_another_stream(moe):
+    """Outputs and workspaces that a call on a given stream makes for itself are
+    not handed to the current stream while that work is still to come."""
+    x, dy, w = normal(1, 600, 4096), normal(2, 600, 4096), normal(3, 4096)
+    off = torch.tensor([0, 250, 600], dtype=torch.int32, device="cuda")
+    we = normal(4, 2, 264, 4096)
+    rstd = moe.norm_before(x, w, rstd=True).rstd
+    expect = [moe.norm_before_backward(dy, x, w, rstd), (moe.grouped_matmul(x, we, off),), tuple(moe.norm_before(x, w)[:1])]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)
+    got = [moe.norm_before_backward(dy, x, w, rstd, stream=s), (moe.grouped_matmul(x, we, off, stream=s),),
+           tuple(moe.norm_before(x, w, stream=s)[:1])]
+    sizes = (moe.norm_workspace_bytes(600, 4096), moe.grouped_workspace_bytes(), 600 * 4096 * 2, 4096 * 4)
+    mine = [torch.full((n,), 0x5A, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
+    torch.cuda.synchronize()
+    for a, b in zip(expect, got):
+        assert all(torch.equal(u, v) for u, v in zip(a, b))
+    assert all(bool((m == 0x5A).all()) for m in mine)
+
+
 FIRST = """
 import torch
 import moe_expert_layer_08_b200 as moe

@@ -91,6 +91,15 @@ def test_whole_stages(moe, fmt, T, N, K):
     check(moe, *random_case(T, N, K, fmt, T * 11 + N), fmt)
 
 
+@pytest.mark.parametrize("fmt,T,N,K", [
+    ("mx", 17, 6300, 7168), ("mx", 8, 9, 57344), ("nvfp4", 2, 9, 57344),   # three passes; the longest rows
+    ("mx", 3, 18, 57312), ("nvfp4", 3, 18, 57312), ("nvfp4", 8, 20, 28000),  # rows that leave room for few tokens
+    ("nvfp4", 5, 300, 14336),
+])
+def test_largest(moe, fmt, T, N, K):
+    check(moe, *random_case(T, N, K, fmt, T * 3 + N), fmt)
+
+
 @pytest.mark.parametrize("fmt,T,bad", [("mx", 7, (1, 3, 5)), ("nvfp4", 2, (1,)), ("nvfp4", 1, (0,))])
 def test_infinities_by_definition(moe, fmt, T, bad):
     """Tokens that are not finite give what the sum of their products gives."""
