@@ -589,7 +589,7 @@ moe_status_t moe_ipc_close(void *base);
  * moe_check_device_error(workspace) as MOE_ERR_BAD_ROUTING; no memory outside
  * the operands is touched.  R = 0 enqueues nothing (the weight gradient: zeros
  * dw and the error word).  N and K must be multiples of 8 and at most 131072,
- * E at most 1024 (else MOE_ERR_UNSUPPORTED_SHAPE).  One kernel per call.
+ * E at most 1024, R at most 2^31 - 65536 (else MOE_ERR_UNSUPPORTED_SHAPE).  One kernel per call.
  */
 moe_status_t moe_grouped_workspace_bytes(size_t *bytes);
 moe_status_t moe_grouped_matmul(const void *x_bf16, const void *w_bf16, const int32_t *offsets, void *y_bf16, int R,
@@ -609,13 +609,15 @@ moe_status_t moe_grouped_matmul_grad_weight(const void *dy_bf16, const void *x_b
  * with the weights as moe_quantize_fp4 (MOE_FP4_MX: UE8M0 scales, G = 32) or
  * moe_quantize_nvfp4 (MOE_FP4_NVFP4: UE4M3 scales, G = 16) writes them:
  * w_fp4 u8 [N, K/2], w_sf u8 [N, K/G] and x bf16 [T, K], all 16-byte
- * aligned; y bf16 [T, N].  x is not quantised; sums are fp32 (x times
- * a power of two enters them as fp16: an element is exact down to 2^-31 of its
- * token's largest one, and off by at most 2^-40 of it below).  Scale bytes 255
- * (UE8M0) and 0x7F (UE4M3; bit 7 is not read) are NaN.  The weights are read
- * once per 8 tokens (fewer for K above 7168).  K must be a multiple of 32 and at
- * most 57344, T at most 65535, else MOE_ERR_UNSUPPORTED_SHAPE.  T = 0 enqueues
- * nothing.  One kernel per call.  A wait inside the kernel that gave up (2 s)
+ * aligned; y bf16 [T, N].  x is not quantised: an element enters the fp32
+ * sums off by at most 2^-40 of its token's largest one (and exact down to 2^-31
+ * of it).  Scale bytes 255 (UE8M0) and 0x7F (UE4M3; bit 7 is not read) are
+ * NaN.  The weights are read once per 8 tokens (fewer for long K).  K must be a
+ * multiple of 32 and at most 57344, T at most 65535, N at most 2^31 - 65536, else
+ * MOE_ERR_UNSUPPORTED_SHAPE.  T = 0 enqueues nothing.  One kernel per call: on
+ * the block-scaled tensor cores or decoding the weights, by size and type, so
+ * a token's last bits may depend on how many tokens there are.  K a multiple of
+ * 128 with w_fp4 32-byte aligned is the fastest.  A wait inside the kernel that gave up (2 s)
  * leaves NaN in its outputs.
  */
 #define MOE_FP4_MX 0
@@ -656,7 +658,7 @@ moe_status_t moe_fp4_matvec(const void *x_bf16, const void *w_fp4, const void *w
  * (256-byte aligned, moe_norm_workspace_bytes(T, H); no initialisation) for the
  * column sums of their blocks, which a second kernel adds in a fixed order:
  * results do not depend on timing.  H must be a multiple of 8 and at most
- * 16384 (else MOE_ERR_UNSUPPORTED_SHAPE); eps must be positive and finite.
+ * 16384, T at most 2^31 - 65536 (else MOE_ERR_UNSUPPORTED_SHAPE); eps must be positive and finite.
  * T = 0 enqueues nothing (the gradients: zeros dweight and a per-channel
  * dgate).
  */

@@ -845,7 +845,8 @@ def fp4_matvec(x, w, w_sf, fmt: str = "mx", out=None, stream=None):
     """A few token vectors times a weight matrix in 4 bits: x [T, K] bf16, and
     (w [N, K/2], w_sf) as quantize_fp4 (``fmt`` "mx") or quantize_nvfp4
     ("nvfp4") returns them -> y [T, N] bf16.  The activations stay bf16.  For
-    decode: the weights are read once per 8 tokens."""
+    decode: the weights are read once per 8 tokens; K a multiple of 128 is the
+    fastest."""
     if stream is not None:
         return _call_on(stream, fp4_matvec, x, w, w_sf, fmt, out)
     _need(x, torch.bfloat16, "x", 2)

@@ -874,7 +874,7 @@ cudaError_t launch_rows(const CUtensorMap &tm, const CUtensorMap &tn, GroupedArg
 
 moe_status_t check_grouped(int R, int E, int N, int K) {
     if (R < 0 || E <= 0 || N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
-    if (E > kMaxExperts || N % 8 || K % 8 || N > kGroupedMaxWidth || K > kGroupedMaxWidth) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (R > kMaxRows || E > kMaxExperts || N % 8 || K % 8 || N > kGroupedMaxWidth || K > kGroupedMaxWidth) return MOE_ERR_UNSUPPORTED_SHAPE;
     // every expert's items fit an int: strips <= 1024, chunks <= R / 64 + E
     if ((int64_t(R) / 64 + E) * ((int64_t(N > K ? N : K) + kTileRows - 1) / kTileRows) > 2000000000ll ||
         int64_t(E) * ((N + 255) / 256) * ((K + 255) / 256) > 2000000000ll)

@@ -401,7 +401,7 @@ using namespace moe;
 extern "C" moe_status_t moe_fp4_matvec(const void *x_bf16, const void *w_fp4, const void *w_sf, void *y_bf16, int T,
                                        int N, int K, int format, moe_stream_t stream) {
     if (T < 0 || N <= 0 || K <= 0 || (format != MOE_FP4_MX && format != MOE_FP4_NVFP4)) return MOE_ERR_INVALID_ARG;
-    if (K % 32 || K > kMvMaxK || T > 65535) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (K % 32 || K > kMvMaxK || T > 65535 || N > kMaxRows) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (T == 0) return MOE_OK;
     if (!x_bf16 || !w_fp4 || !w_sf || !y_bf16 || !aligned(x_bf16, 16) || !aligned(w_fp4, 16) ||
         !aligned(w_sf, 16) || !aligned(y_bf16, 2))

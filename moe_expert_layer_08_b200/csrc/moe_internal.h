@@ -125,6 +125,7 @@ bool encode_weights4(CUtensorMap *m, const void *base, uint64_t rows, uint64_t r
 bool fp4_matvec_tc(bool nv, const void *x, const void *w, const void *sf, void *y, int T, int N, int K, cudaStream_t stream,
                    cudaError_t *status);
 
+constexpr int kMaxRows = 2147418112;     // of the operators around the layer: 2^31 less what their row loops step past the end
 constexpr int kGroupedMaxWidth = 131072;  // features of a grouped product's operands, at most
 
 // Multiprocessors of the current device (cached per device).

@@ -534,7 +534,7 @@ constexpr int kSmSmem = 228 * 1024;  // shared memory of an SM, 1 KB of it per r
 
 moe_status_t check_norm(int T, int H, float eps) {
     if (T < 0 || H <= 0 || !(eps > 0.0f) || !(eps <= 3.4e38f)) return MOE_ERR_INVALID_ARG;
-    if (H % 8 || H > kNormMaxH) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (H % 8 || H > kNormMaxH || T > kMaxRows) return MOE_ERR_UNSUPPORTED_SHAPE;
     return MOE_OK;
 }
 

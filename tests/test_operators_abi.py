@@ -18,7 +18,7 @@ def test_grouped_products(moelib):
                    dict(y=None), dict(ws=None), dict(x=q2), dict(w=q2), dict(off=q2), dict(y=q2),
                    dict(ws=ctypes.c_void_p(0x10010))):
             assert call(**kw) == INVALID, kw
-        for kw in (dict(N=60), dict(K=36), dict(E=1025), dict(N=131080), dict(K=131080)):
+        for kw in (dict(N=60), dict(K=36), dict(E=1025), dict(N=131080), dict(K=131080), dict(R=2 ** 31 - 1, N=8, K=8)):
             assert call(**kw) == SHAPE, kw
         assert call(n=64) == SMALL
     g = moelib.moe_grouped_matmul_grad_weight
@@ -39,7 +39,7 @@ def test_matvec(moelib):
     for kw in (dict(T=-1), dict(N=0), dict(K=0), dict(fmt=2), dict(fmt=-1), dict(x=None), dict(w=None), dict(sf=None),
                dict(y=None), dict(x=q2), dict(w=q2), dict(sf=q2), dict(y=odd)):
         assert call(**kw) == INVALID, kw
-    for kw in (dict(K=48), dict(K=57376), dict(T=65536)):
+    for kw in (dict(K=48), dict(K=57376), dict(T=65536), dict(N=2 ** 31 - 1)):
         assert call(**kw) == SHAPE, kw
 
 
@@ -54,7 +54,7 @@ def test_norm_before(moelib):
                dict(w=None), dict(y=None, q=None, sf=None), dict(q=None), dict(sf=None), dict(x=q2), dict(w=q2),
                dict(y=q2), dict(q=q2), dict(r=q2)):
         assert call(**kw) == INVALID, kw
-    for kw in (dict(H=60), dict(H=16392), dict(H=40)):
+    for kw in (dict(H=60), dict(H=16392), dict(H=40), dict(T=2 ** 31 - 1)):
         assert call(**kw) == SHAPE, kw
 
 
