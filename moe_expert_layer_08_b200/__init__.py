@@ -755,11 +755,15 @@ def grouped_workspace_bytes() -> int:
 
 
 _GROUPED_WORKSPACE = 2048  # moe_grouped_workspace_bytes
+_unread = {}  # by device: the error word of the calls without a workspace, which nobody reads
 
 
 def _grouped_workspace(workspace, device):
     if workspace is None:
-        return torch.empty(_GROUPED_WORKSPACE, dtype=torch.uint8, device=device)
+        ws = _unread.get(device.index)
+        if ws is None:
+            ws = _unread[device.index] = torch.empty(_GROUPED_WORKSPACE, dtype=torch.uint8, device=device)
+        return ws
     _need(workspace, torch.uint8, "workspace")
     if workspace.device != device:
         raise ValueError(f"workspace must be on {device}, got {workspace.device}")

@@ -6,12 +6,14 @@
 //   weight gradient  dW[e, n, k] = sum_{r of e} dy[r, n] x[r, k]
 // bf16 operands, fp32 sums in TMEM (tcgen05.mma.kind::f16), one rounding to
 // bf16 at the end.  In all three a work item is a strip of the output features
-// (two MMA tiles, the M side) times up to kN columns of the N side: rows of one
+// (one or two MMA tiles, the M side) times up to kN columns of the N side: rows of one
 // expert (product, input gradient; N is the row count rounded up to 16, so a
 // ragged group costs what it has and not a full tile) or 256 columns of k
 // (weight gradient).  Large loads run on pairs of CTAs (tcgen05 cta_group::2):
 // a strip of 512 features, each CTA with 256 of them and half of the N side in
-// its shared memory, 48 KB from L2 per 1024 MMA cycles and SM instead of 64.  Operands come by TMA
+// its shared memory, 48 KB from L2 per 1024 MMA cycles and SM instead of 64.  Few
+// items of a long contraction are shared by clusters instead: a block has a part of
+// it, and some columns of the parts' fp32 sums to add, in part order.  Operands come by TMA
 // straight from the caller's row-major tensors in whichever major order the
 // contraction finds them:
 //                    M side                     N side
