@@ -199,6 +199,19 @@ bool encode_bf16_3d(CUtensorMap *m, const void *base, uint64_t cols, uint64_t ro
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_bf16_chunks(CUtensorMap *m, int rank, const void *base, uint64_t cols, uint64_t rows, uint64_t experts,
+                        int box_rows) {
+    EncodeTiledFn f = encode_fn();
+    if (!f) return false;
+    const cuuint64_t dims[4] = {64, cuuint64_t(rows), cuuint64_t(cols / 64), cuuint64_t(experts)};
+    const cuuint64_t strides[3] = {cuuint64_t(cols * 2), 128, cuuint64_t(rows * cols * 2)};
+    const cuuint32_t box[4] = {64, cuuint32_t(box_rows), 2, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cuuint32_t(rank), const_cast<void *>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool encode_bytes_rows(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, int box_rows) {
     EncodeTiledFn f = encode_fn();
     if (!f) return false;

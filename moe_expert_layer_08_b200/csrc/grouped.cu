@@ -82,6 +82,7 @@ struct GroupedArgs {
     int D;                // output features: N (product, weight gradient's rows) or K (input gradient)
     int C;                // contraction length of the product and input gradient
     int K;                // weight gradient: columns of dW
+    int chunks_m, chunks_n;  // MN-major operands: their maps have 64-column chunks as a dimension, two of them a box
     int zero_unused;      // product, input gradient: write zeros to the rows of no expert
     int stages;           // of the operand ring
     int split;            // parts of the contraction, the CTAs of a cluster (then one item per cluster)
@@ -232,6 +233,14 @@ __device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *m
         "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
         " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_4d_pair(void *dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2,
+                                                 int c3, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "l"(policy)
         : "memory");
 }
 // Arrive on the first CTA's barrier at this CTA's address `bar`.
@@ -440,9 +449,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int tiles_m = two_tiles(it) ? 2 : 1;
                 // the weights are read once, or by an expert's row chunks at about the same
                 // time (64 experts of 32 rows, 1024 x 1024: 29.8 us, 33.4 with all to be kept)
-                const uint64_t pol_m = row_of[it.e + 1] - row_of[it.e] <= kN ? pol_once : pol_n;
+                const uint64_t pol_m = kMode != kGradWeight && row_of[it.e + 1] - row_of[it.e] <= kN ? pol_once : pol_n;
                 const int n_part = part(it), n0 = it.n0 + rank * n_part;
-                const int boxes_n = kNMn ? (n_part + 63) / 64 : (n_part + kRowBox - 1) / kRowBox;
+                // (a load costs this thread about 190 cycles: the rows of large parts come in one)
+                const bool big = !kNMn && n_part > C::kBRows / 2;
+                const int boxes_n = kNMn ? (n_part + 63) / 64 : big ? C::kBRows / kRowBox : (n_part + kRowBox - 1) / kRowBox;
                 const uint32_t bytes = uint32_t(tiles_m * kTileRows * 128 + boxes_n * (kNMn ? 64 : kRowBox) * 128);
                 for (int kb = kb_lo(it); kb < kb_hi(it); ++kb) {
                     if (!mbar_wait_cycles(&empty[stage], phase ^ 1u, abort_flag, err, 31)) {
@@ -471,20 +482,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if constexpr (kMode == kProduct) {
                         for (int t = 0; t < tiles_m; ++t)
                             load_3d(a + t * kTileRows * 128, &tmap_m, k, tile_row(it, t), it.e, pol_m);
+                    } else if (args.chunks_m) {
+                        for (int t = 0; t < tiles_m; ++t) {
+                            uint8_t *to = a + t * kTileRows * 128;
+                            if constexpr (kMode == kGradWeight) {
+                                load_3d(to, &tmap_m, 0, row_of[it.e] + k, tile_row(it, t) / 64, pol_m);
+                            } else if constexpr (kPair) {
+                                tma_load_4d_pair(to, &tmap_m, signal, 0, k, tile_row(it, t) / 64, it.e, pol_m);
+                            } else {
+                                tma_load_4d(to, &tmap_m, bar, 0, k, tile_row(it, t) / 64, it.e, pol_m);
+                            }
+                        }
                     } else {
                         for (int t = 0; t < 2 * tiles_m; ++t) {
                             const int d = tile_row(it, t >> 1) + (t & 1) * 64;
                             if constexpr (kMode == kGradInput)
                                 load_3d(a + t * 64 * 128, &tmap_m, d, k, it.e, pol_m);
                             else
-                                load_2d(a + t * 64 * 128, &tmap_m, d, row_of[it.e] + k, pol_n);
+                                load_2d(a + t * 64 * 128, &tmap_m, d, row_of[it.e] + k, pol_m);
                         }
                     }
-                    for (int t = 0; t < boxes_n; ++t) {
-                        if constexpr (kNMn)
-                            load_2d(b + t * 64 * 128, &tmap_n, n0 + t * 64, row_of[it.e] + k, pol_n);
-                        else
-                            load_2d(b + t * kRowBox * 128, &tmap_n, k, n0 + t * kRowBox, pol_n);
+                    if (big) {
+                        load_2d(b, &tmap_out, k, n0, pol_n);  // (those maps' boxes: kBRows rows)
+                    } else if (kNMn && args.chunks_n) {
+                        load_3d(b, &tmap_n, 0, row_of[it.e] + k, n0 / 64, pol_n);
+                    } else {
+                        for (int t = 0; t < boxes_n; ++t) {
+                            if constexpr (kNMn)
+                                load_2d(b + t * 64 * 128, &tmap_n, n0 + t * 64, row_of[it.e] + k, pol_n);
+                            else
+                                load_2d(b + t * kRowBox * 128, &tmap_n, k, n0 + t * kRowBox, pol_n);
+                        }
                     }
                     filled |= 1u << stage;
                     fill_parity = (fill_parity & ~(1u << stage)) | (phase << stage);
@@ -860,17 +888,21 @@ Choice choose(int R, int E, int D, int contraction) {
 }
 
 template <int kMode>
-cudaError_t launch_rows(const CUtensorMap &tm, const CUtensorMap &tn, GroupedArgs a, cudaStream_t stream) {
+cudaError_t launch_rows(const CUtensorMap &tm, const CUtensorMap &tn, const void *rows, GroupedArgs a, cudaStream_t stream) {
     const cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(grouped_kernel<kMode, 64, 1>), kMaxSmem);
     if (e != cudaSuccess) return e;
     const Choice c = choose<kMode>(a.R, a.E, a.D, a.C);
     a.split = c.split;
+    CUtensorMap tb;  // the rows in boxes as large as a stage's part
+    const int box = c.kn == 64 ? GroupedCfg<kMode, 64, 1>::kBRows
+                    : c.kn == 160 ? GroupedCfg<kMode, 160, 1>::kBRows : GroupedCfg<kMode, 256, 1>::kBRows;
+    if (!encode_bf16_rows(&tb, rows, uint64_t(a.C), uint64_t(a.R), box)) return cudaErrorInvalidValue;
     switch (c.kn + c.tiles) {
-        case 64 + 1: return launch_grouped<kMode, 64, 1>(tm, tn, tm, a, c.items, stream);
-        case 64 + 2: return launch_grouped<kMode, 64, 2>(tm, tn, tm, a, c.items, stream);
-        case 160 + 1: return launch_grouped<kMode, 160, 1>(tm, tn, tm, a, c.items, stream);
-        case 256 + 1: return launch_grouped<kMode, 256, 1>(tm, tn, tm, a, c.items, stream);
-        default: return launch_grouped<kMode, 256, 2>(tm, tn, tm, a, c.items, stream);
+        case 64 + 1: return launch_grouped<kMode, 64, 1>(tm, tn, tb, a, c.items, stream);
+        case 64 + 2: return launch_grouped<kMode, 64, 2>(tm, tn, tb, a, c.items, stream);
+        case 160 + 1: return launch_grouped<kMode, 160, 1>(tm, tn, tb, a, c.items, stream);
+        case 256 + 1: return launch_grouped<kMode, 256, 1>(tm, tn, tb, a, c.items, stream);
+        default: return launch_grouped<kMode, 256, 2>(tm, tn, tb, a, c.items, stream);
     }
 }
 
@@ -908,11 +940,13 @@ moe_status_t run_rows(bool grad, const void *rows, const void *w, const int32_t 
     a.K = K;
     a.zero_unused = zero_unused;
     CUtensorMap tm, tn;
-    if (!encode_bf16_3d(&tm, w, uint64_t(K), uint64_t(N), uint64_t(E), grad ? kBlockK : kTileRows) ||
+    a.chunks_m = grad && K % 64 == 0;
+    if (!(a.chunks_m ? encode_bf16_chunks(&tm, 4, w, uint64_t(K), uint64_t(N), uint64_t(E), kBlockK)
+                     : encode_bf16_3d(&tm, w, uint64_t(K), uint64_t(N), uint64_t(E), grad ? kBlockK : kTileRows)) ||
         !encode_bf16_rows(&tn, rows, uint64_t(a.C), uint64_t(R), kRowBox))
         return MOE_ERR_CUDA;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = grad ? launch_rows<kGradInput>(tm, tn, a, st) : launch_rows<kProduct>(tm, tn, a, st);
+    const cudaError_t e = grad ? launch_rows<kGradInput>(tm, tn, rows, a, st) : launch_rows<kProduct>(tm, tn, rows, a, st);
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -968,8 +1002,12 @@ moe_status_t moe_grouped_matmul_grad_weight(const void *dy_bf16, const void *x_b
     a.D = N;
     a.K = K;
     CUtensorMap tm, tn, to;
-    if (!encode_bf16_rows(&tm, dy_bf16, uint64_t(N), uint64_t(R), kBlockK) ||
-        !encode_bf16_rows(&tn, x_bf16, uint64_t(K), uint64_t(R), kBlockK) ||
+    a.chunks_m = N % 64 == 0;
+    a.chunks_n = K % 256 == 0;  // every item has its 256 columns: a CTA's begin at a chunk
+    if (!(a.chunks_m ? encode_bf16_chunks(&tm, 3, dy_bf16, uint64_t(N), uint64_t(R), 1, kBlockK)
+                     : encode_bf16_rows(&tm, dy_bf16, uint64_t(N), uint64_t(R), kBlockK)) ||
+        !(a.chunks_n ? encode_bf16_chunks(&tn, 3, x_bf16, uint64_t(K), uint64_t(R), 1, kBlockK)
+                     : encode_bf16_rows(&tn, x_bf16, uint64_t(K), uint64_t(R), kBlockK)) ||
         !encode_bf16_3d(&to, dw_bf16, uint64_t(K), uint64_t(N), uint64_t(E), 32, 32))
         return MOE_ERR_CUDA;
     a.split = 1;

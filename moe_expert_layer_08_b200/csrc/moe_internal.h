@@ -111,6 +111,12 @@ bool encode_bf16_rows(CUtensorMap *m, const void *base, uint64_t cols, uint64_t 
 bool encode_bf16_3d(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, uint64_t experts, int box_rows,
                     int box_cols = 64);
 
+// Tensor map of row-major bf16 matrices [experts][rows][cols], cols % 64 == 0, with the
+// 64-column chunks as a dimension: (64, rows, chunks, experts), or of one matrix without
+// the last (rank 3). Boxes of 64 columns (128-byte swizzle) x box_rows rows x two chunks.
+bool encode_bf16_chunks(CUtensorMap *m, int rank, const void *base, uint64_t cols, uint64_t rows, uint64_t experts,
+                        int box_rows);
+
 // Tensor map of a row-major byte matrix [rows][cols], cols % 16 == 0: boxes of
 // 128 columns (128-byte swizzle) x box_rows rows.
 bool encode_bytes_rows(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, int box_rows);

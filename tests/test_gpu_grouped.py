@@ -98,6 +98,16 @@ def test_every_shape_of_a_work_item(moe, sizes, N, K, turned):
     check_all(moe, sizes, *((K, N) if turned else (N, K)), before=3, behind=9, seed=3)
 
 
+@pytest.mark.parametrize("sizes,N,K", [
+    ([70], 192, 320), ([300, 0, 20], 320, 448), ([100, 37, 0, 260], 320, 512), ([65, 1, 64], 64, 256),
+    ([700, 900], 1088, 768), ([129] * 12, 832, 1280),
+])
+def test_widths_of_whole_chunks(moe, sizes, N, K):
+    """Widths that are multiples of 64, odd and even, and of 256: operands come
+    two chunks of 64 columns at a time."""
+    check_all(moe, sizes, N, K, before=2, behind=3, seed=8)
+
+
 def test_decode_load_with_one_hot_expert(moe):
     """A mean load of at most 8 rows (32-row chunks) with an expert of 150."""
     check_all(moe, [0] * 20 + [150] + [1] * 30 + [2, 33, 32], 392, 328, seed=5)
