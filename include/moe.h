@@ -617,8 +617,8 @@ moe_status_t moe_grouped_matmul_grad_weight(const void *dy_bf16, const void *x_b
  * MOE_ERR_UNSUPPORTED_SHAPE.  T = 0 enqueues nothing.  One kernel per call: on
  * the block-scaled tensor cores or decoding the weights, by size and type, so
  * a token's last bits may depend on how many tokens there are.  K a multiple of
- * 128 with w_fp4 32-byte aligned is the fastest.  A wait inside the kernel that gave up (2 s)
- * leaves NaN in its outputs.
+ * 128 with w_fp4 32-byte aligned is the fastest.  y must not overlap the inputs.
+ * A wait inside the kernel that gave up (2 s) leaves NaN in its outputs.
  */
 #define MOE_FP4_MX 0
 #define MOE_FP4_NVFP4 1

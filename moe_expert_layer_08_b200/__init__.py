@@ -899,7 +899,7 @@ def norm_before(x, weight, eps: float = 1e-6, bf16: bool = True, fp8: bool = Fal
         raise ValueError("ask for bf16, fp8 or both")
     y = torch.empty_like(x) if bf16 else None
     q = torch.empty_like(x, dtype=torch.uint8) if fp8 else None
-    sf = x.new_empty((T, H // 32), dtype=torch.uint8) if fp8 else None
+    sf = q.new_empty((T, H // 32)) if fp8 else None
     r = x.new_empty(T, dtype=torch.float32) if rstd else None
     _check(load().moe_norm_before(_addr(x), _addr(weight), T, H, eps, _addr(y), _addr(q), _addr(sf), _addr(r),
                                   _stream_on(dev)), "moe_norm_before")
