@@ -65,11 +65,11 @@ constexpr int kMxSfCols = 4 * kMxStageBlocks;  // of a stage and operand
 constexpr int kMxSfbCol = kMxSfaCol + kMxSfCols * kMxMaxStages;
 static_assert(kMxSfbCol + kMxSfCols * kMxMaxStages <= 512, "TMEM");
 constexpr int kMxMisc = 512;
-// TMEM columns with NVFP4: the sums of a stage's eight MMAs, 16 columns each of which
-// one token uses 8 (the next MMA's lie over the others); scales as above
-constexpr int kNvBufCols = 128, kNvShortBufCols = 80;
-constexpr int kNvSfaCol = 4 * kNvShortBufCols, kNvSfbCol = kNvSfaCol + 4 * kMxSets;
-static_assert(kNvSfaCol >= kMxSets * kNvBufCols && kNvSfbCol + kMxSfCols * kMxMaxStages <= 512, "TMEM");
+// TMEM columns with NVFP4: the sums of a block's four MMAs, 16 columns each (eight a
+// token), two buffers an issuer; scales as above
+constexpr int kNvBufCols = 64;
+constexpr int kNvSfaCol = 2 * kMxSets * kNvBufCols, kNvSfbCol = kNvSfaCol + 4 * kMxSets;
+static_assert(kNvSfbCol + kMxSfCols * kMxMaxStages <= 512, "TMEM");
 
 struct MxArgs {
     const __nv_bfloat16 *x;   // [T, K]
@@ -374,9 +374,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             if (lane == 0) {
                 // -------------------------------------------------------- MMA issuer
                 bool ok = true;
-                // NVFP4: a stage's MMAs each have columns of their own, two buffers of them
-                // for one token, one for two; the weights' scales are for the draining warps
-                const int bufs = args.tokens == 1 ? 2 : 1, each = args.tokens == 1 ? 8 : 16;
+                // NVFP4: a block's MMAs each have columns of their own; the weights' scales are
+                // for the draining warps
                 const uint32_t unit = tmem + uint32_t(kNvSfaCol + 4 * w0);
                 if constexpr (kNv) tc_cp_sf(unit, smem_desc_sf(smem_u32(ones)));
                 const uint32_t mma_n = uint32_t((args.cols + 15) / 16 * 16);
@@ -392,27 +391,28 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                         ok = mbar_wait_cycles(&full[stage], phase, abort_flag, g_matvec_tc_err, 76);
                         if (!ok) break;
                         if constexpr (kNv) {
-                            const int b = used % bufs;
-                            ok = mbar_wait_cycles(&tmem_empty[2 * w0 + b], (uint32_t(used / bufs) & 1u) ^ 1u, abort_flag, g_matvec_tc_err, 78);
-                            if (!ok) break;
-                            tc_fence_after();
-                            const uint32_t d = tmem + uint32_t(bufs == 2 ? (2 * w0 + b) * kNvShortBufCols : w0 * kNvBufCols);
                             const uint32_t colb = tmem + uint32_t(kNvSfbCol + kMxSfCols * stage);
 #pragma unroll
                             for (int h = 0; h < kMxStageBlocks; ++h) {
-                                const int kb = kMxStageBlocks * s + h;
+                                const int kb = kMxStageBlocks * s + h, b = used & 1;
                                 if (kb >= blocks) break;
+                                ok = mbar_wait_cycles(&tmem_empty[2 * w0 + b], (uint32_t(used >> 1) & 1u) ^ 1u, abort_flag,
+                                                      g_matvec_tc_err, 78);
+                                if (!ok) break;
+                                tc_fence_after();
+                                const uint32_t d = tmem + uint32_t((2 * w0 + b) * kNvBufCols);
                                 tc_cp_sf(colb + 4 * h, smem_desc_sf(smem_u32(sfb + kb * args.cols * 16)));
                                 const uint64_t ad = smem_desc_sw128(smem_u32(ring + stage * stage_bytes + h * args.rows * 128));
                                 const uint64_t bd = smem_desc_sw128(smem_u32(toks + kb * args.cols * 128));
 #pragma unroll
                                 for (int ks = 0; ks < 4; ++ks)
-                                    tc_mma_mxf8f6f4(d + uint32_t((4 * h + ks) * each), ad + uint64_t(2 * ks), bd + uint64_t(2 * ks),
+                                    tc_mma_mxf8f6f4(d + uint32_t(16 * ks), ad + uint64_t(2 * ks), bd + uint64_t(2 * ks),
                                                     idesc_mxf8f6f4(16u, uint32_t(ks)), unit, colb + 4 * h, 0u);
+                                tc_commit(&tmem_full[2 * w0 + b]);
+                                ++used;
                             }
+                            if (!ok) break;
                             tc_commit(&empty[stage]);
-                            tc_commit(&tmem_full[2 * w0 + b]);
-                            ++used;
                             stage += issuers;
                             if (stage >= kStages) {
                                 stage -= kStages;
@@ -462,28 +462,24 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             cluster_wait();
             if constexpr (kNv) {
                 // every second stage: the sums of its 16 groups of 16 times the row's scales
-                const int set = (warp - kEpiWarp) >> 2, bufs = args.tokens == 1 ? 2 : 1;
+                const int set = (warp - kEpiWarp) >> 2;
                 int s = set, stage = set, used = 0;
                 uint32_t phase = 0;
                 bool ok = true;
                 for (int tile = first; ok && tile < tiles; tile += step, ++li, s -= pairs) {
                     float acc[kMxNvTokens] = {};
                     bool nan = false;
-                    for (; s < pairs; s += kMxSets, ++used) {
-                        const int b = used % bufs;
-                        ok = mx_warp_wait(&full[stage], phase, abort_flag, 79) &&
-                             mx_warp_wait(&tmem_full[2 * set + b], uint32_t(used / bufs) & 1u, abort_flag, 77);
+                    for (; ok && s < pairs; s += kMxSets) {
+                        ok = mx_warp_wait(&full[stage], phase, abort_flag, 79);
                         if (!ok) break;
-                        tc_fence_after();
                         const uint4 sc = *reinterpret_cast<const uint4 *>(sfa + stage * kScaleBytes + row * 16);
                         const uint32_t scales[4] = {sc.x, sc.y, sc.z, sc.w};
-                        const int groups = min(kMxStageBlocks, blocks - kMxStageBlocks * s) * 8;  // of 16 elements
-                        const uint32_t d = tmem + (uint32_t(q * 32) << 16) +
-                                           uint32_t(bufs == 2 ? (2 * set + b) * kNvShortBufCols : set * kNvBufCols);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&empty[stage]);
                         auto scale = [&](int g) {
                             // 2^-8 times a UE4M3 byte's value: its bits are those of an fp16 number of another bias
                             const uint32_t byte = scales[g >> 2] >> (8 * (g & 3)) & 0x7Fu;
-                            if (g < groups) nan |= byte == 0x7Fu;
+                            nan |= byte == 0x7Fu;
                             __half_raw h;
                             h.x = static_cast<unsigned short>(byte << 7);
                             return __half2float(__half(h));
@@ -491,35 +487,31 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                         auto four = [](const uint32_t *r) {
                             return __uint_as_float(r[0]) + (__uint_as_float(r[1]) + (__uint_as_float(r[2]) + __uint_as_float(r[3])));
                         };
-                        if (bufs == 2) {
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {  // eight groups of four columns
-                                if (8 * h >= groups) break;
+                        for (int h = 0; h < kMxStageBlocks; ++h) {
+                            const int b = used & 1;
+                            if (kMxStageBlocks * s + h >= blocks) break;
+                            ok = mx_warp_wait(&tmem_full[2 * set + b], uint32_t(used >> 1) & 1u, abort_flag, 77);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint32_t d = tmem + (uint32_t(q * 32) << 16) + uint32_t((2 * set + b) * kNvBufCols);
+#pragma unroll
+                            for (int m = 0; m < 2; ++m) {  // two MMAs: the halves of two groups of 32, of each token
                                 uint32_t r[32];
-                                tmem_ld_32x32(d + uint32_t(32 * h), r);
+                                tmem_ld_32x32(d + uint32_t(32 * m), r);
                                 tmem_ld_wait();
 #pragma unroll
-                                for (int g = 0; g < 8; ++g) acc[0] = fmaf(four(r + 4 * g), scale(8 * h + g), acc[0]);
-                            }
-                        } else {
-#pragma unroll
-                            for (int h = 0; h < 4; ++h) {  // two MMAs: of each two tokens' two groups
-                                if (4 * h >= groups) break;
-                                uint32_t r[32];
-                                tmem_ld_32x32(d + uint32_t(32 * h), r);
-                                tmem_ld_wait();
-#pragma unroll
-                                for (int g = 0; g < 4; ++g)
+                                for (int g = 0; g < 4; ++g) {
+                                    const float f = scale(8 * h + 4 * m + g);
 #pragma unroll
                                     for (int t = 0; t < kMxNvTokens; ++t)
-                                        acc[t] = fmaf(four(r + 16 * (g >> 1) + 8 * t + 4 * (g & 1)), scale(4 * h + g), acc[t]);
+                                        if (t < ntok) acc[t] = fmaf(four(r + 16 * (g >> 1) + 8 * t + 4 * (g & 1)), f, acc[t]);
+                                }
                             }
-                        }
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(&tmem_empty[2 * set + b]);
-                            mbar_arrive(&empty[stage]);
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&tmem_empty[2 * set + b]);
+                            ++used;
                         }
                         stage += kMxSets;
                         if (stage >= kStages) {
