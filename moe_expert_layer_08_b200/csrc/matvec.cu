@@ -18,9 +18,9 @@
 // that largest one (it is then off by at most 2^-40 of it, less than a rounding
 // of the fp32 sum).  The group scale multiplies the fp32 sum of its group.  The
 // slices' sums meet in shared memory and are added in slice order.
-// With K a multiple of 128 the block-scaled tensor cores take MX weights, and NVFP4
-// weights for one or two tokens, in a kernel without decoding; this one takes the rest,
-// and tokens too long for that one's shared memory.
+// With K a multiple of 128 the block-scaled tensor cores take larger MX matrices, and
+// NVFP4 ones for up to four tokens, in a kernel without decoding; this one takes the
+// rest, and tokens too long for that one's shared memory.
 // What bounds it is the decoding: about 50 instructions per warp and 512 weights,
 // half of them on the integer pipe, against 11 cycles of an SM's share of HBM.
 #include <cuda_fp16.h>

@@ -1,7 +1,7 @@
 // matvec_tc.cu -- the product of a few bf16 token vectors with a weight matrix held in
 // 4 bits, on the block-scaled tensor cores, for K a multiple of 128:
 //   y[t, n] = sum_k x[t, k] * s[n, k / G] * c[n, k]
-// c E2M1, s UE8M0 with G = 32 (MX) or UE4M3 with G = 16 (NVFP4, one or two tokens);
+// c E2M1, s UE8M0 with G = 32 (MX) or UE4M3 with G = 16 (NVFP4, one to four tokens);
 // bound by the HBM stream of N K (1/2 + 1/G) bytes once nothing is done per weight.
 // (Decoding the codes in registers for mma.sync is bound by the integer pipe, at a
 // third of that stream.)  So tcgen05.mma.kind::mxf8f6f4 takes the codes as they are, as
@@ -21,7 +21,7 @@
 // over all of K.  NVFP4: its scales are no power of two, so the weights' scales are
 // ones there, each MMA (32 elements) has columns of its own, twice the pieces (the
 // halves of the 32 apart, zeros elsewhere), and the draining warps multiply a group's
-// sum by its row's scale: with more than two tokens that is more work than decoding.
+// sum by its row's scale: with more than four tokens that is more work than decoding.
 //
 // A block streams tiles of up to 128 rows and a part of K, 256 elements a stage (with
 // 128 the loading thread, at 340 cycles a stage, held everything up), to its shared
@@ -32,11 +32,12 @@
 // tcgen05 instruction costs its thread about 75 cycles, so two to four threads issue,
 // each every second to fourth stage, with sums of its own.  The rows of a tile are as
 // few as fill every cluster equally often.
-// N = 14336, K = 7168: MX 14.4 us for one token and 20.5 for eight, NVFP4 18.9 for one
-// and 23.7 for two (by mma.sync 26.0, 30.6, 31.7 and 32.4).  While it streams, one MX
-// token's blocks take the HBM's rate; 2.4 us pass before (the tokens) and 2.5 after
-// (sums, the cluster).  Eight tokens' operand leaves room for four stages, which are too
-// few to cover a load's latency; NVFP4 is bound by its two issuers, 900 cycles a stage.
+// N = 14336, K = 7168: MX 14.4 us for one token and 20.5 for eight, NVFP4 18.5, 20.4 and
+// 25.8 for one, two and four (by mma.sync 27, 30, 32, 33 and 34).  While it streams, one
+// MX token's blocks take the HBM's rate; 2.4 us pass before (the tokens) and 2.5 after
+// (sums, the cluster).  The operand of eight MX or four NVFP4 tokens leaves room for four
+// stages, which are too few to cover a load's latency; NVFP4 is bound by its two issuers,
+// 1000 cycles a stage.
 #include "moe_common.cuh"
 #include "moe_internal.h"
 
@@ -49,7 +50,7 @@ constexpr int kMxPieces = 4;         // of a token's element: MMA columns
 constexpr int kMxTokens = 8;         // of a pass
 constexpr int kMxIssuers = 4;        // at most
 constexpr int kMxMaxStages = 6;
-constexpr int kMxNvTokens = 2;       // of a pass with NVFP4 weights
+constexpr int kMxNvTokens = 4;       // of a pass with NVFP4 weights, at most
 constexpr int kMxSets = 2;           // NVFP4: issuers, each with four draining warps of its own
 constexpr int kMxMaxParts = 8;
 constexpr int kMxSmem = 232448;
@@ -65,8 +66,8 @@ constexpr int kMxSfCols = 4 * kMxStageBlocks;  // of a stage and operand
 constexpr int kMxSfbCol = kMxSfaCol + kMxSfCols * kMxMaxStages;
 static_assert(kMxSfbCol + kMxSfCols * kMxMaxStages <= 512, "TMEM");
 constexpr int kMxMisc = 512;
-// TMEM columns with NVFP4: the sums of a block's four MMAs, 16 columns each (eight a
-// token), two buffers an issuer; scales as above
+// TMEM columns with NVFP4: the sums of four MMAs, 16 columns each (eight a token), or of
+// two for three and four tokens, two buffers an issuer; scales as above
 constexpr int kNvBufCols = 64;
 constexpr int kNvSfaCol = 2 * kMxSets * kNvBufCols, kNvSfbCol = kNvSfaCol + 4 * kMxSets;
 static_assert(kNvSfbCol + kMxSfCols * kMxMaxStages <= 512, "TMEM");
@@ -153,12 +154,15 @@ __device__ __forceinline__ void leave(float (&v)[8], uint2 piece, float next) {
     }
 }
 
-template <bool kNv>
+// kNvTokens: 0 with MX weights, else up to how many tokens of NVFP4 ones, 2 or 4.
+template <int kNvTokens>
 __global__ void __launch_bounds__(kMxThreads, 1)
     fp4_matvec_tc_kernel(const __grid_constant__ CUtensorMap tmap_w, const MxArgs args) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int kStages = args.stages;
+    constexpr bool kNv = kNvTokens > 0;
+    constexpr int kUnitMmas = kNvTokens == 4 ? 2 : 4, kMmaCols = kNvBufCols / kUnitMmas;  // of a buffer of sums
     constexpr int kEpiWarp = kNv ? 12 : 16, kSets = kNv ? kMxSets : 1, kTokenCols = kNv ? 2 * kMxPieces : kMxPieces;
     constexpr int kScaleBytes = mx_scale_bytes(kNv), kGroup = kNv ? 16 : 32;
     const int stage_bytes = mx_stage_bytes(args);
@@ -393,21 +397,23 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                         if constexpr (kNv) {
                             const uint32_t colb = tmem + uint32_t(kNvSfbCol + kMxSfCols * stage);
 #pragma unroll
-                            for (int h = 0; h < kMxStageBlocks; ++h) {
-                                const int kb = kMxStageBlocks * s + h, b = used & 1;
+                            for (int m0 = 0; m0 < 4 * kMxStageBlocks; m0 += kUnitMmas) {  // a buffer of the stage's MMAs
+                                const int h = m0 / 4, kb = kMxStageBlocks * s + h, b = used & 1;
                                 if (kb >= blocks) break;
                                 ok = mbar_wait_cycles(&tmem_empty[2 * w0 + b], (uint32_t(used >> 1) & 1u) ^ 1u, abort_flag,
                                                       g_matvec_tc_err, 78);
                                 if (!ok) break;
                                 tc_fence_after();
                                 const uint32_t d = tmem + uint32_t((2 * w0 + b) * kNvBufCols);
-                                tc_cp_sf(colb + 4 * h, smem_desc_sf(smem_u32(sfb + kb * args.cols * 16)));
+                                if (m0 % 4 == 0) tc_cp_sf(colb + 4 * h, smem_desc_sf(smem_u32(sfb + kb * args.cols * 16)));
                                 const uint64_t ad = smem_desc_sw128(smem_u32(ring + stage * stage_bytes + h * args.rows * 128));
                                 const uint64_t bd = smem_desc_sw128(smem_u32(toks + kb * args.cols * 128));
 #pragma unroll
-                                for (int ks = 0; ks < 4; ++ks)
-                                    tc_mma_mxf8f6f4(d + uint32_t(16 * ks), ad + uint64_t(2 * ks), bd + uint64_t(2 * ks),
-                                                    idesc_mxf8f6f4(16u, uint32_t(ks)), unit, colb + 4 * h, 0u);
+                                for (int m = 0; m < kUnitMmas; ++m) {
+                                    const int ks = m0 % 4 + m;
+                                    tc_mma_mxf8f6f4(d + uint32_t(m * kMmaCols), ad + uint64_t(2 * ks), bd + uint64_t(2 * ks),
+                                                    idesc_mxf8f6f4(uint32_t(kMmaCols), uint32_t(ks)), unit, colb + 4 * h, 0u);
+                                }
                                 tc_commit(&tmem_full[2 * w0 + b]);
                                 ++used;
                             }
@@ -467,7 +473,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                 uint32_t phase = 0;
                 bool ok = true;
                 for (int tile = first; ok && tile < tiles; tile += step, ++li, s -= pairs) {
-                    float acc[kMxNvTokens] = {};
+                    float acc[kNvTokens] = {};
                     bool nan = false;
                     for (; ok && s < pairs; s += kMxSets) {
                         ok = mx_warp_wait(&full[stage], phase, abort_flag, 79);
@@ -488,25 +494,28 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                             return __uint_as_float(r[0]) + (__uint_as_float(r[1]) + (__uint_as_float(r[2]) + __uint_as_float(r[3])));
                         };
 #pragma unroll
-                        for (int h = 0; h < kMxStageBlocks; ++h) {
+                        for (int m0 = 0; m0 < 4 * kMxStageBlocks; m0 += kUnitMmas) {
                             const int b = used & 1;
-                            if (kMxStageBlocks * s + h >= blocks) break;
+                            if (kMxStageBlocks * s + m0 / 4 >= blocks) break;
                             ok = mx_warp_wait(&tmem_full[2 * set + b], uint32_t(used >> 1) & 1u, abort_flag, 77);
                             if (!ok) break;
                             tc_fence_after();
                             const uint32_t d = tmem + (uint32_t(q * 32) << 16) + uint32_t((2 * set + b) * kNvBufCols);
 #pragma unroll
-                            for (int m = 0; m < 2; ++m) {  // two MMAs: the halves of two groups of 32, of each token
+                            for (int c = 0; c < kNvBufCols; c += 32) {
                                 uint32_t r[32];
-                                tmem_ld_32x32(d + uint32_t(32 * m), r);
+                                tmem_ld_32x32(d + uint32_t(c), r);
                                 tmem_ld_wait();
+                                // columns of an MMA: a token's first 16 elements' four pieces, its last 16's, the next token's
 #pragma unroll
-                                for (int g = 0; g < 4; ++g) {
-                                    const float f = scale(8 * h + 4 * m + g);
+                                for (int m = 0; m < 32 / kMmaCols; ++m)
 #pragma unroll
-                                    for (int t = 0; t < kMxNvTokens; ++t)
-                                        if (t < ntok) acc[t] = fmaf(four(r + 16 * (g >> 1) + 8 * t + 4 * (g & 1)), f, acc[t]);
-                                }
+                                    for (int half = 0; half < 2; ++half) {
+                                        const float f = scale(2 * (m0 + c / kMmaCols + m) + half);
+#pragma unroll
+                                        for (int t = 0; t < kNvTokens; ++t)
+                                            if (t < ntok) acc[t] = fmaf(four(r + m * kMmaCols + 8 * t + 4 * half), f, acc[t]);
+                                    }
                             }
                             tc_fence_before();
                             __syncwarp();
@@ -522,7 +531,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                     const uint32_t to =
                         smem_u32(sums + ((part * kMxSets + set) * args.rounds + li) * args.tokens * own_rows + row % own_rows);
 #pragma unroll
-                    for (int t = 0; t < kMxNvTokens; ++t)
+                    for (int t = 0; t < kNvTokens; ++t)
                         if (t < ntok)
                             cluster_put(to + uint32_t(t * own_rows * 4), adds, nan ? 0x7FC00000u : __float_as_uint(acc[t] * 256.0f));
                 }
@@ -626,12 +635,12 @@ bool fp4_matvec_tc(bool nv, const void *x, const void *w, const void *sf, void *
     // a second eight tokens.  us, this / the other, MX: 2048 x 2048, T = 1 6.3 / 3.2, T = 8
     // 6.4 / 4.2; 4096 x 4096 7.0 / 6.6, 8.4 / 8.8; 16384 x 512 6.4 / 7.8; 1000 x 7168 6.5 /
     // 6.7, 8.0 / 10.4; T = 16: 14336 x 2048 23.6 / 19.7, 14336 x 7168 39.9 / 55.8; NVFP4:
-    // 4096 x 4096 7.6 / 7.6.
+    // 4096 x 4096, T = 2 7.2 / 8.0, T = 4 10.6 / 8.6; 4096 x 7168, T = 4 12.0 / 13.7.
     const int64_t weights = int64_t(N) * K;
     if (T > kMxTokens ? weights < 44000000
-                      : weights < 16000000 && K < 7168 && (N < 16384 || weights < 8000000))
+                      : weights < (nv && T > 2 ? 24000000 : 16000000) && K < 7168 && (N < 16384 || weights < 8000000))
         return false;
-    const auto run = nv ? fp4_matvec_tc_kernel<true> : fp4_matvec_tc_kernel<false>;
+    const auto run = !nv ? fp4_matvec_tc_kernel<0> : T <= 2 ? fp4_matvec_tc_kernel<2> : fp4_matvec_tc_kernel<4>;
     const void *kernel = reinterpret_cast<const void *>(run);
     *status = set_max_dynamic_smem(kernel, kMxSmem);
     if (*status != cudaSuccess) return true;

@@ -84,10 +84,12 @@ def test_sizes(moe, T, N, K, fmt):
     ("nvfp4", 1, 1, 8192), ("nvfp4", 2, 200, 8320), ("nvfp4", 1, 129, 16512), ("nvfp4", 2, 40000, 256),
     ("nvfp4", 1, 4099, 7168), ("nvfp4", 2, 4099, 7168), ("nvfp4", 1, 65600, 128), ("nvfp4", 2, 19000, 1152),
     ("nvfp4", 1, 260, 26624), ("nvfp4", 2, 65, 26752),
+    ("nvfp4", 3, 4099, 7168), ("nvfp4", 4, 4099, 7168), ("nvfp4", 3, 65600, 128), ("nvfp4", 4, 19000, 1152),
+    ("nvfp4", 3, 50000, 384), ("nvfp4", 4, 65, 26752),
 ])
 def test_whole_stages(moe, fmt, T, N, K):
     """K a multiple of 128, which the block-scaled tensor cores take (NVFP4: for
-    two tokens at most)."""
+    four tokens at most)."""
     check(moe, *random_case(T, N, K, fmt, T * 11 + N), fmt)
 
 
