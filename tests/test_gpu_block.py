@@ -228,13 +228,21 @@ graph = torch.cuda.CUDAGraph()
 with torch.cuda.graph(graph):
     n = moe.norm_before(x, gain).y
     moe.grouped_matmul(n, w, off, out=y, workspace=ws)
+    y2 = moe.grouped_matmul(n, w, off)
     moe.fp4_matvec(n[:8], codes, scales, out=z)
 graph.replay()
 torch.cuda.synchronize()
 n2 = moe.norm_before(x, gain).y
 assert torch.equal(n, n2)
 assert torch.equal(y, moe.grouped_matmul(n2, w, off)) and torch.equal(z, moe.fp4_matvec(n2[:8], codes, scales))
-assert moe.check_device_error(ws) == 0
+assert moe.check_device_error(ws) == 0 and torch.equal(y, y2)
+kept = y.clone()
+del graph, n, y2
+torch.cuda.empty_cache()
+fill = [torch.full((4096,), 0x5A, dtype=torch.uint8, device="cuda") for _ in range(64)]
+assert torch.equal(kept, moe.grouped_matmul(n2, w, off))
+torch.cuda.synchronize()
+assert all(bool((f == 0x5A).all()) for f in fill)
 print("same")
 """
 
