@@ -590,8 +590,15 @@ moe_status_t moe_ipc_close(void *base);
  * the operands is touched.  R = 0 enqueues nothing (the weight gradient: zeros
  * dw and the error word).  N and K must be multiples of 8 and at most 131072,
  * E at most 1024, R at most 2^31 - 65536 (else MOE_ERR_UNSUPPORTED_SHAPE).  One kernel per call.
+ *
+ * moe_grouped_unread_workspace -- for callers that do not read the status: a
+ *   workspace of moe_grouped_workspace_bytes on `device` that belongs to the
+ *   library, is never freed, and that any number of calls may use at once, on
+ *   any streams and in graphs.  Not for moe_check_device_error, which would
+ *   report some call's status.
  */
 moe_status_t moe_grouped_workspace_bytes(size_t *bytes);
+moe_status_t moe_grouped_unread_workspace(int device, void **workspace);
 moe_status_t moe_grouped_matmul(const void *x_bf16, const void *w_bf16, const int32_t *offsets, void *y_bf16, int R,
                                 int E, int N, int K, int zero_unused, void *workspace, size_t ws_bytes,
                                 moe_stream_t stream);

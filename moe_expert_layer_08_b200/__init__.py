@@ -125,6 +125,7 @@ def _declare(lib):
         "moe_ipc_open": (I32, [P, I32, c.POINTER(P)]),
         "moe_ipc_close": (I32, [P]),
         "moe_grouped_workspace_bytes": (I32, [c.POINTER(SZ)]),
+        "moe_grouped_unread_workspace": (I32, [I32, c.POINTER(P)]),
         "moe_grouped_matmul": (I32, [P, P, P, P, I32, I32, I32, I32, I32, P, SZ, P]),
         "moe_grouped_matmul_grad_input": (I32, [P, P, P, P, I32, I32, I32, I32, I32, P, SZ, P]),
         "moe_grouped_matmul_grad_weight": (I32, [P, P, P, P, I32, I32, I32, I32, P, SZ, P]),
@@ -755,19 +756,22 @@ def grouped_workspace_bytes() -> int:
 
 
 _GROUPED_WORKSPACE = 2048  # moe_grouped_workspace_bytes
-_unread = {}  # by device: the error word of the calls without a workspace, which nobody reads
+_unread = {}  # by device: address of the library's workspace for calls whose status nobody reads
 
 
 def _grouped_workspace(workspace, device):
+    """Address and bytes of a grouped product's workspace."""
     if workspace is None:
-        ws = _unread.get(device.index)
-        if ws is None:
-            ws = _unread[device.index] = torch.empty(_GROUPED_WORKSPACE, dtype=torch.uint8, device=device)
-        return ws
+        at = _unread.get(device.index)
+        if at is None:
+            p = ctypes.c_void_p()
+            _check(load().moe_grouped_unread_workspace(device.index, ctypes.byref(p)), "moe_grouped_unread_workspace")
+            at = _unread[device.index] = p.value
+        return at, _GROUPED_WORKSPACE
     _need(workspace, torch.uint8, "workspace")
     if workspace.device != device:
         raise ValueError(f"workspace must be on {device}, got {workspace.device}")
-    return workspace
+    return workspace.data_ptr(), workspace.numel()
 
 
 def _grouped_rows(fn, rows, w, offsets, out, workspace, width_in, width_out):
@@ -784,9 +788,9 @@ def _grouped_rows(fn, rows, w, offsets, out, workspace, width_in, width_out):
         out = rows.new_empty(shape)
     else:
         _need_on(out, torch.bfloat16, "out", shape, dev)
-    ws = _grouped_workspace(workspace, dev)
-    _check(getattr(load(), fn)(_addr(rows), _addr(w), _addr(offsets), _addr(out), R, E, N, K, int(zero_unused), _addr(ws),
-                               ws.numel(), _stream_on(dev)), fn)
+    ws, ws_bytes = _grouped_workspace(workspace, dev)
+    _check(getattr(load(), fn)(_addr(rows), _addr(w), _addr(offsets), _addr(out), R, E, N, K, int(zero_unused), ws, ws_bytes,
+                               _stream_on(dev)), fn)
     return out
 
 
@@ -797,7 +801,8 @@ def grouped_matmul(x, w, offsets, out=None, workspace=None, stream=None):
     Rows of no expert are zero in a new output and left as they were in a given
     ``out``.  ``workspace``: u8, grouped_workspace_bytes(); with one of your own
     check_device_error(workspace) reports offsets that decrease or leave [0, R]
-    (read as their clamped running maximum)."""
+    (read as their clamped running maximum) and a wait that gave up; without one
+    nobody is told."""
     if stream is not None:
         return _call_on(stream, grouped_matmul, x, w, offsets, out, workspace)
     _need(x, torch.bfloat16, "x", 2)
@@ -835,9 +840,9 @@ def grouped_matmul_grad_weight(dy, x, offsets, out=None, workspace=None, stream=
         out = x.new_empty((E, N, K))
     else:
         _need_on(out, torch.bfloat16, "out", (E, N, K), dev)
-    ws = _grouped_workspace(workspace, dev)
-    _check(load().moe_grouped_matmul_grad_weight(_addr(dy), _addr(x), _addr(offsets), _addr(out), R, E, N, K, _addr(ws),
-                                                 ws.numel(), _stream_on(dev)),
+    ws, ws_bytes = _grouped_workspace(workspace, dev)
+    _check(load().moe_grouped_matmul_grad_weight(_addr(dy), _addr(x), _addr(offsets), _addr(out), R, E, N, K, ws,
+                                                 ws_bytes, _stream_on(dev)),
            "moe_grouped_matmul_grad_weight")
     return out
 

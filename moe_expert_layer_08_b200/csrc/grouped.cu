@@ -31,6 +31,11 @@
 namespace moe {
 namespace {
 
+// The workspace of calls whose status nobody reads, on every stream and in every graph
+// of a device: memory of the library's own, since an allocator's block may have an
+// earlier owner whose work on one stream is still to come.
+__device__ __align__(256) uint8_t g_grouped_unread[kHdrBytes];
+
 enum GroupedMode { kProduct = 0, kGradInput = 1, kGradWeight = 2 };
 
 constexpr int kBlockK = 64;    // contraction elements of a pipeline stage (one 128-byte swizzled row)
@@ -960,6 +965,23 @@ extern "C" {
 moe_status_t moe_grouped_workspace_bytes(size_t *bytes) {
     if (!bytes) return MOE_ERR_INVALID_ARG;
     *bytes = kHdrBytes;
+    return MOE_OK;
+}
+
+moe_status_t moe_grouped_unread_workspace(int device, void **workspace) {
+    if (device < 0 || !workspace) return MOE_ERR_INVALID_ARG;
+    int current = -1;
+    if (cudaGetDevice(&current) != cudaSuccess) return MOE_ERR_CUDA;
+    if (current != device && cudaSetDevice(device) != cudaSuccess) {
+        cudaGetLastError();
+        return MOE_ERR_CUDA;
+    }
+    void *p = nullptr;
+    const cudaError_t e = cudaGetSymbolAddress(&p, g_grouped_unread);
+    if (e != cudaSuccess) cudaGetLastError();
+    if (current != device) cudaSetDevice(current);
+    if (e != cudaSuccess || !p) return MOE_ERR_CUDA;
+    *workspace = p;
     return MOE_OK;
 }
 
