@@ -27,6 +27,7 @@
 // the neighbour through).
 #include "moe_common.cuh"
 #include "moe_internal.h"
+#include "row_chunks.h"
 
 namespace moe {
 namespace {
@@ -181,9 +182,8 @@ struct Walker {
             it.e = e;
             const int l = u - item_of[e];
             const int r0 = row_of[e], rows = row_of[e + 1] - r0;
-            // as few chunks as hold the rows, of equal size up to the MMA's 16
-            const int nch = (rows + kN - 1) / kN;
-            const int size = ((rows + nch - 1) / nch + 15) / 16 * 16;
+            const RowChunks chunks = row_chunks(rows, kN);
+            const int nch = chunks.count, size = chunks.size;
             // blocks of kChunkBlock row chunks; inside one, strip by strip over its chunks
             const int b = l / (kChunkBlock * strips);
             const int rem = l - b * kChunkBlock * strips;
@@ -191,7 +191,7 @@ struct Walker {
             const int c = b * kChunkBlock + rem % width;
             it.d0 = (rem / width) * kItemStrip;
             it.n0 = r0 + c * size;
-            it.cols = max(min(size, rows - c * size), 0);
+            it.cols = min(size, rows - c * size);
             it.kblocks = kb_const;
             it.tail = kBlockK;
         }

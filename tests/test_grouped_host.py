@@ -1,7 +1,13 @@
 """CPU checks of what the grouped products do on the host."""
 import ctypes
+import os
+import shutil
+import subprocess
 
+import pytest
 import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 INVALID = 1
 
@@ -38,3 +44,44 @@ def test_unread_workspace_refusals(moelib):
     assert moelib.moe_grouped_unread_workspace(-1, ctypes.byref(p)) == INVALID
     assert moelib.moe_grouped_unread_workspace(0, None) == INVALID
     assert p.value is None
+
+
+CHUNKS = r"""
+#include <cstdio>
+#include "row_chunks.h"
+
+int main() {
+    const int top = 2147483647 - 65535;  // rows of a call, at most
+    const int widths[] = {64, 160, 256};
+    for (int most : widths) {
+        const int ends[] = {1, most, 1000 * most, top};
+        for (int end : ends)
+            for (int i = -70000; i <= 70000; ++i) {
+                const long long want = (long long)end + i;
+                if (want < 1 || want > top) continue;
+                const int rows = int(want);
+                const moe::RowChunks c = moe::row_chunks(rows, most);
+                const long long count = c.count, size = c.size;
+                if (count != (want + most - 1) / most || size % 16 || size < 16 || size > most ||
+                    (count - 1) * size >= want || count * size < want || (size - 16) * count >= want) {
+                    std::printf("%d rows of %d: %d of %d\n", rows, most, c.count, c.size);
+                    return 1;
+                }
+            }
+    }
+    return 0;
+}
+"""
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+def test_row_chunks_at_every_size(tmp_path):
+    """Rows are cut into as few chunks as hold them, none empty, up to the largest
+    number of rows that a call accepts (undefined overflows end the program)."""
+    src, exe = tmp_path / "chunks.cpp", tmp_path / "chunks"
+    src.write_text(CHUNKS)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-fsanitize=undefined", "-fno-sanitize-recover", "-Wall", "-Werror",
+                    "-I", os.path.join(ROOT, "moe_expert_layer_08_b200", "csrc"), str(src), "-o", str(exe)],
+                   check=True, capture_output=True, text=True)
+    done = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    assert done.returncode == 0, done.stdout + done.stderr
