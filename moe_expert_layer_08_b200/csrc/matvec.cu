@@ -115,6 +115,30 @@ __device__ __forceinline__ void add_group(float (&acc)[4], const float (&d)[4], 
     acc[3] = fmaf(d[3], s1, acc[3]);
 }
 
+// A result of an MX matrix by definition, for one that is not finite although its token is
+// small: the token's sums are kept 2^(14 - exponent) times as large as its results, and
+// pass fp32's range before these do.  Only scales of more than 2^110 lead there (a slice's
+// groups are at most 224, a group's sum at most 384 times its scale); without one in the
+// row the result stays.
+__device__ __noinline__ float mx_result(float v, const __nv_bfloat16 *x, const uint8_t *w, const uint8_t *sf, int K) {
+    bool large = false;
+    for (int i = 0; i < K / 32; ++i) large |= sf[i] > 237 && sf[i] < 255;
+    if (!large) return v;
+    v = 0.0f;
+#pragma unroll 1
+    for (int i = 0; i < K / 32; ++i) {
+        float sum = 0.0f;
+#pragma unroll 4
+        for (int k = 32 * i; k < 32 * i + 32; ++k) {
+            const uint32_t c = w[k / 2] >> (4 * (k & 1)) & 15u, m = c & 7u;
+            const float mag = m < 4 ? 0.5f * float(m) : m == 4 ? 2.0f : m == 5 ? 3.0f : m == 6 ? 4.0f : 6.0f;
+            sum = fmaf(__bfloat162float(x[k]), c & 8u ? -mag : mag, sum);
+        }
+        v = fmaf(sum, ue8m0_value(sf[i]), v);
+    }
+    return v;
+}
+
 // Where a wait that gave up leaves its mark (the outputs become NaN).
 __device__ int g_matvec_err[8];
 
@@ -230,11 +254,15 @@ __global__ void __launch_bounds__(kMvWarps * 32, 1)
         }
     }
     __syncthreads();
-    float unscale[2];  // of tokens 2t and 2t + 1, the columns of this lane's sums
+    // What brings the sums of tokens 2t and 2t + 1, this lane's columns, back.  MX: with the
+    // 2^14 of the codes, 2^-112 to 2^127, in one factor (2^14 first would take results of 2^114
+    // out of fp32's range).  NVFP4: 2^22 for codes and scales comes first, for sums that are
+    // below 2^20 whatever the token.
+    float unscale[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int j = 2 * t + i;
-        unscale[i] = j < ntok && tops[j] ? __uint_as_float(uint32_t(127 - shift_of(j)) << 23) : 1.0f;
+        unscale[i] = __uint_as_float(uint32_t(127 + (kNv ? 0 : 14) - (j < ntok && tops[j] ? shift_of(j) : 0)) << 23);
     }
 
     const uint8_t *xrow = xs + min(g, ntok - 1) * args.x_stride + (kNv ? t * 8 : t * 16);  // token g
@@ -354,8 +382,7 @@ __global__ void __launch_bounds__(kMvWarps * 32, 1)
                 phase ^= 1u;
             }
         }
-        // 2^14 for the codes, 2^8 for the UE4M3 scales' exponent bias
-        const float back = !ok ? __uint_as_float(0x7FC00000u) : kNv ? 0x1p22f : 0x1p14f;
+        const float back = !ok ? __uint_as_float(0x7FC00000u) : kNv ? 0x1p22f : 1.0f;
         // rows g and g + 8, tokens 2t and 2t + 1 of this slice
         float *part = sums + (buf * kMvWarps + warp) * kMvRows * kMvTokens;
         part[g * kMvTokens + 2 * t] = acc[0] * back * unscale[0];
@@ -372,6 +399,9 @@ __global__ void __launch_bounds__(kMvWarps * 32, 1)
 #pragma unroll
                 for (int i = 0; i < kMvSlices; ++i)
                     v += sums[(buf * kMvWarps + team * kMvSlices + i) * kMvRows * kMvTokens + r * kMvTokens + j];
+                if (!kNv && !(fabsf(v) <= 3.4028235e38f) && tops[j] < 127u << 7)  // the token is below one
+                    v = mx_result(v, args.x + int64_t(tok0 + j) * args.K, args.w + int64_t(n) * (args.K / 2), args.sf + n * sf_ld,
+                                  args.K);
                 args.y[int64_t(tok0 + j) * args.N + n] = __float2bfloat16_rn(v);
             }
         }
