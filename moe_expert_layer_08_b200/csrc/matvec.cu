@@ -12,11 +12,11 @@
 // own ring (TMA boxes of 16 rows x 128 bytes, the scales by cp.async; no waits on
 // other warps), and multiplies on the tensor cores: mma.m16n8k16 with the weights
 // as the 16-row operand and 8 tokens as the other, so 1 to 8 tokens cost the
-// same.  c is exact in fp16.  The tokens are brought to fp16 too, each token's
-// slice scaled by a power of two that puts its largest finite magnitude in
-// [2^14, 2^15): bf16's 8 bits fit, and an element loses bits only below 2^-31 of
-// that largest one (it is then off by at most 2^-40 of it, less than a rounding
-// of the fp32 sum).  The group scale multiplies the fp32 sum of its group.  The
+// same.  c is exact in fp16.  The tokens are brought to fp16 too, each token
+// scaled by a power of two that puts its largest finite magnitude in [2^15, 2^16):
+// bf16's 8 bits fit (65280 at most), and an element loses bits only below 2^-32 of
+// that largest one (it is then off by half of fp16's smallest step, 2^-25, so by at
+// most 2^-40 of that one, less than a rounding of the fp32 sum).  The group scale multiplies the fp32 sum of its group.  The
 // slices' sums meet in shared memory and are added in slice order.
 // With K a multiple of 128 the block-scaled tensor cores take larger MX matrices, and
 // NVFP4 ones for up to four tokens, in a kernel without decoding; this one takes the
@@ -116,10 +116,10 @@ __device__ __forceinline__ void add_group(float (&acc)[4], const float (&d)[4], 
 }
 
 // A result of an MX matrix by definition, for one that is not finite although its token is
-// small: the token's sums are kept 2^(14 - exponent) times as large as its results, and
-// pass fp32's range before these do.  Only scales of more than 2^110 lead there (a slice's
-// groups are at most 224, a group's sum at most 384 times its scale); without one in the
-// row the result stays.
+// small: with 2^m the power of two of the token's largest element, its sums are kept 2^(1 - m)
+// times as large as its results, and pass fp32's range before these do where m < 1.  Only
+// scales of more than 2^110 lead there (a slice's groups are at most 224, a group's sum at
+// most 768 times its scale); without one in the row the result stays.
 __device__ __noinline__ float mx_result(float v, const __nv_bfloat16 *x, const uint8_t *w, const uint8_t *sf, int K) {
     bool large = false;
     for (int i = 0; i < K / 32; ++i) large |= sf[i] > 237 && sf[i] < 255;
@@ -233,8 +233,8 @@ __global__ void __launch_bounds__(kMvWarps * 32, 1)
     top = __reduce_max_sync(0xFFFFFFFFu, top);
     if (lane == 0) atomicMax(&tops[x_tok], top);
     __syncthreads();
-    // 2^shift brings the largest magnitude into [2^14, 2^15); both factors are normal numbers
-    const auto shift_of = [&](int j) { return min(max(14 - (int(tops[j] >> 7) - 127), -113), 126); };
+    // 2^shift brings the largest magnitude into [2^15, 2^16); it and 2^-shift are normal numbers
+    const auto shift_of = [&](int j) { return min(15 - (int(tops[j] >> 7) - 127), 126); };
     {
         const float mul = tops[x_tok] ? __uint_as_float(uint32_t(127 + shift_of(x_tok)) << 23) : 1.0f;
         uint8_t *to = xs + x_tok * args.x_stride;
@@ -255,9 +255,9 @@ __global__ void __launch_bounds__(kMvWarps * 32, 1)
     }
     __syncthreads();
     // What brings the sums of tokens 2t and 2t + 1, this lane's columns, back.  MX: with the
-    // 2^14 of the codes, 2^-112 to 2^127, in one factor (2^14 first would take results of 2^114
+    // 2^14 of the codes, 2^-112 to 2^126, in one factor (2^14 first would take results of 2^114
     // out of fp32's range).  NVFP4: 2^22 for codes and scales comes first, for sums that are
-    // below 2^20 whatever the token.
+    // below 2^21 whatever the token.
     float unscale[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kMvWarps * 32, 1)
 #pragma unroll
                 for (int i = 0; i < kMvSlices; ++i)
                     v += sums[(buf * kMvWarps + team * kMvSlices + i) * kMvRows * kMvTokens + r * kMvTokens + j];
-                if (!kNv && !(fabsf(v) <= 3.4028235e38f) && tops[j] < 127u << 7)  // the token is below one
+                if (!kNv && !(fabsf(v) <= 3.4028235e38f) && tops[j] < 128u << 7)  // the token is below two
                     v = mx_result(v, args.x + int64_t(tok0 + j) * args.K, args.w + int64_t(n) * (args.K / 2), args.sf + n * sf_ld,
                                   args.K);
                 args.y[int64_t(tok0 + j) * args.N + n] = __float2bfloat16_rn(v);

@@ -72,3 +72,41 @@ def test_a_small_token_that_is_not_finite_beside_large_scales(moe, K):
     assert bool(torch.isnan(y[1]).all())
     assert bool(torch.isfinite(y[2]).all())
     check(moe, x[2:].contiguous(), w, sf, "mx")
+
+
+def wide_tokens(T, K, seed):
+    """Tokens of every kind, T of them: elements over 60 powers of two, zeros, a
+    small one, a large one, one large element, every other zero, the smallest bf16
+    numbers, one element of 2^100."""
+    g = generator(seed)
+    x = torch.randn((8, K), dtype=BF16, device="cuda", generator=g)
+    x[0] *= torch.exp2(torch.randint(-40, 20, (K,), device="cuda", generator=g).to(BF16))
+    x[1] = 0
+    x[2] *= 2.0 ** -110
+    x[3] *= 2.0 ** 60
+    x[4, 5] = 3e30
+    x[5, ::2] = 0
+    x[6] = 2.0 ** -133 * torch.randint(-9, 10, (K,), device="cuda", generator=g).to(BF16)
+    x[7, K // 2] = 2.0 ** 100
+    return x[:T] if seed % 2 else x[8 - T:].contiguous()
+
+
+@pytest.mark.parametrize("fmt,T,n", [("mx", 8, 1056), ("mx", 8, 8192), ("mx", 1, 8192), ("nvfp4", 4, 8192), ("nvfp4", 2, 8192),
+                                     ("nvfp4", 8, 1056)])
+@pytest.mark.parametrize("seed", [93, 94])
+def test_every_element_by_itself(moe, fmt, T, n, seed):
+    """The unit matrix gives the tokens back: an element exactly down to 2^-31 of
+    its token's largest one, below that within 2^-40 of it (and one rounding)."""
+    w = torch.zeros((n, n // 2), dtype=torch.uint8, device="cuda")
+    row = torch.arange(n, device="cuda")
+    w[row, row // 2] = torch.where(row % 2 == 1, 2 << 4, 2).to(torch.uint8)     # 1.0
+    one, group = (127, 32) if fmt == "mx" else (0x38, 16)
+    sf = torch.full((n, n // group), one, dtype=torch.uint8, device="cuda")
+    x = wide_tokens(T, n, seed)
+    x[0, 77] = 2.0 ** 127
+    y = moe.fp4_matvec(x, w, sf, fmt=fmt)
+    largest = x.double().abs().amax(1, keepdim=True)
+    high = x.double().abs() >= 2.0 ** -31 * largest
+    assert torch.equal(y[high], x[high])
+    off = 2.0 ** -40 * largest
+    assert bool(((y.double() - x.double()).abs() <= off + 2.0 ** -8 * (x.double().abs() + off))[~high].all())
