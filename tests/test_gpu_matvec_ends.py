@@ -91,6 +91,15 @@ def wide_tokens(T, K, seed):
     return x[:T] if seed % 2 else x[8 - T:].contiguous()
 
 
+@pytest.mark.parametrize("fmt,T,K", [("mx", 8, 8192), ("mx", 8, 8320), ("mx", 3, 8320), ("nvfp4", 4, 8320), ("nvfp4", 2, 8192),
+                                     ("nvfp4", 1, 8320), ("nvfp4", 8, 8320)])
+@pytest.mark.parametrize("seed", [91, 92])
+def test_wide_tokens_times_long_rows(moe, fmt, T, K, seed):
+    """test_tokens_of_a_wide_range at the tensor cores' sizes."""
+    w, sf = random_case(1, 200, K, fmt, seed)[1:]
+    check(moe, wide_tokens(T, K, seed), w, sf, fmt)
+
+
 @pytest.mark.parametrize("fmt,T,n", [("mx", 8, 1056), ("mx", 8, 8192), ("mx", 1, 8192), ("nvfp4", 4, 8192), ("nvfp4", 2, 8192),
                                      ("nvfp4", 8, 1056)])
 @pytest.mark.parametrize("seed", [93, 94])
@@ -110,3 +119,31 @@ def test_every_element_by_itself(moe, fmt, T, n, seed):
     assert torch.equal(y[high], x[high])
     off = 2.0 ** -40 * largest
     assert bool(((y.double() - x.double()).abs() <= off + 2.0 ** -8 * (x.double().abs() + off))[~high].all())
+
+
+def test_mx_scales_at_their_ends_of_long_rows(moe):
+    x, w, sf = random_case(8, 40, 8320, "mx", 95)
+    x *= 2.0 ** 20
+    sf[0], sf[1], sf[2] = 0, 200, 1
+    for T in (1, 5, 8):
+        check(moe, x[:T].contiguous(), w, sf, "mx")
+    sf[7, 259], sf[30, 0] = 255, 255   # NaN
+    fine = [n for n in range(40) if n not in (7, 30)]
+    for T in (1, 8):
+        y = moe.fp4_matvec(x[:T].contiguous(), w, sf)
+        assert bool(torch.isnan(y[:, [7, 30]]).all()) and bool(torch.isfinite(y[:, fine]).all())
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("fmt,T,K", [("mx", 8, 8192), ("mx", 5, 8320), ("nvfp4", 4, 8320), ("nvfp4", 2, 8192)])
+def test_a_token_does_not_reach_another_in_long_rows(moe, bad, fmt, T, K):
+    x, w, sf = random_case(T, 300, K, fmt, 96)
+    w |= 0x22                      # no zero weights
+    if fmt == "nvfp4":
+        sf.clamp_(1, 126)          # and no zero or NaN scales
+    clean = moe.fp4_matvec(x, w, sf, fmt=fmt)
+    x[1, 100] = bad
+    y = moe.fp4_matvec(x, w, sf, fmt=fmt)
+    others = [t for t in range(T) if t != 1]
+    assert torch.equal(y[others], clean[others]) and not bool(torch.isfinite(y[1]).any())
+    assert bool(torch.isnan(y[1]).all() if bad != bad else torch.isinf(y[1]).all())
