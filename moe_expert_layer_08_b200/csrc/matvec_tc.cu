@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         args.y[int64_t(tok0 + t) * args.N + n] = __float2bfloat16_rn(v);
     }
     if (wrong & 0x7FFFFFFFu) {
-        // tokens with infinities or NaN: the definition, a warp per result
+        // tokens with infinities or NaN: the sum of these elements' products, a warp per result
         constexpr float kMag[8] = {0.0f, 0.5f, 1.0f, 1.5f, 2.0f, 3.0f, 4.0f, 6.0f};
         for (int i = warp; i < rounds * per_tile; i += kMxThreads / 32) {
             const int li = i / per_tile, t = (i - li * per_tile) / own_rows, own = i - li * per_tile - t * own_rows;
@@ -616,7 +616,10 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                     h.x = static_cast<unsigned short>((s & 0x7Fu) << 7);
                     scale = (s & 0x7Fu) == 0x7Fu ? __uint_as_float(0x7FC00000u) : __half2float(__half(h)) * 256.0f;
                 }
-                v += __bfloat162float(args.x[int64_t(tok0 + t) * args.K + k]) * (c & 8u ? -kMag[c & 7u] : kMag[c & 7u]) * scale;
+                // (a finite element changes nothing beside them, but 6 times it may pass fp32's range;
+                // its scale may be NaN)
+                const float x = __bfloat162float(args.x[int64_t(tok0 + t) * args.K + k]);
+                v += (fabsf(x) <= 3.4e38f ? 0.0f : x * (c & 8u ? -kMag[c & 7u] : kMag[c & 7u])) * scale;
             }
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);

@@ -147,3 +147,20 @@ def test_a_token_does_not_reach_another_in_long_rows(moe, bad, fmt, T, K):
     others = [t for t in range(T) if t != 1]
     assert torch.equal(y[others], clean[others]) and not bool(torch.isfinite(y[1]).any())
     assert bool(torch.isnan(y[1]).all() if bad != bad else torch.isinf(y[1]).all())
+
+
+@pytest.mark.parametrize("fmt,K", [("mx", 96), ("mx", 8192), ("nvfp4", 96), ("nvfp4", 8192)])
+def test_an_infinity_beside_the_largest_elements(moe, fmt, K):
+    """Finite products, however large before their scale, leave an infinite result
+    as it is."""
+    x = torch.zeros((1, K), dtype=BF16, device="cuda")
+    x[0, 0], x[0, 5], x[0, 40] = float("inf"), 1.5 * 2.0 ** 127, -1.5 * 2.0 ** 127
+    w = torch.full((8, K // 2), 0x22, dtype=torch.uint8, device="cuda")
+    w[:4, 2] = 0xF2                # element 5 is -6
+    w[2:6, 20] = 0x27              # element 40 is 6
+    small = 100 if fmt == "mx" else 1
+    sf = torch.full((8, K // (32 if fmt == "mx" else 16)), small, dtype=torch.uint8, device="cuda")
+    w[1, 0] = w[3, 0] = 0x2A       # element 0 is -1
+    y = moe.fp4_matvec(x, w, sf, fmt=fmt)
+    exact = x.double() @ decode(w, sf, fmt).T
+    assert bool(torch.isinf(exact).all()) and torch.equal(y.double(), exact)
