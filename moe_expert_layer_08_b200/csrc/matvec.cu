@@ -120,11 +120,12 @@ __device__ __forceinline__ void add_group(float (&acc)[4], const float (&d)[4], 
 // times as large as its results, and pass fp32's range before these do where m < 1.  Only
 // scales of more than 2^110 lead there (a slice's groups are at most 224, a group's sum at
 // most 768 times its scale); without one in the row the result stays.
-__device__ __noinline__ float mx_result(float v, const __nv_bfloat16 *x, const uint8_t *w, const uint8_t *sf, int K) {
+__device__ __noinline__ void mx_result(__nv_bfloat16 *y, const __nv_bfloat16 *x, const uint8_t *w, const uint8_t *sf, int K) {
     bool large = false;
+#pragma unroll 1
     for (int i = 0; i < K / 32; ++i) large |= sf[i] > 237 && sf[i] < 255;
-    if (!large) return v;
-    v = 0.0f;
+    if (!large) return;
+    float v = 0.0f;
 #pragma unroll 1
     for (int i = 0; i < K / 32; ++i) {
         float sum = 0.0f;
@@ -136,7 +137,7 @@ __device__ __noinline__ float mx_result(float v, const __nv_bfloat16 *x, const u
         }
         v = fmaf(sum, ue8m0_value(sf[i]), v);
     }
-    return v;
+    *y = __float2bfloat16_rn(v);
 }
 
 // Where a wait that gave up leaves its mark (the outputs become NaN).
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(kMvWarps * 32, 1)
     const uint8_t *xrow = xs + min(g, ntok - 1) * args.x_stride + (kNv ? t * 8 : t * 16);  // token g
     int slot = 0, buf = 0;
     uint32_t phase = 0;
-    bool ok = true;
+    bool ok = true, again = false;  // again: a result of this thread's is not finite
     const int swz = g * 16;  // 16-byte pieces of a row of codes: piece ^ row % 8
     for (int tile = first; tile < tiles; tile += step, buf ^= 1) {
         float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -399,11 +400,21 @@ __global__ void __launch_bounds__(kMvWarps * 32, 1)
 #pragma unroll
                 for (int i = 0; i < kMvSlices; ++i)
                     v += sums[(buf * kMvWarps + team * kMvSlices + i) * kMvRows * kMvTokens + r * kMvTokens + j];
-                if (!kNv && !(fabsf(v) <= 3.4028235e38f) && tops[j] < 128u << 7)  // the token is below two
-                    v = mx_result(v, args.x + int64_t(tok0 + j) * args.K, args.w + int64_t(n) * (args.K / 2), args.sf + n * sf_ld,
-                                  args.K);
+                again |= !(fabsf(v) <= 3.4028235e38f);
                 args.y[int64_t(tok0 + j) * args.N + n] = __float2bfloat16_rn(v);
             }
+        }
+    }
+    if (!kNv && again) {
+        // (its own stores, which this thread sees; inside the loop the call cost launches of
+        // 3 us 0.1 us each)
+        const int id = mine * 32 + lane, j = id >> 4;
+        for (int tile = first; tops[j] < 128u << 7 && tile < tiles; tile += step) {  // the token is below two
+            const int n = tile * kMvRows + (id & 15);
+            if (n >= args.N) break;
+            __nv_bfloat16 *at = args.y + int64_t(tok0 + j) * args.N + n;
+            if (!(fabsf(__bfloat162float(*at)) <= 3.4e38f))
+                mx_result(at, args.x + int64_t(tok0 + j) * args.K, args.w + int64_t(n) * (args.K / 2), args.sf + n * sf_ld, args.K);
         }
     }
     if (abort_flag) {
