@@ -425,6 +425,17 @@ __global__ void __launch_bounds__(kMvWarps * 32, 1)
     }
 }
 
+// Bytes of a token in shared memory: those of a quarter-warp's 16-byte reads are 64 bytes
+// apart modulo 128.
+int mv_token_bytes(int K) { return (2 * K + 127) / 128 * 128 + 64; }
+// Tokens that fit beside a number of stages.
+int mv_tokens_beside(bool nv, int K, int stages) { return (kMvMaxSmem - 16 - mv_fixed_bytes(nv, stages)) / mv_token_bytes(K); }
+// Tokens of a pass over the weights.
+int mv_pass_tokens(bool nv, int T, int K) {
+    const int most = mv_tokens_beside(nv, K, 2), tokens = T < kMvTokens ? T : kMvTokens;
+    return tokens < most ? tokens : most;
+}
+
 template <bool kNv, int kStages>
 cudaError_t launch_matvec(const CUtensorMap &tmap_w, const MatvecArgs &a, dim3 grid, cudaStream_t stream) {
     const cudaError_t e =
@@ -435,6 +446,21 @@ cudaError_t launch_matvec(const CUtensorMap &tmap_w, const MatvecArgs &a, dim3 g
 }
 
 }  // namespace
+
+// Fitted to the measurements at the choice between the kernels (off by 9 % in the root mean
+// square): the tokens' preparation and a block's tiles of 16 rows, by their elements and by
+// the stages of a slice (a last one that is no half or whole costs more), as often as the
+// passes fill the device.
+double fp4_matvec_mma_us(bool nv, int T, int N, int K) {
+    const int tokens = mv_pass_tokens(nv, T, K), passes = (T + tokens - 1) / tokens, sms = num_sms();
+    const int64_t row_tiles = (int64_t(N) + kMvRows - 1) / kMvRows, blocks = row_tiles < sms ? row_tiles : sms;
+    const int slice = (K / 32 + kMvSlices - 1) / kMvSlices * 32, chunks = (slice + kMvChunk - 1) / kMvChunk;
+    const double times = double((blocks * passes + sms - 1) / sms), tiles = double((row_tiles + blocks - 1) / blocks);
+    const double k = K / 1000.0, prepare = (nv ? 0.11 : 0.08) * k * T / passes;
+    const double tile = nv ? 0.4 + 0.37 * k + 0.22 * chunks + (slice % 128 ? 0.1 : 0.0)
+                           : 0.28 + 0.21 * k + 0.17 * chunks + (slice % 128 ? 0.18 : 0.0);
+    return 0.5 + times * (0.8 + prepare + tiles * tile + (nv ? 0.12 : 0.24) * k);
+}
 }  // namespace moe
 
 using namespace moe;
@@ -462,12 +488,10 @@ extern "C" moe_status_t moe_fp4_matvec(const void *x_bf16, const void *w_fp4, co
     a.N = N;
     a.K = K;
     a.factors = {{512, 32, 2}, {4096, 256, 16}};
-    // the tokens of a quarter-warp's 16-byte reads are 64 bytes apart modulo 128
-    a.x_stride = (2 * K + 127) / 128 * 128 + 64;
+    a.x_stride = mv_token_bytes(K);
     const bool nv = format == MOE_FP4_NVFP4;
-    const auto fits = [&](int stages) { return (kMvMaxSmem - 16 - mv_fixed_bytes(nv, stages)) / a.x_stride; };
-    a.tokens = T < kMvTokens ? T : kMvTokens;
-    if (a.tokens > fits(2)) a.tokens = fits(2);
+    const auto fits = [&](int stages) { return mv_tokens_beside(nv, K, stages); };
+    a.tokens = mv_pass_tokens(nv, T, K);
     const int tiles = (N + kMvRows - 1) / kMvRows, sms = num_sms();
     const dim3 grid(unsigned(tiles < sms ? tiles : sms), unsigned((T + a.tokens - 1) / a.tokens));
     CUtensorMap tm;

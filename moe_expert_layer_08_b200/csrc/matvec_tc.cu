@@ -633,16 +633,18 @@ __global__ void __launch_bounds__(kMxThreads, 1)
 bool fp4_matvec_tc(bool nv, const void *x, const void *w, const void *sf, void *y, int T, int N, int K, cudaStream_t stream,
                    cudaError_t *status) {
     if (K % kMxBlockK || !aligned(w, 32) || (nv && T > kMxNvTokens)) return false;
-    // A launch of this kernel takes 5.5 us at least, one of the other 2.7, but longer for
-    // its weights, a long K and many short rows; and this one reads the weights again for
-    // a second eight tokens.  us, this / the other, MX: 2048 x 2048, T = 1 6.3 / 3.2, T = 8
-    // 6.4 / 4.2; 4096 x 4096 7.0 / 6.6, 8.4 / 8.8; 16384 x 512 6.4 / 7.8; 1000 x 7168 6.5 /
-    // 6.7, 8.0 / 10.4; T = 16: 14336 x 2048 23.6 / 19.7, 14336 x 7168 39.9 / 55.8; NVFP4:
-    // 4096 x 4096, T = 2 7.2 / 8.0, T = 4 10.6 / 8.6; 4096 x 7168, T = 4 12.0 / 13.7.
-    const int64_t weights = int64_t(N) * K;
-    if (T > kMxTokens ? weights < 44000000
-                      : weights < (nv && T > 2 ? 24000000 : 16000000) && K < 7168 && (N < 16384 || weights < 8000000))
-        return false;
+    // This kernel or the other, by the two estimates in us.  Of a launch of this one: its
+    // start and end, the rows that its blocks stream (in 128 K elements), the tokens that
+    // they prepare, and the ends of a block's tiles; as often as its passes fill the device.
+    // On 2530 sizes, 1 to 32 tokens, K from 512 to 57344, N from 1 to 65536, the choice took
+    // 0.5 % more time than the faster kernel in the mean and 29 % at most.  us, this / the
+    // other, MX: one row of K = 4096, T = 1 4.5 / 4.3, of 7168 5.2 / 6.4, T = 8 6.5 / 10.2;
+    // 2048 x 2048, T = 1 6.3 / 3.3, T = 8 6.4 / 4.3; 1024 x 7168, T = 1 6.6 / 6.7, T = 8 8.0 /
+    // 10.4; 4096 x 4096, T = 1 6.9 / 6.7, T = 8 8.3 / 8.9; 16384 x 512, T = 1 6.4 / 7.8; T = 16:
+    // 12288 x 2048 21.4 / 18.0, 4096 x 8192 21.3 / 37.4; NVFP4: 2048 x 4096, T = 2 6.8 / 5.6,
+    // 4096 x 7168, T = 2 9.1 / 12.3, T = 4 12.1 / 13.5.
+    const double other = fp4_matvec_mma_us(nv, T, N, K), ends = nv ? (T <= 2 ? 4.5 : 5.5) : 5.0;
+    if (other <= ends - 0.3) return false;
     const auto run = !nv ? fp4_matvec_tc_kernel<0> : T <= 2 ? fp4_matvec_tc_kernel<2> : fp4_matvec_tc_kernel<4>;
     const void *kernel = reinterpret_cast<const void *>(run);
     *status = set_max_dynamic_smem(kernel, kMxSmem);
@@ -661,7 +663,7 @@ bool fp4_matvec_tc(bool nv, const void *x, const void *w, const void *sf, void *
     // The parts of K that leave a block the least to stream (the rows of a stage count as
     // 72 at least, what its instructions take, and a block of a token as 14), while its
     // tokens and sums leave room.
-    int64_t best_rows = 0, clusters = 0;
+    int64_t best_rows = 0, clusters = 0, fit = 0;
     for (a.parts = 1; a.parts <= kMxMaxParts && 2 * a.parts <= all_blocks + 1; a.parts *= 2) {
         const int64_t units = resident_clusters(kernel, a.parts, kMxThreads, kMxSmem);
         a.rounds = int((N + kTileRows * units - 1) / (kTileRows * units));
@@ -677,16 +679,23 @@ bool fp4_matvec_tc(bool nv, const void *x, const void *w, const void *sf, void *
             best_rows = stream_rows;
             const int64_t tiles = (N + a.rows - 1) / a.rows;
             clusters = tiles < units ? tiles : units;
+            fit = units;
         }
     }
     if (best.parts == 0) return false;
+    const int64_t passes = (T + best.tokens - 1) / best.tokens, times = (clusters * passes + fit - 1) / fit;
+    const double rows = double(best.rounds) * (best.rows > 72 ? best.rows : 72) * best.blocks, prepared = double(best.tokens) * best.blocks;
+    const double row_us = !nv ? 0.0012 : T <= 2 ? 0.0021 : 0.0022, token_us = !nv ? 0.018 : T <= 2 ? 0.05 : 0.053;
+    const double end_us = !nv ? 0.47 : T <= 2 ? 0.26 : 0.62;
+    if (double(times) * (ends + row_us * rows + token_us * prepared + end_us * (best.rounds - 1)) - (nv ? 0.0 : 0.3) >= other)
+        return false;
     CUtensorMap tm;
     *status = cudaErrorUnknown;
     if (!encode_weights4(&tm, w, uint64_t(N), uint64_t(K / 2), 1, uint64_t(K / 2), uint64_t(all_blocks), kMxBlockK / 2,
                          best.rows, 1, kMxStageBlocks))
         return true;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(clusters * best.parts), unsigned((T + best.tokens - 1) / best.tokens));
+    cfg.gridDim = dim3(unsigned(clusters * best.parts), unsigned(passes));
     cfg.blockDim = dim3(kMxThreads);
     // All of an SM's, whatever is used: a block holds all of its TMEM until its cluster has
     // met, so blocks of two clusters on two SMs, each with one waiting for the other's

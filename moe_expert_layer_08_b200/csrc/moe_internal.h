@@ -126,6 +126,8 @@ bool encode_bytes_rows(CUtensorMap *m, const void *base, uint64_t cols, uint64_t
 bool encode_weights4(CUtensorMap *m, const void *base, uint64_t rows, uint64_t row_stride, uint64_t a_dim,
                      uint64_t a_stride, uint64_t b_dim, uint64_t b_stride, int box_rows, int box_a, int kblocks);
 
+// What a launch of the 4-bit product by mma.sync takes, in us, by an estimate.
+double fp4_matvec_mma_us(bool nv, int T, int N, int K);
 // The product of a few tokens with an MX or NVFP4 matrix on the block-scaled tensor
 // cores: false if these sizes are not its own; else launched, or *status says why not.
 bool fp4_matvec_tc(bool nv, const void *x, const void *w, const void *sf, void *y, int T, int N, int K, cudaStream_t stream,
