@@ -719,7 +719,9 @@ def ipc_close(base: int) -> None:
 
 # ------------------------------------------------------------ around the expert layer
 # These calls take a few microseconds on the GPU at decode, so the binding keeps
-# its own share small: one test of a tensor where it is as it should be.
+# its own share small: one test of a tensor where it is as it should be.  Autograd
+# does not know their gradients, which are calls of their own: a result whose inputs
+# require gradients refuses a backward pass (a given output is written and no more).
 def _need_on(t, dtype, name, shape, device):
     if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device \
             and t.is_contiguous():
@@ -746,6 +748,27 @@ def _call_on(stream, fn, first, *args):
         raise ValueError(f"stream must be on {first.device}, got {stream.device}")
     with torch.cuda.stream(stream):
         return fn(first, *args)
+
+
+class _NoBackward(torch.autograd.Function):
+    """A result tied to the inputs it was computed from, so that a backward pass which
+    needs it is refused instead of leaving their gradients out in silence."""
+
+    @staticmethod
+    def forward(ctx, result, name, gradients, *inputs):
+        ctx.name, ctx.gradients = name, gradients
+        return result.view_as(result)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError(f"{ctx.name} has no backward pass for autograd: {ctx.gradients}, or call it on detached "
+                           "tensors or under torch.no_grad()")
+
+
+def _tied(result, name, gradients, *inputs):
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs):
+        return _NoBackward.apply(result, name, gradients, *inputs)
+    return result
 
 
 def grouped_workspace_bytes() -> int:
@@ -807,7 +830,10 @@ def grouped_matmul(x, w, offsets, out=None, workspace=None, stream=None):
         return _call_on(stream, grouped_matmul, x, w, offsets, out, workspace)
     _need(x, torch.bfloat16, "x", 2)
     _need(w, torch.bfloat16, "w", 3)
-    return _grouped_rows("moe_grouped_matmul", x, w, offsets, out, workspace, 0, 0)
+    y = _grouped_rows("moe_grouped_matmul", x, w, offsets, out, workspace, 0, 0)
+    if out is None and (x.requires_grad or w.requires_grad):
+        y = _tied(y, "grouped_matmul", "its gradients are grouped_matmul_grad_input and grouped_matmul_grad_weight", x, w)
+    return y
 
 
 def grouped_matmul_grad_input(dy, w, offsets, out=None, workspace=None, stream=None):
@@ -866,13 +892,16 @@ def fp4_matvec(x, w, w_sf, fmt: str = "mx", out=None, stream=None):
     (T, K), N, dev = x.shape, w.shape[0], x.device
     _need_on(w, torch.uint8, "w", (N, K // 2), dev)
     _need_on(w_sf, torch.uint8, "w_sf", (N, K // group), dev)
+    y = out
     if out is None:
-        out = x.new_empty((T, N))
+        y = x.new_empty((T, N))
     else:
         _need_on(out, torch.bfloat16, "out", (T, N), dev)
-    _check(load().moe_fp4_matvec(_addr(x), _addr(w), _addr(w_sf), _addr(out), T, N, K, code, _stream_on(dev)),
+    _check(load().moe_fp4_matvec(_addr(x), _addr(w), _addr(w_sf), _addr(y), T, N, K, code, _stream_on(dev)),
            "moe_fp4_matvec")
-    return out
+    if out is None and x.requires_grad:
+        y = _tied(y, "fp4_matvec", "it is for inference", x)
+    return y
 
 
 class NormBefore(NamedTuple):
@@ -908,6 +937,8 @@ def norm_before(x, weight, eps: float = 1e-6, bf16: bool = True, fp8: bool = Fal
     r = x.new_empty(T, dtype=torch.float32) if rstd else None
     _check(load().moe_norm_before(_addr(x), _addr(weight), T, H, eps, _addr(y), _addr(q), _addr(sf), _addr(r),
                                   _stream_on(dev)), "moe_norm_before")
+    if bf16 and (x.requires_grad or weight.requires_grad):
+        y = _tied(y, "norm_before", "its gradients are norm_before_backward", x, weight)
     return NormBefore(y, q, sf, r)
 
 
@@ -938,14 +969,17 @@ def norm_after(x, residual, weight, eps: float = 1e-6, gate=None, residual_scale
     _need_on(residual, torch.bfloat16, "residual", (T, H), dev)
     _need_on(weight, torch.bfloat16, "weight", (H,), dev)
     kind = _gate(gate, T, H, dev)
+    y = out
     if out is None:
-        out = torch.empty_like(x)
+        y = torch.empty_like(x)
     else:
         _need_on(out, torch.bfloat16, "out", (T, H), dev)
     r = x.new_empty(T, dtype=torch.float32) if rstd else None
     _check(load().moe_norm_after(_addr(x), _addr(residual), _addr(weight), _addr(gate), kind, T, H, eps, residual_scale,
-                                 _addr(out), _addr(r), _stream_on(dev)), "moe_norm_after")
-    return NormAfter(out, r)
+                                 _addr(y), _addr(r), _stream_on(dev)), "moe_norm_after")
+    if out is None and (x.requires_grad or residual.requires_grad or weight.requires_grad or (kind and gate.requires_grad)):
+        y = _tied(y, "norm_after", "its gradients are norm_after_backward", x, residual, weight, gate)
+    return NormAfter(y, r)
 
 
 def norm_workspace_bytes(T_max: int, H: int) -> int:
