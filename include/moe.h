@@ -626,6 +626,9 @@ moe_status_t moe_grouped_matmul_grad_weight(const void *dy_bf16, const void *x_b
  * a token's last bits may depend on how many tokens there are.  K a multiple of
  * 128 with w_fp4 32-byte aligned is the fastest.  y must not overlap the inputs.
  * A wait inside the kernel that gave up (2 s) leaves NaN in its outputs.
+ * A result is infinite where it, or a sum of its products on the way to it, passes
+ * fp32's range (on the block-scaled tensor cores, which add an element in pieces,
+ * from 31/32 of it on).
  */
 #define MOE_FP4_MX 0
 #define MOE_FP4_NVFP4 1
@@ -664,7 +667,7 @@ moe_status_t moe_fp4_matvec(const void *x_bf16, const void *w_fp4, const void *w
  * per-token gate 2-byte); float arrays 4-byte.  The gradients take a workspace
  * (256-byte aligned, moe_norm_workspace_bytes(T, H); no initialisation) for the
  * column sums of their blocks, which a second kernel adds in a fixed order:
- * results do not depend on timing.  H must be a multiple of 8 and at most
+ * results do not depend on timing; a workspace serves one call at a time.  H must be a multiple of 8 and at most
  * 16384, T at most 2^31 - 65536 (else MOE_ERR_UNSUPPORTED_SHAPE); eps must be positive and finite.
  * T = 0 enqueues nothing (the gradients: zeros dweight and a per-channel
  * dgate).
