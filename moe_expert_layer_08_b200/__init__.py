@@ -755,9 +755,10 @@ class _NoBackward(torch.autograd.Function):
     needs it is refused instead of leaving their gradients out in silence."""
 
     @staticmethod
-    def forward(ctx, result, name, gradients, *inputs):
+    def forward(ctx, held, name, gradients, *inputs):
+        # (held: a list, so that the result is no input and stays writable in place)
         ctx.name, ctx.gradients = name, gradients
-        return result.view_as(result)
+        return held[0]
 
     @staticmethod
     def backward(ctx, *grads):
@@ -767,7 +768,7 @@ class _NoBackward(torch.autograd.Function):
 
 def _tied(result, name, gradients, *inputs):
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs):
-        return _NoBackward.apply(result, name, gradients, *inputs)
+        return _NoBackward.apply([result], name, gradients, *inputs)
     return result
 
 

@@ -12,12 +12,16 @@ def test_a_tied_result(moelib):
     with torch.no_grad():
         assert m._tied(y, "f", "its gradient is g", x, w) is y
     tied = m._tied(y, "f", "its gradient is g", x, w)
-    assert torch.equal(tied, y) and tied.data_ptr() == y.data_ptr() and not y.requires_grad
+    assert tied.data_ptr() == y.data_ptr() and tied.requires_grad and not tied._is_view()
     with pytest.raises(RuntimeError, match="f has no backward pass for autograd: its gradient is g"):
         (tied * 2 + x).sum().backward()
+    before = tied.detach().clone()
+    tied += 1                      # written in place, with a graph and without one
     with torch.no_grad():
-        tied.add_(1)
-    assert torch.equal(tied.detach(), y)
+        tied.mul_(2)
+    assert torch.equal(tied.detach(), (before + 1) * 2)
+    with pytest.raises(RuntimeError, match="f has no backward pass"):
+        tied.sum().backward()
 
 
 @pytest.mark.gpu
@@ -46,7 +50,7 @@ def test_a_backward_pass_through_an_operator_is_refused(moelib):
             y = call(*leaves)
             assert torch.equal(y.detach(), want)
             with pytest.raises(RuntimeError, match=name + " has no backward pass"):
-                y.float().sum().backward()
+                y.mul_(2).float().sum().backward()
             with torch.no_grad():
                 assert not call(*leaves).requires_grad
     # a given output stays the caller's, and the gradients' own calls give plain tensors
