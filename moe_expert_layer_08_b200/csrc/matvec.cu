@@ -117,29 +117,46 @@ __device__ __forceinline__ void add_group(float (&acc)[4], const float (&d)[4], 
     acc[3] = fmaf(d[3], s1, acc[3]);
 }
 
-// A result of an MX matrix by definition, for one that is not finite although its token is
-// small: with 2^m the power of two of the token's largest element, its sums are kept 2^(1 - m)
-// times as large as its results, and pass fp32's range before these do where m < 1.  Only
-// scales of more than 2^110 lead there (a slice's groups are at most 224, a group's sum at
-// most 768 times its scale); without one in the row the result stays.
-__device__ __noinline__ void mx_result(__nv_bfloat16 *y, const __nv_bfloat16 *x, const uint8_t *w, const uint8_t *sf, int K) {
-    bool large = false;
-#pragma unroll 1
-    for (int i = 0; i < K / 32; ++i) large |= sf[i] > 237 && sf[i] < 255;
-    if (!large) return;
-    float v = 0.0f;
-#pragma unroll 1
-    for (int i = 0; i < K / 32; ++i) {
-        float sum = 0.0f;
+// Results of an MX matrix by definition, those of a thread (rows row, row + step, ... of a
+// token) that are not finite although the token is small: with 2^m the power of two of the
+// token's largest element, its sums are kept 2^(1 - m) times as large as its results, and
+// pass fp32's range before these do where m < 1.  Only scales of more than 2^110 lead there
+// (a slice's groups are at most 224, a group's sum at most 768 times its scale); a result
+// stays without one in its row, and with a NaN in the token (halves: the token in fp16,
+// read by the lanes of its half of the warp that are here together).
+__device__ __noinline__ void mx_again(__nv_bfloat16 *y, const __nv_bfloat16 *x, const uint8_t *halves, const uint8_t *w,
+                                      const uint8_t *sf, int row, int step, int N, int K) {
+    const uint32_t lane = threadIdx.x & 31, here = __activemask(), half = here & (lane < 16 ? 0xFFFFu : 0xFFFF0000u);
+    bool nan = false;
 #pragma unroll 4
-        for (int k = 32 * i; k < 32 * i + 32; ++k) {
-            const uint32_t c = w[k / 2] >> (4 * (k & 1)) & 15u, m = c & 7u;
-            const float mag = m < 4 ? 0.5f * float(m) : m == 4 ? 2.0f : m == 5 ? 3.0f : m == 6 ? 4.0f : 6.0f;
-            sum = fmaf(__bfloat162float(x[k]), c & 8u ? -mag : mag, sum);
-        }
-        v = fmaf(sum, ue8m0_value(sf[i]), v);
+    for (int k = __popc(half & ((1u << lane) - 1)) * 8; k < K; k += __popc(half) * 8) {
+        const uint4 h = *reinterpret_cast<const uint4 *>(halves + k * 2);
+        const uint32_t m = __vmaxu2(__vmaxu2(h.x & 0x7FFF7FFFu, h.y & 0x7FFF7FFFu), __vmaxu2(h.z & 0x7FFF7FFFu, h.w & 0x7FFF7FFFu));
+        nan |= max(m & 0xFFFFu, m >> 16) > 0x7C00u;
     }
-    *y = __float2bfloat16_rn(v);
+    if (__ballot_sync(here, nan) & half) return;
+#pragma unroll 1
+    for (; row < N; row += step) {
+        if (fabsf(__bfloat162float(y[row])) <= 3.4e38f) continue;
+        const uint8_t *codes = w + int64_t(row) * (K / 2), *scales = sf + int64_t(row) * (K / 32);
+        bool large = false;
+#pragma unroll 16
+        for (int i = 0; i < K / 32; ++i) large |= scales[i] > 237 && scales[i] < 255;
+        if (!large) continue;
+        float v = 0.0f;
+#pragma unroll 1
+        for (int i = 0; i < K / 32; ++i) {
+            float sum = 0.0f;
+#pragma unroll 4
+            for (int k = 32 * i; k < 32 * i + 32; ++k) {
+                const uint32_t c = codes[k / 2] >> (4 * (k & 1)) & 15u, m = c & 7u;
+                const float mag = m < 4 ? 0.5f * float(m) : m == 4 ? 2.0f : m == 5 ? 3.0f : m == 6 ? 4.0f : 6.0f;
+                sum = fmaf(__bfloat162float(x[k]), c & 8u ? -mag : mag, sum);
+            }
+            v = fmaf(sum, ue8m0_value(scales[i]), v);
+        }
+        y[row] = __float2bfloat16_rn(v);
+    }
 }
 
 // Where a wait that gave up leaves its mark (the outputs become NaN).
@@ -408,16 +425,12 @@ __global__ void __launch_bounds__(kMvWarps * 32, 1)
         }
     }
     if (!kNv && again) {
-        // (its own stores, which this thread sees; inside the loop the call cost launches of
-        // 3 us 0.1 us each)
+        // (its own stores, which a thread sees; inside the loop the call cost launches of 3 us
+        // 0.1 us each)
         const int id = mine * 32 + lane, j = id >> 4;
-        for (int tile = first; tops[j] < 128u << 7 && tile < tiles; tile += step) {  // the token is below two
-            const int n = tile * kMvRows + (id & 15);
-            if (n >= args.N) break;
-            __nv_bfloat16 *at = args.y + int64_t(tok0 + j) * args.N + n;
-            if (!(fabsf(__bfloat162float(*at)) <= 3.4e38f))
-                mx_result(at, args.x + int64_t(tok0 + j) * args.K, args.w + int64_t(n) * (args.K / 2), args.sf + n * sf_ld, args.K);
-        }
+        if (tops[j] < 128u << 7)  // the token is below two
+            mx_again(args.y + int64_t(tok0 + j) * args.N, args.x + int64_t(tok0 + j) * args.K, xs + j * args.x_stride, args.w,
+                     args.sf, first * kMvRows + (id & 15), step * kMvRows, args.N, args.K);
     }
     if (abort_flag) {
         // a wait gave up: a quarter of a second, in which the copies under way land

@@ -15,8 +15,8 @@
 // and no barrier is needed to read them.  The arithmetic is on pairs of columns
 // (fp32x2 instructions; with rows of a block in groups and scale bytes straight from
 // the bits they took the quantised norm of 8192 x 7168 from 71.7 to 53.3 us, later
-// steps to 44).  Sums are fp32; the column sums of the blocks are written out and added in block order by a second
-// kernel, so results do not depend on timing.
+// steps to 44).  Sums are fp32; the column sums of the blocks are written out and added
+// in block order by a second kernel, so results do not depend on timing.
 #include "moe_common.cuh"
 #include "moe_internal.h"
 

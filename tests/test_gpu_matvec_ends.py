@@ -59,9 +59,9 @@ def test_nvfp4_tokens_of_every_size(moe, T, N, K):
     check(moe, x, w, sf, "nvfp4")
 
 
-@pytest.mark.parametrize("K", [96, 8192])
-def test_a_small_token_that_is_not_finite_beside_large_scales(moe, K):
-    x, w, sf = random_case(3, 40, K, "mx", 84)
+@pytest.mark.parametrize("N,K", [(40, 96), (9001, 96), (40, 8192)])
+def test_a_small_token_that_is_not_finite_beside_large_scales(moe, N, K):
+    x, w, sf = random_case(3, N, K, "mx", 84)
     x *= 2.0 ** -40
     sf[:] = 250
     w |= 0x22                      # no zero weights
